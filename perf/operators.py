@@ -10,6 +10,7 @@ Two operators, in each direction that a user runs them:
 With ``own`` false, ``run`` computes a case from elementary torch operations in 32 bits,
 rounded once at the end.  With ``own`` true it calls the library.
 """
+import functools
 import math
 
 import torch
@@ -292,8 +293,14 @@ def _run_plain(s):
     return {"q": dq, "k": dk, "q_weight": dqw, "k_weight": dkw}
 
 
-def _run_own(s):
+@functools.cache
+def _library():
     from linear_recurrent_sequence_causal_gb300 import linattn
+    return linattn
+
+
+def _run_own(s):
+    linattn = _library()
     if s["op"] == "decode":
         out = linattn.prism_linattn_decode_step(s["q"], s["k"], s["v"], s["log_decay"], s["state"], scale=s["scale"],
                                                 slots=s["slot"])
