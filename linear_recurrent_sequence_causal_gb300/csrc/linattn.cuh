@@ -1,0 +1,383 @@
+// Causal linear attention with one decay per head: the shared definitions, the fp32 kernel
+// and the single-token step.
+//
+// One pass computes, for a sequence and head with lambda = exp(log_decay_h),
+//   out_t = sp sum_{s <= t} lambda^(t-s) (x_t . y_s) z_s + so lambda^(..) S_in x_t
+// forwards, or with s >= t and lambda^(s-t) backwards.  The prompt is one such pass (x, y,
+// z = q, k, v) and its gradient three of them:
+//   dq = pass(dO, v, k) forwards, on the transposed state;
+//   dv = pass(k, q, dO) and dk = pass(v, dO, q) backwards, on the state's gradient
+//   H_(t-1) = lambda (H_t + scale dO_t q_t^T) and its transpose, H_(T-1) = d_final_state.
+// In chunks of C tokens (n of them there), with i, j counted inside the chunk:
+//   out_i = sp sum_j lambda^|i-j| (x_i . y_j) z_j [j <= i, or j >= i backwards]
+//         + so lambda^e(i) S x_i,                e(i) = i + 1, backwards n - 1 - i
+//   S    <- lambda^n S + su sum_j lambda^f(j) z_j y_j^T,  f(j) = n - 1 - j, backwards j + 1
+// S [d_z, d_y] is what the chunk receives: forwards the state before its first token,
+// backwards the gradient of the state after its last one.
+//
+// Segments.  Where there are few sequences and heads, each sequence is cut into nseg runs of
+// chunks.  A first launch computes each run's own contribution D_r to the state (from zero),
+// and the full pass of run s starts from
+//   S_s = lambda^(done_s) S_0 + sum_{r<s} lambda^(done_s - done_(r+1)) D_r
+// with done_s the tokens processed before run s.  Every D_r is read from the workspace by
+// the CTAs that need it, so no further launch joins them.
+#pragma once
+
+#include "prism_common.cuh"
+
+namespace prism {
+
+struct LinattnJob {
+  const void *x, *y, *z;                  // [B][T][H][D] with the strides below
+  long long xs[2], ys[2], zs[2];          // elements from sequence to sequence, token to token
+  int xi, yi, zi;                         // which of the call's tensor maps they are (bf16 path)
+  void* out;                              // [B][T][H][D] contiguous; null: the state alone
+  const float* s_in;                      // [B][H][D][D] or null (zero)
+  float* s_out;                           // [B][H][D][D] or null
+  float sp, su, so;
+  int rev;                                // backwards
+  int in_t, out_t;                        // the state in memory is [d_y][d_z]
+};
+
+constexpr int kLinattnMaxSeg = 16;
+
+struct LinattnArgs {
+  LinattnJob job[3];
+  int njobs;
+  int B, T, H;
+  const float* log_decay;
+  const int* seq_lens;
+  int nseg, seg_chunks;                   // runs per sequence, chunks per run
+  int phase;                              // 0: full passes; 1: the runs' own states into seg
+  float* seg;                             // [njobs][B][H][nseg - 1][D][D]
+  int* status;                            // bounded waits (bf16 path)
+};
+
+struct LinattnDecodeArgs {
+  int B, H, n_states;
+  const void *q, *k, *v;
+  long long qs, ks, vs;                   // elements from sequence to sequence
+  const float* log_decay;
+  float* state;
+  const int* slots;
+  void* out;
+  float scale;
+};
+
+// lambda^n as 2^(n l2).  log_decay = -inf is clamped so that lambda^0 stays 1 (and not
+// exp(0 * -inf)); NaN stays NaN.
+struct Decay {
+  float ld, l2;
+  __device__ __forceinline__ explicit Decay(float log_decay) {
+    ld = log_decay < -1e30f ? -1e30f : log_decay;
+    l2 = ld * 1.4426950408889634f;
+  }
+  __device__ __forceinline__ float pow(int n) const { return exp2f((float)n * l2); }
+  // lambda^n in two terms, for the factor that the state meets once a chunk: a slow decay's
+  // rounding error would be the same in every chunk and add up over the 1 / (1 - lambda^n)
+  // chunks of its memory (4e-6 of the state at lambda = 1 - 2^-11 with one fp32 term).  Near 1,
+  // lambda^n = 1 + expm1(n ld) leaves 2^-24 of the small term alone.
+  __device__ __forceinline__ float2 step(int n) const {
+    const float x = (float)n * ld;
+    if (x > -0.5f && x < 0.5f) {
+      const float e = expm1f(x), hi = 1.f + e;
+      return make_float2(hi, e - (hi - 1.f));
+    }
+    return make_float2(pow(n), 0.f);
+  }
+};
+__device__ __forceinline__ float decayed(float2 l, float s) { return fmaf(l.x, s, l.y * s); }
+
+// A sequence cut into runs: run s takes the chunks first..last-1 in processing order.
+struct LinattnRuns {
+  int len, chunks, rev, C;
+  __device__ __forceinline__ LinattnRuns(const LinattnArgs& p, int b, int rev_, int C_) : rev(rev_), C(C_) {
+    len = p.seq_lens ? min(max(__ldg(p.seq_lens + b), 0), p.T) : p.T;
+    chunks = (len + C - 1) / C;
+  }
+  // tokens in the first i chunks of the processing order
+  __device__ __forceinline__ int done(int i) const {
+    if (i >= chunks) return len;
+    return rev ? (i == 0 ? 0 : len - (chunks - i) * C) : i * C;
+  }
+};
+
+// Element (z, y) of the state that run `seg` of (b, h) starts from.
+template <int D>
+__device__ __forceinline__ float linattn_start(const LinattnArgs& p, const LinattnJob& jb, int job, int bh, int seg,
+                                               const LinattnRuns& rn, const Decay& dc, int z, int y) {
+  const int d = rn.done(seg * p.seg_chunks);
+  float s = jb.s_in ? jb.s_in[(size_t)bh * D * D + (jb.in_t ? y * D + z : z * D + y)] * dc.pow(d) : 0.f;
+  const float* g = p.seg + ((size_t)job * p.B * p.H + bh) * (p.nseg - 1) * D * D + z * D + y;
+  for (int r = 0; r < seg; ++r) s = fmaf(dc.pow(d - rn.done((r + 1) * p.seg_chunks)), g[(size_t)r * D * D], s);
+  return s;
+}
+
+// ---- fp32 arithmetic on the CUDA cores (either type) ----
+//
+// One CTA per (b, h, run, 32 rows of the state): rows of S and columns of the output are
+// independent.  Chunks of 32 tokens; x, y, z, the scores and S's rows in shared memory, S
+// itself in registers.  Bound by the shared-memory reads of the products.
+template <int D_>
+struct LinattnFma {
+  static constexpr int D = D_, C = 32, BZ = D < 32 ? D : 32, NSL = D / BZ, NT = 256;
+  static constexpr int LD = D + 4, LZ = BZ + 4, LP = C + 4;
+  static constexpr size_t bytes = sizeof(float) * (2 * C * LD + C * LZ + C * LP + BZ * LD + C);
+};
+
+template <class E, int N, int LDS>
+__device__ __forceinline__ void linattn_tile(float* dst, const E* src, long long stride, int n) {
+  constexpr int V = 16 / sizeof(E);                  // elements a load
+  for (int i = threadIdx.x; i < 32 * N / V; i += 256) {
+    const int r = i / (N / V), c = i % (N / V) * V;
+    float f[V];
+    if (r < n) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + r * stride + c));
+      E e[V];
+      memcpy(e, &u, 16);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = Elem<E>::to_f(e[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = 0.f;        // padding, whatever it holds
+    }
+#pragma unroll
+    for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(dst + r * LDS + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+  }
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
+  using S = LinattnFma<D>;
+  constexpr int C = S::C, BZ = S::BZ, LD = S::LD, LZ = S::LZ, LP = S::LP;
+  extern __shared__ __align__(16) float sm[];
+  float *sx = sm, *sy = sx + C * LD, *sz = sy + C * LD, *sp = sz + C * LZ, *ss = sp + C * LP, *sw = ss + BZ * LD;
+  const int job = blockIdx.y;
+  const LinattnJob& jb = p.job[job];
+  const int runs = p.phase == 1 ? p.nseg - 1 : p.nseg;
+  const int slice = blockIdx.x % S::NSL, seg = blockIdx.x / S::NSL % runs, bh = blockIdx.x / S::NSL / runs;
+  const int b = bh / p.H, h = bh % p.H, z0 = slice * BZ, tid = threadIdx.x;
+  const LinattnRuns rn(p, b, jb.rev, C);
+  const Decay dc(__ldg(p.log_decay + h));
+  const bool full = p.phase == 0;
+  // the thread's part of S: rows zr.., columns yc..yc+3
+  constexpr int DG = D / 4, NGR = 256 / DG, RPT = BZ > NGR ? BZ / NGR : 1;
+  const int zr = tid / DG * RPT, yc = tid % DG * 4;
+  const bool owner = zr < BZ;
+  float st[RPT][4];
+#pragma unroll
+  for (int r = 0; r < RPT; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      st[r][c] = full && owner ? linattn_start<D>(p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc + c) : 0.f;
+  const E* gx = static_cast<const E*>(jb.x) + b * jb.xs[0] + h * D;
+  const E* gy = static_cast<const E*>(jb.y) + b * jb.ys[0] + h * D;
+  const E* gz = static_cast<const E*>(jb.z) + b * jb.zs[0] + h * D + z0;
+  E* out = static_cast<E*>(jb.out) + ((size_t)b * p.T * p.H + h) * D + z0;
+  const int i0 = seg * p.seg_chunks, i1 = min(i0 + p.seg_chunks, rn.chunks);
+  const int ti = tid / 16 * 2, tj = tid % 16;
+  for (int it = i0; it < i1; ++it) {
+    const int c = jb.rev ? rn.chunks - 1 - it : it, t0 = c * C, n = min(C, rn.len - t0);
+    if (full) linattn_tile<E, D, LD>(sx, gx + t0 * jb.xs[1], jb.xs[1], n);
+    linattn_tile<E, D, LD>(sy, gy + t0 * jb.ys[1], jb.ys[1], n);
+    linattn_tile<E, BZ, LZ>(sz, gz + t0 * jb.zs[1], jb.zs[1], n);
+    if (tid < C) sw[tid] = tid < n ? jb.su * dc.pow(jb.rev ? tid + 1 : n - 1 - tid) : 0.f;
+    if (full && owner) {
+#pragma unroll
+      for (int r = 0; r < RPT; ++r)
+        *reinterpret_cast<float4*>(ss + (zr + r) * LD + yc) = make_float4(st[r][0], st[r][1], st[r][2], st[r][3]);
+    }
+    __syncthreads();
+    if (full) {
+      float a[2][2] = {{0.f, 0.f}, {0.f, 0.f}};      // scores of rows ti, ti+1 and columns tj, tj+16
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 xv[2], yv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          xv[e] = *reinterpret_cast<const float4*>(sx + (ti + e) * LD + d);
+          yv[e] = *reinterpret_cast<const float4*>(sy + (tj + 16 * e) * LD + d);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            a[e][f] = fmaf(xv[e].x, yv[f].x, a[e][f]);
+            a[e][f] = fmaf(xv[e].y, yv[f].y, a[e][f]);
+            a[e][f] = fmaf(xv[e].z, yv[f].z, a[e][f]);
+            a[e][f] = fmaf(xv[e].w, yv[f].w, a[e][f]);
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int k = jb.rev ? tj + 16 * f - ti - e : ti + e - tj - 16 * f;   // tokens apart
+          sp[(ti + e) * LP + tj + 16 * f] = k >= 0 ? a[e][f] * (jb.sp * dc.pow(k)) : 0.f;
+        }
+      __syncthreads();
+      constexpr int NC2 = BZ / 16;                   // columns tj, tj+16
+      float o[2][NC2], oi[2][NC2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int f = 0; f < NC2; ++f) o[e][f] = oi[e][f] = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int f = 0; f < NC2; ++f) o[e][f] = fmaf(sp[(ti + e) * LP + j], sz[j * LZ + tj + 16 * f], o[e][f]);
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 sv[NC2];
+#pragma unroll
+        for (int f = 0; f < NC2; ++f) sv[f] = *reinterpret_cast<const float4*>(ss + (tj + 16 * f) * LD + d);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 xv = *reinterpret_cast<const float4*>(sx + (ti + e) * LD + d);
+#pragma unroll
+          for (int f = 0; f < NC2; ++f) {
+            oi[e][f] = fmaf(xv.x, sv[f].x, oi[e][f]);
+            oi[e][f] = fmaf(xv.y, sv[f].y, oi[e][f]);
+            oi[e][f] = fmaf(xv.z, sv[f].z, oi[e][f]);
+            oi[e][f] = fmaf(xv.w, sv[f].w, oi[e][f]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = ti + e;
+        if (i >= n) continue;
+        const float g = jb.so * dc.pow(jb.rev ? n - 1 - i : i + 1);
+#pragma unroll
+        for (int f = 0; f < NC2; ++f)
+          out[(size_t)(t0 + i) * p.H * D + tj + 16 * f] = Elem<E>::from_f(fmaf(g, oi[e][f], o[e][f]));
+      }
+    }
+    if (owner) {
+      const float2 ln = dc.step(n);
+#pragma unroll
+      for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st[r][q] = decayed(ln, st[r][q]);
+#pragma unroll 4
+      for (int j = 0; j < C; ++j) {
+        const float w = sw[j];
+        const float4 yv = *reinterpret_cast<const float4*>(sy + j * LD + yc);
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+          const float zv = sz[j * LZ + zr + r] * w;
+          st[r][0] = fmaf(zv, yv.x, st[r][0]);
+          st[r][1] = fmaf(zv, yv.y, st[r][1]);
+          st[r][2] = fmaf(zv, yv.z, st[r][2]);
+          st[r][3] = fmaf(zv, yv.w, st[r][3]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (full) {                                        // padding: zeros, shared out over the runs
+    for (long long i = (long long)seg * 256 + tid; i < (long long)(p.T - rn.len) * BZ; i += p.nseg * 256)
+      out[(size_t)(rn.len + i / BZ) * p.H * D + i % BZ] = Elem<E>::from_f(0.f);
+  }
+  if (!owner) return;
+  float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D
+               : seg == p.nseg - 1 && jb.s_out ? jb.s_out + (size_t)bh * D * D : nullptr;
+  if (!dst) return;
+  const bool tr = full && jb.out_t;
+#pragma unroll
+  for (int r = 0; r < RPT; ++r)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int z = z0 + zr + r, y = yc + q;
+      dst[tr ? y * D + z : z * D + y] = st[r][q];
+    }
+}
+
+// ---- one token of every sequence ----
+//
+// S <- lambda S + v k^T, o = scale S q: reads and writes the fp32 state once, which is all
+// its time (2 D^2 4 bytes a head; k, q, v and o are a D-th of that).  D/4 lanes hold 4
+// columns each of one row; a lane keeps NR rows' pieces in flight.  The rows' dot products
+// are summed over the lanes together: each exchange halves the rows that a lane still sums.
+template <int D_>
+struct LinattnDecode {
+  static constexpr int D = D_, LR = D / 4;           // lanes per row
+  static constexpr int NR = D >= 32 ? 8 : 2;         // rows per lane
+  static constexpr int RW = 32 / LR * NR;            // rows per warp: a divisor of D
+  static constexpr int NT = 128;
+};
+
+// The sums over LR lanes of v[0..N): on return lane l (of the LR) holds in v[0] the sum of row
+// rows(l), where the bits of l from the highest select the half of the rows kept.
+template <int LR, int N>
+__device__ __forceinline__ void linattn_rowsum(float (&v)[N], int lane, int& row) {
+  row = 0;
+#pragma unroll
+  for (int o = LR / 2, m = N / 2; o >= 1; o /= 2, m /= 2) {
+    if (m >= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < (m >= 1 ? m : 1); ++i) {
+        const float give = up ? v[i] : v[i + m], keep = up ? v[i + m] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+      row += up ? m : 0;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(128) linattn_decode_kernel(LinattnDecodeArgs p) {
+  using S = LinattnDecode<D>;
+  constexpr int LR = S::LR, NR = S::NR, RW = S::RW, GR = 32 / LR;
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * (S::NT / 32) + (threadIdx.x >> 5);
+  const long long bh = item / (D / RW);
+  if (bh >= (long long)p.B * p.H) return;            // whole warps
+  const int r0 = (int)(item % (D / RW)) * RW;
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  const int slot = p.slots ? __ldg(p.slots + b) : b;
+  const int g = lane / LR, c = lane % LR * 4;        // row r0 + g + GR i, columns c..c+3
+  E* out = static_cast<E*>(p.out) + bh * D;
+  if (slot < 0 || slot >= p.n_states) {
+    for (int i = lane; i < RW; i += 32) out[r0 + i] = Elem<E>::from_f(0.f);
+    return;
+  }
+  float* st = p.state + ((size_t)slot * p.H + h) * D * D + (size_t)(r0 + g) * D + c;
+  float4 s[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(st + (size_t)i * GR * D));
+  const E* q = static_cast<const E*>(p.q) + b * p.qs + h * D;
+  const E* k = static_cast<const E*>(p.k) + b * p.ks + h * D;
+  const E* v = static_cast<const E*>(p.v) + b * p.vs + h * D + r0 + g;
+  float qv[4], kv[4], vv[NR], o[NR];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    qv[j] = Elem<E>::to_f(q[c + j]);
+    kv[j] = Elem<E>::to_f(k[c + j]);
+  }
+#pragma unroll
+  for (int i = 0; i < NR; ++i) vv[i] = Elem<E>::to_f(v[i * GR]);
+  const float la = expf(__ldg(p.log_decay + h));
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    s[i].x = fmaf(la, s[i].x, vv[i] * kv[0]);
+    s[i].y = fmaf(la, s[i].y, vv[i] * kv[1]);
+    s[i].z = fmaf(la, s[i].z, vv[i] * kv[2]);
+    s[i].w = fmaf(la, s[i].w, vv[i] * kv[3]);
+    __stcs(reinterpret_cast<float4*>(st + (size_t)i * GR * D), s[i]);
+    o[i] = fmaf(s[i].x, qv[0], fmaf(s[i].y, qv[1], fmaf(s[i].z, qv[2], s[i].w * qv[3])));
+  }
+  int row;
+  linattn_rowsum<LR, NR>(o, lane, row);
+  // lanes that differ only in the bits below those used to halve the rows hold the same sum
+  constexpr int DUP = LR > NR ? LR / NR : 1, LEFT = NR > LR ? NR / LR : 1;
+  static_assert(LEFT == 1, "the rows are halved down to one a lane");
+  if (lane % DUP == 0) out[r0 + g + GR * row] = Elem<E>::from_f(o[0] * p.scale);
+}
+
+}  // namespace prism
