@@ -1,5 +1,5 @@
-// Linear attention on the CUDA cores and its single-token step: instantiations for both
-// types and every head dim.
+// Linear attention on the CUDA cores (fp32) and its single-token step (both types):
+// instantiations for every head dim.
 #include <cuda_runtime.h>
 
 #include "linattn.cuh"
@@ -7,10 +7,10 @@
 
 namespace prism {
 
-template <class E, int D>
+template <int D>
 cudaError_t launch_fma_t(const LinattnArgs& a, cudaStream_t s) {
   using S = LinattnFma<D>;
-  auto fn = linattn_fma_kernel<E, D>;
+  auto fn = linattn_fma_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes);
   if (e != cudaSuccess) return e;
   LinattnArgs p = a;
@@ -42,8 +42,8 @@ cudaError_t launch_decode_linattn_t(const LinattnDecodeArgs& a, cudaStream_t s) 
   }                                              \
   return cudaErrorInvalidValue;
 
-cudaError_t launch_linattn_fma(int dtype, int D, const LinattnArgs& a, cudaStream_t s) {
-#define PRISM_F(N) (dtype == 0 ? launch_fma_t<float, N>(a, s) : launch_fma_t<__nv_bfloat16, N>(a, s))
+cudaError_t launch_linattn_fma(int D, const LinattnArgs& a, cudaStream_t s) {
+#define PRISM_F(N) launch_fma_t<N>(a, s)
   PRISM_BY_DIM(D, PRISM_F)
 #undef PRISM_F
 }

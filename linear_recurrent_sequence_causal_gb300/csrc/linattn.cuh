@@ -113,7 +113,7 @@ __device__ __forceinline__ float linattn_start(const LinattnArgs& p, const Linat
   return s;
 }
 
-// ---- fp32 arithmetic on the CUDA cores (either type) ----
+// ---- fp32, on the CUDA cores ----
 //
 // One CTA per (b, h, run, 32 rows of the state): rows of S and columns of the output are
 // independent.  Chunks of 32 tokens; x, y, z, the scores and S's rows in shared memory, S
@@ -125,33 +125,22 @@ struct LinattnFma {
   static constexpr size_t bytes = sizeof(float) * (2 * C * LD + C * LZ + C * LP + BZ * LD + C);
 };
 
-template <class E, int N, int LDS>
-__device__ __forceinline__ void linattn_tile(float* dst, const E* src, long long stride, int n) {
-  constexpr int V = 16 / sizeof(E);                  // elements a load
-  for (int i = threadIdx.x; i < 32 * N / V; i += 256) {
-    const int r = i / (N / V), c = i % (N / V) * V;
-    float f[V];
-    if (r < n) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + r * stride + c));
-      E e[V];
-      memcpy(e, &u, 16);
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = Elem<E>::to_f(e[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = 0.f;        // padding, whatever it holds
-    }
-#pragma unroll
-    for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(dst + r * LDS + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+template <int N, int LDS>
+__device__ __forceinline__ void linattn_tile(float* dst, const float* src, long long stride, int n) {
+  for (int i = threadIdx.x; i < 32 * N / 4; i += 256) {
+    const int r = i / (N / 4), c = i % (N / 4) * 4;
+    *reinterpret_cast<float4*>(dst + r * LDS + c) =
+        r < n ? __ldg(reinterpret_cast<const float4*>(src + r * stride + c))
+              : make_float4(0.f, 0.f, 0.f, 0.f);       // padding, whatever it holds
   }
 }
 
-template <class E, int D>
+template <int D>
 __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   using S = LinattnFma<D>;
   constexpr int C = S::C, BZ = S::BZ, LD = S::LD, LZ = S::LZ, LP = S::LP;
-  extern __shared__ __align__(16) float sm[];
-  float *sx = sm, *sy = sx + C * LD, *sz = sy + C * LD, *sp = sz + C * LZ, *ss = sp + C * LP, *sw = ss + BZ * LD;
+  extern __shared__ __align__(16) float fma_sm[];
+  float *sx = fma_sm, *sy = sx + C * LD, *sz = sy + C * LD, *sp = sz + C * LZ, *ss = sp + C * LP, *sw = ss + BZ * LD;
   const int job = blockIdx.y;
   const LinattnJob& jb = p.job[job];
   const int runs = p.phase == 1 ? p.nseg - 1 : p.nseg;
@@ -170,17 +159,17 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       st[r][c] = full && owner ? linattn_start<D>(p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc + c) : 0.f;
-  const E* gx = static_cast<const E*>(jb.x) + b * jb.xs[0] + h * D;
-  const E* gy = static_cast<const E*>(jb.y) + b * jb.ys[0] + h * D;
-  const E* gz = static_cast<const E*>(jb.z) + b * jb.zs[0] + h * D + z0;
-  E* out = static_cast<E*>(jb.out) + ((size_t)b * p.T * p.H + h) * D + z0;
+  const float* gx = static_cast<const float*>(jb.x) + b * jb.xs[0] + h * D;
+  const float* gy = static_cast<const float*>(jb.y) + b * jb.ys[0] + h * D;
+  const float* gz = static_cast<const float*>(jb.z) + b * jb.zs[0] + h * D + z0;
+  float* out = static_cast<float*>(jb.out) + ((size_t)b * p.T * p.H + h) * D + z0;
   const int i0 = seg * p.seg_chunks, i1 = min(i0 + p.seg_chunks, rn.chunks);
   const int ti = tid / 16 * 2, tj = tid % 16;
   for (int it = i0; it < i1; ++it) {
     const int c = jb.rev ? rn.chunks - 1 - it : it, t0 = c * C, n = min(C, rn.len - t0);
-    if (full) linattn_tile<E, D, LD>(sx, gx + t0 * jb.xs[1], jb.xs[1], n);
-    linattn_tile<E, D, LD>(sy, gy + t0 * jb.ys[1], jb.ys[1], n);
-    linattn_tile<E, BZ, LZ>(sz, gz + t0 * jb.zs[1], jb.zs[1], n);
+    if (full) linattn_tile<D, LD>(sx, gx + t0 * jb.xs[1], jb.xs[1], n);
+    linattn_tile<D, LD>(sy, gy + t0 * jb.ys[1], jb.ys[1], n);
+    linattn_tile<BZ, LZ>(sz, gz + t0 * jb.zs[1], jb.zs[1], n);
     if (tid < C) sw[tid] = tid < n ? jb.su * dc.pow(jb.rev ? tid + 1 : n - 1 - tid) : 0.f;
     if (full && owner) {
 #pragma unroll
@@ -252,7 +241,7 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
         const float g = jb.so * dc.pow(jb.rev ? n - 1 - i : i + 1);
 #pragma unroll
         for (int f = 0; f < NC2; ++f)
-          out[(size_t)(t0 + i) * p.H * D + tj + 16 * f] = Elem<E>::from_f(fmaf(g, oi[e][f], o[e][f]));
+          out[(size_t)(t0 + i) * p.H * D + tj + 16 * f] = fmaf(g, oi[e][f], o[e][f]);
       }
     }
     if (owner) {
@@ -279,7 +268,7 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   }
   if (full) {                                        // padding: zeros, shared out over the runs
     for (long long i = (long long)seg * 256 + tid; i < (long long)(p.T - rn.len) * BZ; i += p.nseg * 256)
-      out[(size_t)(rn.len + i / BZ) * p.H * D + i % BZ] = Elem<E>::from_f(0.f);
+      out[(size_t)(rn.len + i / BZ) * p.H * D + i % BZ] = 0.f;
   }
   if (!owner) return;
   float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D

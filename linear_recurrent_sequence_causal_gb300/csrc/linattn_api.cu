@@ -1,10 +1,14 @@
 // C ABI of the linear attention layer's operators: argument checks, segment plan and
 // dispatch.  See include/prism_linattn.h for the contract of each entry point.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/prism_linattn.h"
-#include "linattn.cuh"
+#include "linattn_tc.cuh"
 #include "linattn.h"
 #include "rope.cuh"
 
@@ -91,18 +95,28 @@ int check_linattn(const prism_linattn_dims* d) {
   return PRISM_OK;
 }
 
-// Runs that each sequence is cut into: enough CTAs for about four on each SM, runs of at
-// least kMinRunChunks chunks.
-constexpr int kSMs = 152, kMinRunChunks = 4;
+// Runs that each sequence is cut into.  The CTAs of a launch take ceil(CTAs / resident) turns of
+// their run's chunks; cutting adds a first launch over the runs' states (all but the last run)
+// whose chunks cost about kStateChunk of a full one, and each CTA about kStart chunks of setting
+// up.  The cheapest count wins; runs keep at least two chunks.
+constexpr int kSMs = 152;
+constexpr double kStateChunk = 0.6, kStart = 1.5;
 void plan_runs(const prism_linattn_dims* d, int njobs, prism::LinattnArgs& a) {
-  const int C = 32, slices = d->d > 32 ? d->d / 32 : 1;
+  const bool tc = d->dtype == PRISM_BF16;
+  const int C = tc ? 128 : 32, slices = !tc && d->d > 32 ? d->d / 32 : 1;
+  const long long resident = (long long)kSMs * (tc ? (d->d == 128 ? 1 : 2) : 3);
   const long long ctas = (long long)d->B * d->H * slices * njobs;
   const int chunks = (d->T + C - 1) / C;
-  long long n = 4 * kSMs / ctas;
-  if (n > chunks / kMinRunChunks) n = chunks / kMinRunChunks;
-  if (n > prism::kLinattnMaxSeg) n = prism::kLinattnMaxSeg;
-  if (n < 2) n = 1;
-  a.seg_chunks = (int)((chunks + n - 1) / n);
+  double least = 0.;
+  for (int n = 1; n <= prism::kLinattnMaxSeg && n <= (chunks + 1) / 2; ++n) {
+    const int per = (chunks + n - 1) / n;
+    const double turns = (double)((ctas * n + resident - 1) / resident) * (per + kStart);
+    const double states = n == 1 ? 0. : (double)((ctas * (n - 1) + resident - 1) / resident) * (kStateChunk * per + kStart);
+    if (n == 1 || turns + states < least) {
+      least = turns + states;
+      a.seg_chunks = per;
+    }
+  }
   a.nseg = (chunks + a.seg_chunks - 1) / a.seg_chunks;
   a.njobs = njobs;
 }
@@ -118,7 +132,45 @@ size_t workspace_for(const prism_linattn_dims* d, int njobs) {
   return seg_bytes(d, a);
 }
 
-int run_linattn(const prism_linattn_dims* d, prism::LinattnArgs& a, const float* log_decay, const int32_t* seq_lens,
+struct Operand {
+  const void* p;
+  long long s[2];
+};
+
+// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the driver library).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// TMA map of a bf16 [B][T][H][d] input as (d, H, T, B), in boxes of 128 tokens of one head and up
+// to 64 dims, swizzled as wide as their rows.
+bool make_map(CUtensorMap* m, const Operand& in, const prism_linattn_dims* d) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const int cols = d->d < 64 ? d->d : 64;
+  const cuuint64_t dim[4] = {(cuuint64_t)d->d, (cuuint64_t)d->H, (cuuint64_t)d->T, (cuuint64_t)d->B};
+  const cuuint64_t stride[3] = {(cuuint64_t)d->d * 2, (cuuint64_t)in.s[1] * 2, (cuuint64_t)in.s[0] * 2};
+  const cuuint32_t box[4] = {(cuuint32_t)cols, 1, 128, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle sw = cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                             : CU_TENSOR_MAP_SWIZZLE_32B;
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(in.p), dim, stride, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int run_linattn(const prism_linattn_dims* d, prism::LinattnArgs& a, const Operand* in, int nin, const float* log_decay, const int32_t* seq_lens,
                 void* workspace, size_t workspace_bytes, void* stream) {
   const size_t need = seg_bytes(d, a);
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
@@ -127,16 +179,24 @@ int run_linattn(const prism_linattn_dims* d, prism::LinattnArgs& a, const float*
   a.log_decay = log_decay; a.seq_lens = seq_lens;
   a.seg = static_cast<float*>(workspace);
   a.status = nullptr;
-  return prism::launch_linattn_fma(d->dtype == PRISM_F32 ? 0 : 1, d->d, a, static_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
-             ? PRISM_OK
-             : PRISM_ERR_LAUNCH;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->dtype == PRISM_F32) return prism::launch_linattn_fma(d->d, a, s) == cudaSuccess ? PRISM_OK : PRISM_ERR_LAUNCH;
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_linattn_status) != cudaSuccess) return PRISM_ERR_CUDA;
+  a.status = static_cast<int*>(word);
+  prism::LinattnTcArgs t;
+  t.a = a;
+  for (int i = 0; i < nin; ++i)
+    if (!make_map(&t.map[i], in[i], d)) return PRISM_ERR_CUDA;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (d->d) {
+    case 16: e = prism::launch_linattn_tc_16(t, s); break;
+    case 32: e = prism::launch_linattn_tc_32(t, s); break;
+    case 64: e = prism::launch_linattn_tc_64(t, s); break;
+    case 128: e = prism::launch_linattn_tc_128(t, s); break;
+  }
+  return e == cudaSuccess ? PRISM_OK : PRISM_ERR_LAUNCH;
 }
-
-struct Operand {
-  const void* p;
-  long long s[2];
-};
 
 prism::LinattnJob make_job(const Operand* in, int x, int y, int z, void* out, const float* s_in, int in_t,
                            float* s_out, int out_t, float sp, float su, float so, int rev) {
@@ -241,7 +301,7 @@ extern "C" PRISM_API int prism_linattn_forward(const prism_linattn_dims* dims, c
   plan_runs(dims, 1, a);
   const float c = dims->scale;
   a.job[0] = make_job(in, 0, 1, 2, out, initial_state, 0, final_state, 0, c, 1.f, c, 0);
-  return run_linattn(dims, a, log_decay, seq_lens, workspace, workspace_bytes, stream);
+  return run_linattn(dims, a, in, 3, log_decay, seq_lens, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_linattn_backward(const prism_linattn_dims* dims, const void* q, const void* k,
@@ -267,7 +327,7 @@ extern "C" PRISM_API int prism_linattn_backward(const prism_linattn_dims* dims, 
   a.job[0] = make_job(in, 3, 2, 1, dq, initial_state, 1, nullptr, 0, c, 1.f, c, 0);
   a.job[1] = make_job(in, 1, 0, 3, dv, d_final_state, 0, d_initial_state, 0, c, c, 1.f, 1);
   a.job[2] = make_job(in, 2, 3, 0, dk, d_final_state, 1, nullptr, 0, c, c, 1.f, 1);
-  return run_linattn(dims, a, log_decay, seq_lens, workspace, workspace_bytes, stream);
+  return run_linattn(dims, a, in, 4, log_decay, seq_lens, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_linattn_decode_step(const prism_linattn_dims* dims, const void* q, const void* k,
