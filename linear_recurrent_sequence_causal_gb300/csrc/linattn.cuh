@@ -102,15 +102,32 @@ struct LinattnRuns {
   }
 };
 
-// Element (z, y) of the state that run `seg` of (b, h) starts from.
-template <int D>
-__device__ __forceinline__ float linattn_start(const LinattnArgs& p, const LinattnJob& jb, int job, int bh, int seg,
-                                               const LinattnRuns& rn, const Decay& dc, int z, int y) {
+// Elements (z, y..y+N-1) of the state that run `seg` of (b, h) starts from.
+template <int D, int N>
+__device__ __forceinline__ void linattn_start(float* st, const LinattnArgs& p, const LinattnJob& jb, int job, int bh,
+                                              int seg, const LinattnRuns& rn, const Decay& dc, int z, int y) {
   const int d = rn.done(seg * p.seg_chunks);
-  float s = jb.s_in ? jb.s_in[(size_t)bh * D * D + (jb.in_t ? y * D + z : z * D + y)] * dc.pow(d) : 0.f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) st[c] = 0.f;
+  auto add = [&](const float* g, float f, int step) {
+    if (step == 1) {
+#pragma unroll
+      for (int c = 0; c < N; c += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(g + c);
+        st[c] = fmaf(f, v.x, st[c]);
+        st[c + 1] = fmaf(f, v.y, st[c + 1]);
+        st[c + 2] = fmaf(f, v.z, st[c + 2]);
+        st[c + 3] = fmaf(f, v.w, st[c + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) st[c] = fmaf(f, g[c * D], st[c]);
+    }
+  };
+  if (jb.s_in) add(jb.s_in + (size_t)bh * D * D + (jb.in_t ? y * D + z : z * D + y), dc.pow(d), jb.in_t ? D : 1);
   const float* g = p.seg + ((size_t)job * p.B * p.H + bh) * (p.nseg - 1) * D * D + z * D + y;
-  for (int r = 0; r < seg; ++r) s = fmaf(dc.pow(d - rn.done((r + 1) * p.seg_chunks)), g[(size_t)r * D * D], s);
-  return s;
+#pragma unroll 1
+  for (int r = 0; r < seg; ++r) add(g + (size_t)r * D * D, dc.pow(d - rn.done((r + 1) * p.seg_chunks)), 1);
 }
 
 // ---- fp32, on the CUDA cores ----
@@ -155,10 +172,10 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   const bool owner = zr < BZ;
   float st[RPT][4];
 #pragma unroll
-  for (int r = 0; r < RPT; ++r)
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      st[r][c] = full && owner ? linattn_start<D>(p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc + c) : 0.f;
+  for (int r = 0; r < RPT; ++r) {
+    st[r][0] = st[r][1] = st[r][2] = st[r][3] = 0.f;
+    if (full && owner) linattn_start<D, 4>(st[r], p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc);
+  }
   const float* gx = static_cast<const float*>(jb.x) + b * jb.xs[0] + h * D;
   const float* gy = static_cast<const float*>(jb.y) + b * jb.ys[0] + h * D;
   const float* gz = static_cast<const float*>(jb.z) + b * jb.zs[0] + h * D + z0;

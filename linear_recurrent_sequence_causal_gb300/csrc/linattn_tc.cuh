@@ -6,18 +6,19 @@
 //   U  = Z^T Yd                     M D (rows of S)   N D               K 128, once a term of Yd
 // out_i = O1_i + so lambda^e(i) O2_i in fp32 and S <- lambda^n S + U in fp32 registers; S enters
 // O2 rounded to bf16 once.  Yd_j = su lambda^f(j) y_j is split into bf16 terms, each holding what
-// the ones before rounded off: two (16 bits) where the state only feeds outputs, which the
-// roundings of S and of the scores bound anyway; three (24 bits) where the caller gets it.
+// the ones before cut off: two (16 bits) where the state only feeds outputs, which the
+// roundings of S and of the scores bound anyway; three (24 bits) where the caller gets the
+// state and it still remembers the chunk (lambda^rest >= 1/16, rest the tokens that follow).
 // Three terms go in two steps of 64 tokens, so that they need no more shared memory.
 //
 // Roles.  The last warp copies the x, y and z tiles by TMA into a ring of five slots; the one
-// before issues the MMAs; A turns P into bf16 scores in place in TMEM and writes the outputs; B
-// splits y into its terms and keeps the state (for D < 128 the MMA repeats Z^T down its 128 rows,
-// and the warps share the columns of a row).  The chain from chunk to chunk is U -> state -> O2;
-// the scores of the next chunk, its copies and this chunk's outputs run beside it.
-// The element-wise work is bound by latency, not by issue slots: A and B have eight warps each
-// where one CTA has the SM, and their loops are kept short enough for the instruction
-// cache (unrolled and with four warps each, D = 128 took 18 000 cycles a chunk).
+// before issues the MMAs; A turns P into bf16 scores in place in TMEM, splits y, and sends the
+// outputs through x's slot by TMA; B keeps the state (for D < 128 the MMA repeats Z^T down its
+// 128 rows, and the warps share the columns of a row).  The chain from chunk to chunk is
+// U -> state -> O2; the scores of the next chunk, its copies and this chunk's outputs run beside
+// it.  The element-wise work is bound by latency and instruction fetch, not by issue slots: hence
+// eight warps in A, no long-lived registers there, and short loops (D = 128 took 18 000 cycles
+// a chunk unrolled and with four warps each in A and B).
 //
 // Tiles lie in shared memory as TMA writes them with a swizzle as wide as a row (32, 64, 128
 // bytes; D = 128 is two boxes of 64 columns): K-major as X, Y and S are read, MN-major as Z
@@ -34,14 +35,15 @@ namespace prism {
 
 struct LinattnTcArgs {
   CUtensorMap map[4];             // q, k, v, dO as [D][H][T][B] in boxes of 128 tokens
+  CUtensorMap out[3];             // the passes' outputs
   LinattnArgs a;
 };
 
 template <int D_>
 struct LinattnTc {
   static constexpr int D = D_, C = 128, SLOTS = 5;
-  static constexpr int W = D == 128 ? 8 : 4;                    // warps of A, and of B
-  static constexpr int NT = (2 * W + 2) * 32;
+  static constexpr int WA = 8, WB = D == 128 ? 8 : 4;           // warps of A and of B
+  static constexpr int NT = (WA + WB + 2) * 32;
   static constexpr uint32_t RB = D >= 64 ? 128 : 2 * D;         // bytes of a tile row in one box
   static constexpr uint32_t NB = 2 * D / RB;                    // boxes of a tile
   static constexpr uint32_t kTile = C * 2 * D, kBox = C * RB;
@@ -50,7 +52,7 @@ struct LinattnTc {
   static constexpr uint32_t oPow = oRing + SLOTS * kTile;       // lambda^k, k = 0..C
   static constexpr uint32_t oApart = oPow + (C + 4) * 4;        // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
-  static constexpr uint32_t bytes = oBar + 19 * 8 + 8;
+  static constexpr uint32_t bytes = oBar + 20 * 8 + 8;
   // TMEM columns.  D = 64: U takes the half of P that the bf16 scores leave free, so that two
   // CTAs share an SM's 512 columns.
   static constexpr bool kShareU = D == 64;
@@ -58,10 +60,10 @@ struct LinattnTc {
   static constexpr uint32_t kCols = D == 128 ? 512 : 256;
   static constexpr int kCtas = D == 128 ? 1 : 2;                // resident per SM
   // state: a thread of B has a row and a part of its columns
-  static constexpr int NP = W / 4 * (D >= 128 ? 1 : 128 / D > 4 ? 4 : 128 / D);
+  static constexpr int NP = D == 128 ? 2 : D == 64 ? 2 : 4;
   static constexpr int NS = D / NP;
   // bf16 scores: each part of A's columns keeps its own in place, from the start of its part
-  static constexpr uint32_t kPart = 128 / (W / 4);
+  static constexpr uint32_t kPart = 128 / (WA / 4);
   static __device__ __forceinline__ constexpr uint32_t score(int kk) {
     return cP + kk * 16 / kPart * kPart + kk * 16 % kPart / 2;
   }
@@ -81,26 +83,20 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn_major, bool b
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
-// The MMAs of a whole warp: every lane comes with the same operands and one of them, always the
-// same, issues.  (Issued from a branch that one lane takes, the operands reach the uniform
-// registers that the instruction reads one by one: about 100 cycles an MMA.)
-__device__ __forceinline__ void mma_w(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+// True in one lane of a converged warp, always the same.  A branch on it (and not on a lane
+// number) lets the operands of the MMAs inside stay in uniform registers; moved there one by
+// one they cost about 100 cycles an MMA.
+__device__ __forceinline__ bool elect() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
 }
 // A from TMEM (two bf16 of one row in a 32-bit column)
-__device__ __forceinline__ void mma_wt(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
-}
-__device__ __forceinline__ void commit_w(uint64_t* bar) {
-  asm volatile(
-      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)));
 }
 __device__ __forceinline__ void ld16a(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -143,6 +139,17 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {
   return u;
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+// the upper half of an fp32 value, as a bf16, and of two
+__device__ __forceinline__ float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+__device__ __forceinline__ uint32_t top2(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ void tma_store_4d(const void* map, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 }  // namespace tc
 
@@ -150,7 +157,7 @@ template <int D>
 __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     linattn_tc_kernel(const __grid_constant__ LinattnTcArgs args) {
   using S = LinattnTc<D>;
-  constexpr int C = S::C, SLOTS = S::SLOTS, W = S::W;
+  constexpr int C = S::C, SLOTS = S::SLOTS, WA = S::WA, WB = S::WB;
   extern __shared__ __align__(1024) unsigned char sm[];
   const LinattnArgs& p = args.a;
   float* pw = reinterpret_cast<float*>(sm + S::oPow);
@@ -164,8 +171,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_u = bar_qk + 4;              // their products are in U
   uint64_t* bar_s = bar_qk + 5;              // S is in shared memory, U of the last chunk is read
   uint64_t* bar_z = bar_qk + 6;              // padding rows of y and z are zeros (once a sequence)
-  uint64_t* bar_end = bar_qk + 7;            // every MMA issued is done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + 19 * 8);
+  uint64_t* bar_out = bar_qk + 7;            // the outputs are in x's slot
+  uint64_t* bar_end = bar_qk + 8;            // every MMA issued is done
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + 20 * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int job = blockIdx.y;
@@ -176,10 +184,12 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   const LinattnRuns rn(p, b, jb.rev, C);
   const int i0 = seg * p.seg_chunks, nch = max(min(i0 + p.seg_chunks, rn.chunks) - i0, 0);
   const Decay dc(__ldg(p.log_decay + h));
-  const int terms = jb.s_out ? 3 : 2, rows = terms == 3 ? C / 2 : C;    // rows of y in a step
   // chunk of step it: its first token and how many are there
   auto first = [&](int it) { return (rev ? rn.chunks - 1 - (i0 + it) : i0 + it) * C; };
   auto count = [&](int t0) { return min(C, rn.len - t0); };
+  // terms of Yd in step it's chunk; rows of y in a step
+  auto terms_of = [&](int it) { return jb.s_out && dc.pow(rn.len - rn.done(i0 + it + 1)) >= 0.0625f ? 3 : 2; };
+  auto rows_of = [&](int terms) { return terms == 3 ? C / 2 : C; };
   // K-steps of 16 tokens with tokens in them; whether the last has padding of this sequence
   auto ksteps = [&](int n) { return (n + 15) / 16; };
   auto ragged = [&](int t0, int n) { return (n & 15) != 0 && t0 + n < p.T; };
@@ -190,12 +200,13 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       tc::bar_init(bar_empty + i, 1);
     }
     tc::bar_init(bar_qk, 1);
-    tc::bar_init(bar_p, W);
+    tc::bar_init(bar_p, WA);
     tc::bar_init(bar_o, 1);
-    tc::bar_init(bar_y, W);
+    tc::bar_init(bar_y, WA);
     tc::bar_init(bar_u, 1);
-    tc::bar_init(bar_s, W);
-    tc::bar_init(bar_z, W);
+    tc::bar_init(bar_s, WB);
+    tc::bar_init(bar_z, WA);
+    tc::bar_init(bar_out, WA);
     tc::bar_init(bar_end, 1);
     tc::bar_fence_init();
   }
@@ -204,7 +215,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     apart[k] = x >= 0 ? jb.sp * dc.pow(x) : 0.f;
     if (k <= C) pw[k] = dc.pow(k);
   }
-  if (warp == 2 * W) tc::alloc(tslot, S::kCols);
+  if (warp == WA + WB) tc::alloc(tslot, S::kCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   // tiles a chunk: x, y, z (or y, z): the i-th tile of the run lies in slot i % SLOTS
   const int per = full ? 3 : 2;
 
-  if (warp == 2 * W + 1) {
+  if (warp == WA + WB + 1) {
     // ---- copies ----
     if (lane == 0) {
       int tile = 0;
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       // a copy still in flight may not outlive the CTA
       for (int i = max(tile - SLOTS, 0); i < tile; ++i) ok &= tc::bar_wait(bar_full + i % SLOTS, (i / SLOTS) & 1);
     }
-  } else if (warp == 2 * W) {
+  } else if (warp == WA + WB) {
     // ---- MMAs: the whole warp runs, one lane issues ----
     {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -258,7 +269,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       constexpr uint32_t kNextZ = D == 128 ? S::kBox : 0;    // rows past D repeat Z^T
       const uint64_t d_ring = tc::desc_sw<S::RB>(base + S::oRing, S::kBox);
       const uint64_t d_zt = tc::desc_sw<S::RB>(base + S::oRing, kNextZ);
-      const uint64_t d_mid = tc::desc_sw<S::RB>(base + S::oMid, rows * S::RB);
       const uint64_t d_s = tc::desc_sw<S::RB>(base + S::oS, 16);
       auto at = [](int tile) { return (uint64_t)((uint32_t)(tile % SLOTS) * (S::kTile / 16)); };
       // K-step kk (16 columns) in a K-major tile whose boxes are `box` bytes, in 16 bytes
@@ -270,10 +280,13 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         const int t0 = first(it);
         if (ragged(t0, count(t0)) && !wait(bar_z, 0)) return;
         if (S::kShareU && !wait(bar_s, it)) return;          // U of the last chunk is read
+        if (tc::elect()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_w(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
-        tc::commit_w(bar_qk);
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
+          tc::commit(bar_qk);
+        }
+        __syncwarp();
       };
       if (full && steps > 0) scores(0);
       int step = 0;                                          // steps of Yd so far
@@ -284,50 +297,81 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         if (full) {
           const uint64_t dz = d_ring + at(tz), dx = d_ring + at(ty - 1);
           if (!wait(bar_p, it)) break;
+          if (tc::elect()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < ks) tc::mma_wt(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk < ks) tc::mma_ta(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
+          }
+          __syncwarp();
           if (!wait(bar_s, it)) break;
+          if (tc::elect()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_w(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
-          tc::commit_w(bar_o);
-          tc::commit_w(bar_empty + (ty - 1) % SLOTS);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
+            tc::commit(bar_o);
+          }
+          __syncwarp();
         } else {
           if (it > 0 && !wait(bar_s, it)) break;             // U of the last chunk is read
           if (ragged(t0, n) && !wait(bar_z, 0)) break;
         }
+        const int terms = __shfl_sync(0xffffffffu, terms_of(it), 0), rows = rows_of(terms);
+        const uint64_t d_mid = tc::desc_sw<S::RB>(base + S::oMid, rows * S::RB);
         for (int r0 = 0; r0 < ks * 16; r0 += rows, ++step) {
           if (!wait(bar_y, step)) break;
           const uint64_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
           const int kn = min(ks - r0 / 16, rows / 16);
+          if (tc::elect()) {
 #pragma unroll 1
-          for (int t = 0; t < terms; ++t) {
-            const uint64_t d = t == 0 ? dy : d_mid + (t - 1) * (S::kTile / 32);
+            for (int t = 0; t < terms; ++t) {
+              const uint64_t d = t == 0 ? dy : d_mid + (t - 1) * (S::kTile / 32);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              if (kk < kn) tc::mma_w(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+              for (int kk = 0; kk < 8; ++kk)
+                if (kk < kn) tc::mma(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+            }
+            tc::commit(bar_u);
           }
-          tc::commit_w(bar_u);
+          __syncwarp();
         }
         if (!ok) break;
-        tc::commit_w(bar_empty + ty % SLOTS);
-        tc::commit_w(bar_empty + tz % SLOTS);
+        if (tc::elect()) {
+          tc::commit(bar_empty + ty % SLOTS);
+          tc::commit(bar_empty + tz % SLOTS);
+        }
+        __syncwarp();
         if (full && it + 1 < steps) scores(it + 1);
       }
-      tc::commit_w(bar_end);
+      if (tc::elect()) tc::commit(bar_end);
+      __syncwarp();
       ok &= tc::bar_wait(bar_end, 0);
     }
-  } else if (warp < W) {
-    // ---- A: scores and outputs; thread = token i of the chunk and a part of the columns ----
-    if (full) {
-      constexpr int PA = W / 4, JB = 4 / PA, CO = D / PA, G = CO < 32 ? CO : 32;
-      const int i = (warp & 3) * 32 + lane, part = warp >> 2;
-      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
-      const bool wide = (reinterpret_cast<uintptr_t>(jb.out) & 31) == 0;
-      for (int it = 0; it < nch; ++it) {
-        const int t0 = first(it), n = count(t0), ks = ksteps(n);
+  } else if (warp < WA) {
+    // ---- A: scores, the terms of y, outputs ----
+    constexpr int PA = WA / 4, JB = 4 / PA, CO = D / PA, G = CO < 32 ? CO : 32;
+    const int i = (warp & 3) * 32 + lane, part = warp >> 2;  // token of the chunk, part of the columns
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    int step = 0;
+    for (int it = 0; it < nch && ok; ++it) {
+      const int t0 = first(it), n = count(t0), ks = ksteps(n), krows = ks * 16;
+      const int ty = per * it + per - 2, tz = ty + 1;
+      unsigned char* ys = sm + S::oRing + (ty % SLOTS) * S::kTile;
+      if (!wait(bar_full + ty % SLOTS, ty / SLOTS)) break;
+      if (ragged(t0, n)) {
+        // padding rows of the last K-step may hold NaN: zeros in y and z
+        if (!wait(bar_full + tz % SLOTS, tz / SLOTS)) break;
+        unsigned char* zs = sm + S::oRing + (tz % SLOTS) * S::kTile;
+        const uint32_t pieces = (krows - n) * S::RB / 16;
+        for (uint32_t k = tid; k < pieces * S::NB; k += WA * 32) {
+          const uint32_t o = k / pieces * S::kBox + n * S::RB + k % pieces * 16;
+          *reinterpret_cast<uint4*>(ys + o) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(zs + o) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_smem_to_async();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar_z);
+        if (!wait(bar_z, 0)) break;
+      }
+      if (full) {
         if (!wait(bar_qk, it)) break;
 #pragma unroll 1
         for (int jq = part * JB; jq < (part + 1) * JB && jq * 2 < ks; ++jq) {
@@ -350,52 +394,106 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(bar_p);
+      }
+      const int terms = terms_of(it), rows = rows_of(terms);
+#pragma unroll 1
+      for (int r0 = 0; r0 < krows; r0 += rows, ++step) {
+        if (step > 0 && !wait(bar_u, step - 1)) break;       // the last step's terms are read
+        const uint32_t end = (uint32_t)min(rows, krows - r0) * S::RB;
+        // 16-byte pieces of the rows of this step, box by box
+#pragma unroll 2
+        for (uint32_t k = tid * 16; k < S::NB * end; k += WA * 32 * 16) {
+          const uint32_t box = S::NB == 1 ? 0 : k >= end, o = k - box * end;
+          const int r = r0 + (int)(o / S::RB);
+          unsigned char* y = ys + box * S::kBox + r0 * S::RB + o;
+          const uint4 u = *reinterpret_cast<const uint4*>(y);
+          const float w = r < n ? jb.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
+          const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+          uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // each term takes the upper half of the fp32 value, the next what that cuts off
+            const float a = tc::bf_lo(in[e]) * w, c = tc::bf_hi(in[e]) * w;
+            hi[e] = tc::top2(a, c);
+            const float ra = a - tc::top(a), rc = c - tc::top(c);
+            mid[e] = tc::top2(ra, rc);
+            lo[e] = tc::top2(ra - tc::top(ra), rc - tc::top(rc));
+          }
+          unsigned char* m = sm + S::oMid + box * (rows * S::RB) + o;
+          *reinterpret_cast<uint4*>(y) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(m) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+          if (terms == 3) *reinterpret_cast<uint4*>(m + S::kTile / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        tc::fence_smem_to_async();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar_y);
+        if (!full || r0 > 0) continue;
+        // the outputs, into x's slot and out by TMA; padding rows are zeros
         const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
-        __nv_bfloat16* dst = out + (size_t)(t0 + i) * p.H * D + part * CO;
+        const int slot = (ty - 1) % SLOTS;
+        unsigned char* xs = sm + S::oRing + slot * S::kTile;
         if (!wait(bar_o, it)) break;
 #pragma unroll 1
-        for (int c = 0; c < CO; c += G) {
+        for (int c = part * CO; c < (part + 1) * CO; c += G) {
           uint32_t a[G], e[G];
-          tc::lda(lanes + S::cO1 + part * CO + c, a);
-          tc::lda(lanes + S::cO2 + part * CO + c, e);
+          tc::lda(lanes + S::cO1 + c, a);
+          tc::lda(lanes + S::cO2 + c, e);
           tc::wait_ld(a, e);
 #pragma unroll
-          for (int q = 0; q < G; q += 16) {
-            uint32_t o[8];
+          for (int q = 0; q < G; q += 8) {
+            uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 4; ++k)
               o[k] = tc::bf2(fmaf(g, __uint_as_float(e[q + 2 * k]), __uint_as_float(a[q + 2 * k])),
                              fmaf(g, __uint_as_float(e[q + 2 * k + 1]), __uint_as_float(a[q + 2 * k + 1])));
-            if (i >= n) continue;
-            if (wide) {                                      // whole 32-byte sectors
-              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + c + q), "r"(o[0]), "r"(o[1]),
-                           "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                           : "memory");
-            } else {
-              *reinterpret_cast<uint4*>(dst + c + q) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(dst + c + q + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
+            const uint32_t off = (uint32_t)((c + q) / 64) * S::kBox + i * S::RB + (c + q) % 64 * 2;
+            *reinterpret_cast<uint4*>(xs + (off ^ ((off >> 3) & (S::RB - 16)))) =
+                i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
           }
         }
+        tc::fence_smem_to_async();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar_out);
+        if (tid == 0 && wait(bar_out, it)) {
+          for (uint32_t x = 0; x < S::NB; ++x)
+            tc::tma_store_4d(&args.out[job], xs + x * S::kBox, x * 64, h, t0, b);
+          tc::bulk_commit();
+          tc::bulk_wait_read();
+          tc::bar_arrive(bar_empty + slot);
+        }
       }
-      // padding: zeros, shared out over the runs
-      for (long long k = (long long)seg * (W * 32) + tid; k < (long long)(p.T - rn.len) * (D / 8); k += p.nseg * (W * 32))
-        *reinterpret_cast<uint4*>(out + (size_t)(rn.len + k / (D / 8)) * p.H * D + k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+    }
+    if (full) {
+      if (tid == 0) tc::bulk_wait_all();
+      // chunks of padding: zeros, shared out over the runs
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
+      const int from = min(rn.chunks * C, p.T);
+      for (long long k = (long long)seg * (WA * 32) + tid; k < (long long)(p.T - from) * (D / 8); k += p.nseg * (WA * 32))
+        *reinterpret_cast<uint4*>(out + (size_t)(from + k / (D / 8)) * p.H * D + k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     }
   } else {
-    // ---- B: the terms of y and the state ----
+    // ---- B: the state ----
     constexpr int NS = S::NS;
-    const int t = tid - W * 32, wb = warp - W;
+    const int wb = warp - WA;
     const uint32_t lanes = tmem + ((uint32_t)((wb & 3) * 32) << 16);
     const int row = ((wb & 3) * 32 + lane) % D;              // row of S (TMEM lane l holds row l % D)
     const int y0 = (D == 128 ? wb >> 2 : D == 64 ? wb >> 1 : wb) * NS;
     const bool mine = D >= 32 || lane < D;                   // D = 16: lanes 16.. repeat
     float st[NS];
+    if (full) {
+      linattn_start<D, NS>(st, p, jb, job, bh, seg, rn, dc, row, y0);
+    } else {
 #pragma unroll
-    for (int c = 0; c < NS; ++c)
-      st[c] = full ? linattn_start<D>(p, jb, job, bh, seg, rn, dc, row, y0 + c) : 0.f;
-    auto hand_state = [&]() {
-      if (full && mine) {                                    // bf16 rows of S, K-major
+      for (int c = 0; c < NS; ++c) st[c] = 0.f;
+    }
+    const float2 whole = dc.step(C);
+    int step = 0;
+#pragma unroll 1
+    for (int it = 0; it < nch; ++it) {
+      // hand the state over: bf16 rows of S, K-major; U of the last chunk is read
+      if (full && mine) {
         if constexpr (NS >= 8) {
 #pragma unroll
           for (int c = 0; c < NS; c += 8) {
@@ -415,63 +513,11 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(bar_s);
-    };
-    hand_state();
-    int step = 0;
-    for (int it = 0; it < nch && ok; ++it) {
-      const int t0 = first(it), n = count(t0), krows = ksteps(n) * 16;
-      const int ty = per * it + per - 2, tz = ty + 1;
-      unsigned char* ys = sm + S::oRing + (ty % SLOTS) * S::kTile;
-      if (!wait(bar_full + ty % SLOTS, ty / SLOTS)) break;
-      if (ragged(t0, n)) {
-        // padding rows of the last K-step may hold NaN: zeros in y and z
-        if (!wait(bar_full + tz % SLOTS, tz / SLOTS)) break;
-        unsigned char* zs = sm + S::oRing + (tz % SLOTS) * S::kTile;
-        const uint32_t pieces = (krows - n) * S::RB / 16;
-        for (uint32_t k = t; k < pieces * S::NB; k += W * 32) {
-          const uint32_t o = k / pieces * S::kBox + n * S::RB + k % pieces * 16;
-          *reinterpret_cast<uint4*>(ys + o) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(zs + o) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_smem_to_async();
-        asm volatile("bar.sync 1, %0;\n" ::"n"(W * 32) : "memory");
-        if (lane == 0) tc::bar_arrive(bar_z);
-      }
-      if (full && !wait(bar_qk, it)) break;                  // the scores have read y
-#pragma unroll 1
-      for (int r0 = 0; r0 < krows; r0 += rows, ++step) {
-        if (r0 > 0 && !wait(bar_u, step - 1)) break;         // the last step's terms are read
-        const uint32_t end = (uint32_t)min(rows, krows - r0) * S::RB;
-        // 16-byte pieces of the rows of this step, box by box
-#pragma unroll 2
-        for (uint32_t k = t * 16; k < S::NB * end; k += W * 32 * 16) {
-          const uint32_t box = S::NB == 1 ? 0 : k >= end, o = k - box * end;
-          const int r = r0 + (int)(o / S::RB);
-          unsigned char* y = ys + box * S::kBox + r0 * S::RB + o;
-          const uint4 u = *reinterpret_cast<const uint4*>(y);
-          const float w = r < n ? jb.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
-          const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-          uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = tc::bf_lo(in[e]), c = tc::bf_hi(in[e]);
-            hi[e] = tc::bf2(a * w, c * w);
-            const float ra = fmaf(a, w, -tc::bf_lo(hi[e])), rc = fmaf(c, w, -tc::bf_hi(hi[e]));
-            mid[e] = tc::bf2(ra, rc);
-            lo[e] = tc::bf2(ra - tc::bf_lo(mid[e]), rc - tc::bf_hi(mid[e]));
-          }
-          unsigned char* m = sm + S::oMid + box * (rows * S::RB) + o;
-          *reinterpret_cast<uint4*>(y) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(m) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-          if (terms == 3) *reinterpret_cast<uint4*>(m + S::kTile / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        tc::fence_smem_to_async();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(bar_y);
-      }
-      if (!wait(bar_u, step - 1)) break;
-      const float2 ln = dc.step(n);
+      const int n = count(first(it)), krows = ksteps(n) * 16, rows = rows_of(terms_of(it));
+      for (int r0 = 0; r0 < krows; r0 += rows, ++step)
+        if (!wait(bar_u, step)) break;
+      if (!ok) break;
+      const float2 ln = n == C ? whole : dc.step(n);
       constexpr int G = NS >= 16 ? 16 : NS;
 #pragma unroll
       for (int c = 0; c < NS; c += G) {
@@ -482,7 +528,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         for (int k = 0; k < G; ++k) st[c + k] = fmaf(ln.x, st[c + k], fmaf(ln.y, st[c + k], __uint_as_float(u[k])));
       }
       if (full && !wait(bar_o, it)) break;                   // O2 has read S
-      if (it + 1 < nch) hand_state();
     }
     float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D
                  : seg == p.nseg - 1 && jb.s_out ? jb.s_out + (size_t)bh * D * D : nullptr;
@@ -502,7 +547,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   if (!ok) atomicOr(p.status, 1);
   tc::fence_before();
   __syncthreads();
-  if (warp == 2 * W) tc::dealloc(tmem, S::kCols);
+  if (warp == WA + WB) tc::dealloc(tmem, S::kCols);
 }
 
 template <int D>
