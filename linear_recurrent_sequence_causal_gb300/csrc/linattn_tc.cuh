@@ -12,8 +12,8 @@
 // Three terms go in two steps of 64 tokens, so that they need no more shared memory.
 //
 // Roles.  The last warp copies the x, y and z tiles by TMA into a ring of five slots; the one
-// before issues the MMAs; A turns P into bf16 scores in place in TMEM, splits y, and sends the
-// outputs through x's slot by TMA; B keeps the state (for D < 128 the MMA repeats Z^T down its
+// before issues the MMAs; A turns P into bf16 scores in place in TMEM, splits y, and
+// writes the outputs; B keeps the state (for D < 128 the MMA repeats Z^T down its
 // 128 rows, and the warps share the columns of a row).  The chain from chunk to chunk is
 // U -> state -> O2; the scores of the next chunk, its copies and this chunk's outputs run beside
 // it.  The element-wise work is bound by latency and instruction fetch, not by issue slots: hence
@@ -35,13 +35,12 @@ namespace prism {
 
 struct LinattnTcArgs {
   CUtensorMap map[4];             // q, k, v, dO as [D][H][T][B] in boxes of 128 tokens
-  CUtensorMap out[3];             // the passes' outputs
   LinattnArgs a;
 };
 
 template <int D_>
 struct LinattnTc {
-  static constexpr int D = D_, C = 128, SLOTS = 5;
+  static constexpr int D = D_, C = 128, SLOTS = D >= 64 ? 5 : 8;
   static constexpr int WA = 8, WB = D == 128 ? 8 : 4;           // warps of A and of B
   static constexpr int NT = (WA + WB + 2) * 32;
   static constexpr uint32_t RB = D >= 64 ? 128 : 2 * D;         // bytes of a tile row in one box
@@ -49,10 +48,10 @@ struct LinattnTc {
   static constexpr uint32_t kTile = C * 2 * D, kBox = C * RB;
   static constexpr uint32_t kState = D * 2 * D, kSBox = D * RB;
   static constexpr uint32_t oS = 0, oMid = (kState + 1023) & ~1023u, oRing = oMid + kTile;
-  static constexpr uint32_t oPow = oRing + SLOTS * kTile;       // lambda^k, k = 0..C
-  static constexpr uint32_t oApart = oPow + (C + 4) * 4;        // sp lambda^|x| at x = i - j + C, 0 on the masked side
+  static constexpr uint32_t oPow = oRing + SLOTS * kTile;       // lambda^k at k + C, 0 for k < 0
+  static constexpr uint32_t oApart = oPow + (2 * C + 4) * 4;    // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
-  static constexpr uint32_t bytes = oBar + 20 * 8 + 8;
+  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 8) * 8 + 8;
   // TMEM columns.  D = 64: U takes the half of P that the bf16 scores leave free, so that two
   // CTAs share an SM's 512 columns.
   static constexpr bool kShareU = D == 64;
@@ -82,6 +81,47 @@ __device__ __forceinline__ uint64_t desc_sw(uint32_t addr, uint32_t lbo) {
 __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// tc::bar_wait with the polls asleep for up to 20 us each (a second in all): a waiting warp takes
+// no issue slots from the working ones.
+__device__ __forceinline__ bool bar_wait_long(uint64_t* bar, uint32_t parity) {
+  for (uint32_t it = 0; it < 50000u; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_addr(bar)), "r"(parity)
+               : "memory");
+  return ok;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 // True in one lane of a converged warp, always the same.  A branch on it (and not on a lane
 // number) lets the operands of the MMAs inside stay in uniform registers; moved there one by
@@ -144,12 +184,6 @@ __device__ __forceinline__ float top(float a) { return __uint_as_float(__float_a
 __device__ __forceinline__ uint32_t top2(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ void tma_store_4d(const void* map, const void* src, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 }  // namespace tc
 
@@ -160,7 +194,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   constexpr int C = S::C, SLOTS = S::SLOTS, WA = S::WA, WB = S::WB;
   extern __shared__ __align__(1024) unsigned char sm[];
   const LinattnArgs& p = args.a;
-  float* pw = reinterpret_cast<float*>(sm + S::oPow);
+  float* pw = reinterpret_cast<float*>(sm + S::oPow) + C;
   float* apart = reinterpret_cast<float*>(sm + S::oApart);
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(sm + S::oBar);
   uint64_t* bar_empty = bar_full + SLOTS;
@@ -171,9 +205,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_u = bar_qk + 4;              // their products are in U
   uint64_t* bar_s = bar_qk + 5;              // S is in shared memory, U of the last chunk is read
   uint64_t* bar_z = bar_qk + 6;              // padding rows of y and z are zeros (once a sequence)
-  uint64_t* bar_out = bar_qk + 7;            // the outputs are in x's slot
-  uint64_t* bar_end = bar_qk + 8;            // every MMA issued is done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + 20 * 8);
+  uint64_t* bar_end = bar_qk + 7;            // every MMA issued is done
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 8) * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int job = blockIdx.y;
@@ -206,14 +239,13 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     tc::bar_init(bar_u, 1);
     tc::bar_init(bar_s, WB);
     tc::bar_init(bar_z, WA);
-    tc::bar_init(bar_out, WA);
     tc::bar_init(bar_end, 1);
     tc::bar_fence_init();
   }
   for (int k = tid; k <= 2 * C; k += S::NT) {
     const int x = rev ? C - k : k - C;                       // tokens apart, backwards or forwards
     apart[k] = x >= 0 ? jb.sp * dc.pow(x) : 0.f;
-    if (k <= C) pw[k] = dc.pow(k);
+    pw[k - C] = k >= C ? dc.pow(k - C) : 0.f;
   }
   if (warp == WA + WB) tc::alloc(tslot, S::kCols);
   tc::fence_before();
@@ -224,7 +256,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   bool ok = true;
   // after a wait that gave up a role issues no more work and ends
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = tc::bar_wait(bar, parity & 1);
+    if (ok) ok = tc::bar_wait_long(bar, parity & 1);
     tc::fence_after();
     return ok;
   };
@@ -259,7 +291,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       auto first = [&](int it) { return (rev ? chunks - 1 - (i0 + it) : i0 + it) * C; };
       auto count = [&](int t0) { return min(C, len - t0); };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, tc::bar_wait(bar, parity & 1));
+        if (ok) ok = __all_sync(0xffffffffu, tc::bar_wait_long(bar, parity & 1));
         tc::fence_after();
         return ok;
       };
@@ -273,8 +305,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       auto at = [](int tile) { return (uint64_t)((uint32_t)(tile % SLOTS) * (S::kTile / 16)); };
       // K-step kk (16 columns) in a K-major tile whose boxes are `box` bytes, in 16 bytes
       auto kstep = [](int kk, uint32_t box) { return (uint64_t)((uint32_t)(kk / 4) * (box / 16) + (uint32_t)(kk % 4) * 2); };
-      auto scores = [&](int it) {
-        const int tx = 3 * it, ty = tx + 1;
+      int scored = 0;                                        // chunks whose scores are issued
+      auto scores = [&]() {
+        const int it = scored, tx = 3 * it, ty = tx + 1;
         const uint64_t dx = d_ring + at(tx), dy = d_ring + at(ty);
         if (!wait(bar_full + tx % SLOTS, tx / SLOTS) || !wait(bar_full + ty % SLOTS, ty / SLOTS)) return;
         const int t0 = first(it);
@@ -287,12 +320,13 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           tc::commit(bar_qk);
         }
         __syncwarp();
+        ++scored;
       };
-      if (full && steps > 0) scores(0);
       int step = 0;                                          // steps of Yd so far
       for (int it = 0; it < steps && ok; ++it) {
         const int ty = per * it + per - 2, tz = ty + 1;
         const int t0 = first(it), n = count(t0), ks = ksteps(n);
+        if (full && scored == it) scores();
         if (!wait(bar_full + tz % SLOTS, tz / SLOTS)) break;
         if (full) {
           const uint64_t dz = d_ring + at(tz), dx = d_ring + at(ty - 1);
@@ -309,11 +343,20 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             for (int kk = 0; kk < D / 16; ++kk)
               tc::mma(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
             tc::commit(bar_o);
+            tc::commit(bar_empty + (ty - 1) % SLOTS);
           }
           __syncwarp();
         } else {
           if (it > 0 && !wait(bar_s, it)) break;             // U of the last chunk is read
           if (ragged(t0, n) && !wait(bar_z, 0)) break;
+        }
+        // the next chunk's scores before this one's U, if their tiles are there: A needs them
+        // first, and U waits for A
+        if (full && !S::kShareU && it + 1 < steps) {
+          const int ux = 3 * it + 3, uy = ux + 1, u0 = first(it + 1);
+          if (!ragged(u0, count(u0)) && __all_sync(0xffffffffu, tc::bar_test(bar_full + ux % SLOTS, ux / SLOTS & 1) &&
+                                                                    tc::bar_test(bar_full + uy % SLOTS, uy / SLOTS & 1)))
+            scores();
         }
         const int terms = __shfl_sync(0xffffffffu, terms_of(it), 0), rows = rows_of(terms);
         const uint64_t d_mid = tc::desc_sw<S::RB>(base + S::oMid, rows * S::RB);
@@ -339,7 +382,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           tc::commit(bar_empty + tz % SLOTS);
         }
         __syncwarp();
-        if (full && it + 1 < steps) scores(it + 1);
       }
       if (tc::elect()) tc::commit(bar_end);
       __syncwarp();
@@ -350,6 +392,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     constexpr int PA = WA / 4, JB = 4 / PA, CO = D / PA, G = CO < 32 ? CO : 32;
     const int i = (warp & 3) * 32 + lane, part = warp >> 2;  // token of the chunk, part of the columns
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
+    const bool wide = (reinterpret_cast<uintptr_t>(jb.out) & 31) == 0;
     int step = 0;
     for (int it = 0; it < nch && ok; ++it) {
       const int t0 = first(it), n = count(t0), ks = ksteps(n), krows = ks * 16;
@@ -399,79 +443,95 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
 #pragma unroll 1
       for (int r0 = 0; r0 < krows; r0 += rows, ++step) {
         if (step > 0 && !wait(bar_u, step - 1)) break;       // the last step's terms are read
-        const uint32_t end = (uint32_t)min(rows, krows - r0) * S::RB;
-        // 16-byte pieces of the rows of this step, box by box
+        // 16-byte pieces of the rows of this step, box by box.  Rows past n hold zeros, or are in
+        // no K-step.
+        constexpr int RI = WA * 32 * 16 / S::RB;             // rows that A takes at once
+        const int r1 = r0 + tid / (S::RB / 16);
+        const float* wp = pw + (rev ? r1 + 1 : n - 1 - r1);
+        unsigned char* y = ys + r0 * S::RB + tid * 16;
+        unsigned char* m = sm + S::oMid + tid * 16;
+#pragma unroll 1
+        for (uint32_t box = 0; box < S::NB; ++box, y += S::kBox, m += rows * S::RB) {
 #pragma unroll 2
-        for (uint32_t k = tid * 16; k < S::NB * end; k += WA * 32 * 16) {
-          const uint32_t box = S::NB == 1 ? 0 : k >= end, o = k - box * end;
-          const int r = r0 + (int)(o / S::RB);
-          unsigned char* y = ys + box * S::kBox + r0 * S::RB + o;
-          const uint4 u = *reinterpret_cast<const uint4*>(y);
-          const float w = r < n ? jb.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
-          const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-          uint32_t hi[4], mid[4], lo[4];
+          for (int r = 0; r < min(rows, krows - r0); r += RI) {
+            if (RI > 64 && r1 - r0 + r >= rows) continue;    // D = 16, 32: a step has fewer rows than A takes
+            const uint4 u = *reinterpret_cast<const uint4*>(y + r * S::RB);
+            const float w = jb.su * wp[rev ? r : -r];
+            const uint64_t w2 = tc::pack2(w, w), minus = tc::pack2(-1.f, -1.f);
+            const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+            uint32_t hi[4], mid[4], lo[4];
+            uint64_t left[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // each term takes the upper half of the fp32 value, the next what that cuts off
-            const float a = tc::bf_lo(in[e]) * w, c = tc::bf_hi(in[e]) * w;
-            hi[e] = tc::top2(a, c);
-            const float ra = a - tc::top(a), rc = c - tc::top(c);
-            mid[e] = tc::top2(ra, rc);
-            lo[e] = tc::top2(ra - tc::top(ra), rc - tc::top(rc));
+            for (int e = 0; e < 4; ++e) {
+              // each term takes the upper half of the fp32 value, the next what that cuts off
+              const uint64_t v = tc::mul2(tc::pack2(tc::bf_lo(in[e]), tc::bf_hi(in[e])), w2);
+              float a, c;
+              tc::unpack2(v, a, c);
+              hi[e] = tc::top2(a, c);
+              left[e] = tc::fma2(tc::pack2(tc::top(a), tc::top(c)), minus, v);
+              tc::unpack2(left[e], a, c);
+              mid[e] = tc::top2(a, c);
+            }
+            *reinterpret_cast<uint4*>(y + r * S::RB) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(m + r * S::RB) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            if (terms == 3) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float a, c;
+                tc::unpack2(left[e], a, c);
+                tc::unpack2(tc::fma2(tc::pack2(tc::top(a), tc::top(c)), minus, left[e]), a, c);
+                lo[e] = tc::top2(a, c);
+              }
+              *reinterpret_cast<uint4*>(m + S::kTile / 2 + r * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
           }
-          unsigned char* m = sm + S::oMid + box * (rows * S::RB) + o;
-          *reinterpret_cast<uint4*>(y) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(m) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-          if (terms == 3) *reinterpret_cast<uint4*>(m + S::kTile / 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         tc::fence_smem_to_async();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(bar_y);
         if (!full || r0 > 0) continue;
-        // the outputs, into x's slot and out by TMA; padding rows are zeros
+        // the outputs: a row's 32-byte sectors from its own thread.  (Through shared memory and
+        // TMA the store waits behind the ring's loads: 2500 cycles at d = 128.)
         const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
-        const int slot = (ty - 1) % SLOTS;
-        unsigned char* xs = sm + S::oRing + slot * S::kTile;
+        const uint64_t g2 = tc::pack2(g, g);
+        __nv_bfloat16* dst = out + (size_t)(t0 + i) * p.H * D;
         if (!wait(bar_o, it)) break;
 #pragma unroll 1
         for (int c = part * CO; c < (part + 1) * CO; c += G) {
-          uint32_t a[G], e[G];
+          uint32_t a[G], e[G], o[G / 2];
           tc::lda(lanes + S::cO1 + c, a);
           tc::lda(lanes + S::cO2 + c, e);
           tc::wait_ld(a, e);
 #pragma unroll
-          for (int q = 0; q < G; q += 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[k] = tc::bf2(fmaf(g, __uint_as_float(e[q + 2 * k]), __uint_as_float(a[q + 2 * k])),
-                             fmaf(g, __uint_as_float(e[q + 2 * k + 1]), __uint_as_float(a[q + 2 * k + 1])));
-            const uint32_t off = (uint32_t)((c + q) / 64) * S::kBox + i * S::RB + (c + q) % 64 * 2;
-            *reinterpret_cast<uint4*>(xs + (off ^ ((off >> 3) & (S::RB - 16)))) =
-                i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < G; k += 2) {
+            float x, y;
+            tc::unpack2(tc::fma2(g2, tc::pack2(__uint_as_float(e[k]), __uint_as_float(e[k + 1])),
+                                 tc::pack2(__uint_as_float(a[k]), __uint_as_float(a[k + 1]))),
+                        x, y);
+            o[k / 2] = tc::bf2(x, y);
           }
-        }
-        tc::fence_smem_to_async();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(bar_out);
-        if (tid == 0 && wait(bar_out, it)) {
-          for (uint32_t x = 0; x < S::NB; ++x)
-            tc::tma_store_4d(&args.out[job], xs + x * S::kBox, x * 64, h, t0, b);
-          tc::bulk_commit();
-          tc::bulk_wait_read();
-          tc::bar_arrive(bar_empty + slot);
+          if (i >= n) continue;
+          if (G >= 16 && wide) {
+#pragma unroll
+            for (int k = 0; k < G / 2; k += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + c + 2 * k), "r"(o[k % (G / 2)]),
+                           "r"(o[(k + 1) % (G / 2)]), "r"(o[(k + 2) % (G / 2)]), "r"(o[(k + 3) % (G / 2)]),
+                           "r"(o[(k + 4) % (G / 2)]), "r"(o[(k + 5) % (G / 2)]), "r"(o[(k + 6) % (G / 2)]),
+                           "r"(o[(k + 7) % (G / 2)])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int k = 0; k < G / 2; k += 4)
+              *reinterpret_cast<uint4*>(dst + c + 2 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
         }
       }
     }
     if (full) {
-      if (tid == 0) tc::bulk_wait_all();
-      // chunks of padding: zeros, shared out over the runs
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
-      const int from = min(rn.chunks * C, p.T);
-      for (long long k = (long long)seg * (WA * 32) + tid; k < (long long)(p.T - from) * (D / 8); k += p.nseg * (WA * 32))
-        *reinterpret_cast<uint4*>(out + (size_t)(from + k / (D / 8)) * p.H * D + k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      // padding: zeros, shared out over the runs
+      for (long long k = (long long)seg * (WA * 32) + tid; k < (long long)(p.T - rn.len) * (D / 8); k += p.nseg * (WA * 32))
+        *reinterpret_cast<uint4*>(out + (size_t)(rn.len + k / (D / 8)) * p.H * D + k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     }
   } else {
     // ---- B: the state ----
@@ -518,6 +578,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         if (!wait(bar_u, step)) break;
       if (!ok) break;
       const float2 ln = n == C ? whole : dc.step(n);
+      const uint64_t lx = tc::pack2(ln.x, ln.x), ly = tc::pack2(ln.y, ln.y);
       constexpr int G = NS >= 16 ? 16 : NS;
 #pragma unroll
       for (int c = 0; c < NS; c += G) {
@@ -525,7 +586,11 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         tc::lda(lanes + S::cU + y0 + c, u);
         tc::wait_ld(u);
 #pragma unroll
-        for (int k = 0; k < G; ++k) st[c + k] = fmaf(ln.x, st[c + k], fmaf(ln.y, st[c + k], __uint_as_float(u[k])));
+        for (int k = 0; k < G; k += 2) {
+          const uint64_t s2 = tc::pack2(st[c + k], st[c + k + 1]);
+          const uint64_t v = tc::fma2(ly, s2, tc::pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
+          tc::unpack2(tc::fma2(lx, s2, v), st[c + k], st[c + k + 1]);
+        }
       }
       if (full && !wait(bar_o, it)) break;                   // O2 has read S
     }
