@@ -69,13 +69,16 @@ struct LinattnTc {
 };
 
 namespace tc {
-// Shared-memory matrix descriptor with a swizzle of RB bytes.  K-major: sbo = 8 rows (lbo unused);
-// MN-major: sbo = 8 rows (8 steps of K), lbo = the next RB bytes of M or N.
+// Shared-memory matrix descriptor with a swizzle of RB bytes, in two halves: the lower one moves
+// with the address (in units of 16 bytes).  K-major: the stride between 8-row groups is 8 RB
+// bytes (lbo unused); MN-major: that is the stride between 8 steps of K, and lbo the one to the
+// next RB bytes of M or N.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) & 0x3FFFu) << 16;
+}
 template <uint32_t RB>
-__device__ __forceinline__ uint64_t desc_sw(uint32_t addr, uint32_t lbo) {
-  constexpr uint64_t kind = RB == 128 ? 2 : RB == 64 ? 4 : 6;
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((8 * RB) >> 4) << 32) | ((uint64_t)1 << 46) | (kind << 61);
+__device__ __forceinline__ constexpr uint32_t desc_hi() {
+  return (8 * RB) >> 4 | 1u << 14 | (RB == 128 ? 2u : RB == 64 ? 4u : 6u) << 29;
 }
 // kind::f16 with bf16 A and B, fp32 accumulators, M = 128
 __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn_major, bool b_mn_major) {
@@ -124,19 +127,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 // True in one lane of a converged warp, always the same.  A branch on it (and not on a lane
-// number) lets the operands of the MMAs inside stay in uniform registers; moved there one by
-// one they cost about 100 cycles an MMA.
+// number) in a warp whose number and loop counts the compiler knows to be the same in every
+// lane lets the operands of the MMAs inside stay in uniform registers; moved there one by one
+// they cost about 100 cycles an MMA.
 __device__ __forceinline__ bool elect() {
   uint32_t e;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
   return e != 0;
 }
-// A from TMEM (two bf16 of one row in a 32-bit column)
-__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
+template <uint32_t RB>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+      "{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(desc_hi<RB>()));
+}
+// A from TMEM (two bf16 of one row in a 32-bit column)
+template <uint32_t RB>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(desc_hi<RB>()));
 }
 __device__ __forceinline__ void ld16a(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_end = bar_qk + 7;            // every MMA issued is done
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 8) * 8);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int job = blockIdx.y;
   const LinattnJob& jb = p.job[job];
   const bool full = p.phase == 0, rev = jb.rev != 0;
@@ -297,18 +309,17 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       };
       constexpr uint32_t id_p = tc::idesc_bf16(128, false, false), id_s = tc::idesc_bf16(D, false, false);
       constexpr uint32_t id_o = tc::idesc_bf16(D, false, true), id_u = tc::idesc_bf16(D, true, true);
-      constexpr uint64_t kStepMn = 16 * S::RB / 16;          // 16 tokens of an MN-major tile, in 16 bytes
+      constexpr uint32_t kStepMn = 16 * S::RB / 16;          // 16 tokens of an MN-major tile, in 16 bytes
       constexpr uint32_t kNextZ = D == 128 ? S::kBox : 0;    // rows past D repeat Z^T
-      const uint64_t d_ring = tc::desc_sw<S::RB>(base + S::oRing, S::kBox);
-      const uint64_t d_zt = tc::desc_sw<S::RB>(base + S::oRing, kNextZ);
-      const uint64_t d_s = tc::desc_sw<S::RB>(base + S::oS, 16);
-      auto at = [](int tile) { return (uint64_t)((uint32_t)(tile % SLOTS) * (S::kTile / 16)); };
+      const uint32_t d_ring = tc::desc_lo(base + S::oRing, S::kBox), d_zt = tc::desc_lo(base + S::oRing, kNextZ);
+      const uint32_t d_s = tc::desc_lo(base + S::oS, 16);
+      auto at = [](int tile) { return (uint32_t)(tile % SLOTS) * (S::kTile / 16); };
       // K-step kk (16 columns) in a K-major tile whose boxes are `box` bytes, in 16 bytes
-      auto kstep = [](int kk, uint32_t box) { return (uint64_t)((uint32_t)(kk / 4) * (box / 16) + (uint32_t)(kk % 4) * 2); };
+      auto kstep = [](int kk, uint32_t box) { return (uint32_t)(kk / 4) * (box / 16) + (uint32_t)(kk % 4) * 2; };
       int scored = 0;                                        // chunks whose scores are issued
       auto scores = [&]() {
         const int it = scored, tx = 3 * it, ty = tx + 1;
-        const uint64_t dx = d_ring + at(tx), dy = d_ring + at(ty);
+        const uint32_t dx = d_ring + at(tx), dy = d_ring + at(ty);
         if (!wait(bar_full + tx % SLOTS, tx / SLOTS) || !wait(bar_full + ty % SLOTS, ty / SLOTS)) return;
         const int t0 = first(it);
         if (ragged(t0, count(t0)) && !wait(bar_z, 0)) return;
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         if (tc::elect()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
+            tc::mma_ss<S::RB>(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
           tc::commit(bar_qk);
         }
         __syncwarp();
@@ -329,19 +340,25 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         if (full && scored == it) scores();
         if (!wait(bar_full + tz % SLOTS, tz / SLOTS)) break;
         if (full) {
-          const uint64_t dz = d_ring + at(tz), dx = d_ring + at(ty - 1);
+          const uint32_t dz = d_ring + at(tz), dx = d_ring + at(ty - 1);
           if (!wait(bar_p, it)) break;
           if (tc::elect()) {
+            if (ks == 8) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              if (kk < ks) tc::mma_ta(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
+              for (int kk = 0; kk < 8; ++kk)
+                tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < ks; ++kk)
+                tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
+            }
           }
           __syncwarp();
           if (!wait(bar_s, it)) break;
           if (tc::elect()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
+              tc::mma_ss<S::RB>(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
             tc::commit(bar_o);
             tc::commit(bar_empty + (ty - 1) % SLOTS);
           }
@@ -359,18 +376,29 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             scores();
         }
         const int terms = __shfl_sync(0xffffffffu, terms_of(it), 0), rows = rows_of(terms);
-        const uint64_t d_mid = tc::desc_sw<S::RB>(base + S::oMid, rows * S::RB);
+        const uint32_t d_mid = tc::desc_lo(base + S::oMid, rows * S::RB);
         for (int r0 = 0; r0 < ks * 16; r0 += rows, ++step) {
           if (!wait(bar_y, step)) break;
-          const uint64_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
+          const uint32_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
           const int kn = min(ks - r0 / 16, rows / 16);
           if (tc::elect()) {
 #pragma unroll 1
             for (int t = 0; t < terms; ++t) {
-              const uint64_t d = t == 0 ? dy : d_mid + (t - 1) * (S::kTile / 32);
+              const uint32_t d = t == 0 ? dy : d_mid + (t - 1) * (S::kTile / 32);
+              if (kn == rows / 16) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                if (kk < kn) tc::mma(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                for (int kk = 0; kk < 4; ++kk)
+                  tc::mma_ss<S::RB>(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                if (kn == 8) {
+#pragma unroll
+                  for (int kk = 4; kk < 8; ++kk)
+                    tc::mma_ss<S::RB>(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, true);
+                }
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk < kn; ++kk)
+                  tc::mma_ss<S::RB>(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+              }
             }
             tc::commit(bar_u);
           }
