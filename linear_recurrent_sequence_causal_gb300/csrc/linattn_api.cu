@@ -188,6 +188,9 @@ int run_linattn(const prism_linattn_dims* d, prism::LinattnArgs& a, const Operan
   t.a = a;
   for (int i = 0; i < nin; ++i)
     if (!make_map(&t.map[i], in[i], d)) return PRISM_ERR_CUDA;
+  const long long row = (long long)d->H * d->d;
+  for (int i = 0; i < a.njobs; ++i)
+    if (!make_map(&t.out[i], Operand{a.job[i].out, {d->T * row, row}}, d)) return PRISM_ERR_CUDA;
   cudaError_t e = cudaErrorInvalidValue;
   switch (d->d) {
     case 16: e = prism::launch_linattn_tc_16(t, s); break;

@@ -35,12 +35,13 @@ namespace prism {
 
 struct LinattnTcArgs {
   CUtensorMap map[4];             // q, k, v, dO as [D][H][T][B] in boxes of 128 tokens
+  CUtensorMap out[3];             // the passes' outputs
   LinattnArgs a;
 };
 
 template <int D_>
 struct LinattnTc {
-  static constexpr int D = D_, C = 128, SLOTS = D >= 64 ? 5 : 8;
+  static constexpr int D = D_, C = 128, SLOTS = D == 128 ? 5 : D == 64 ? 4 : 8;
   static constexpr int WA = 8, WB = D == 128 ? 8 : 4;           // warps of A and of B
   static constexpr int NT = (WA + WB + 2) * 32;
   static constexpr uint32_t RB = D >= 64 ? 128 : 2 * D;         // bytes of a tile row in one box
@@ -48,10 +49,14 @@ struct LinattnTc {
   static constexpr uint32_t kTile = C * 2 * D, kBox = C * RB;
   static constexpr uint32_t kState = D * 2 * D, kSBox = D * RB;
   static constexpr uint32_t oS = 0, oMid = (kState + 1023) & ~1023u, oRing = oMid + kTile;
-  static constexpr uint32_t oPow = oRing + SLOTS * kTile;       // lambda^k at k + C, 0 for k < 0
+  // outputs on their way out: at D = 128 in S's tile, which is as large and free from O2 to the
+  // next state
+  static constexpr bool kOutS = D == 128;
+  static constexpr uint32_t oOut = kOutS ? oS : oRing + SLOTS * kTile;
+  static constexpr uint32_t oPow = oRing + SLOTS * kTile + (kOutS ? 0 : kTile);   // lambda^k at k + C, 0 for k < 0
   static constexpr uint32_t oApart = oPow + (2 * C + 4) * 4;    // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
-  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 8) * 8 + 8;
+  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 10) * 8 + 8;
   // TMEM columns.  D = 64: U takes the half of P that the bf16 scores leave free, so that two
   // CTAs share an SM's 512 columns.
   static constexpr bool kShareU = D == 64;
@@ -196,6 +201,12 @@ __device__ __forceinline__ float top(float a) { return __uint_as_float(__float_a
 __device__ __forceinline__ uint32_t top2(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
+__device__ __forceinline__ void tma_store_4d(const void* map, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 }  // namespace tc
 
@@ -217,8 +228,10 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_u = bar_qk + 4;              // their products are in U
   uint64_t* bar_s = bar_qk + 5;              // S is in shared memory, U of the last chunk is read
   uint64_t* bar_z = bar_qk + 6;              // padding rows of y and z are zeros (once a sequence)
-  uint64_t* bar_end = bar_qk + 7;            // every MMA issued is done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 8) * 8);
+  uint64_t* bar_out = bar_qk + 7;            // the outputs are in shared memory
+  uint64_t* bar_sent = bar_qk + 8;           // and have been read there
+  uint64_t* bar_end = bar_qk + 9;            // every MMA issued is done
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 10) * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int job = blockIdx.y;
@@ -233,7 +246,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   auto first = [&](int it) { return (rev ? rn.chunks - 1 - (i0 + it) : i0 + it) * C; };
   auto count = [&](int t0) { return min(C, rn.len - t0); };
   // terms of Yd in step it's chunk; rows of y in a step
-  auto terms_of = [&](int it) { return jb.s_out && dc.pow(rn.len - rn.done(i0 + it + 1)) >= 0.0625f ? 3 : 2; };
+  const int near = !jb.s_out ? -1 : dc.ld < 0.f ? (int)fminf(-2.7725887f / dc.ld, 1e9f) : 0x7fffffff;   // ln 16
+  auto terms_of = [&](int it) { return (long long)(rn.chunks - 1 - i0 - it) * C <= near ? 3 : 2; };
   auto rows_of = [&](int terms) { return terms == 3 ? C / 2 : C; };
   // K-steps of 16 tokens with tokens in them; whether the last has padding of this sequence
   auto ksteps = [&](int n) { return (n + 15) / 16; };
@@ -251,6 +265,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     tc::bar_init(bar_u, 1);
     tc::bar_init(bar_s, WB);
     tc::bar_init(bar_z, WA);
+    tc::bar_init(bar_out, WA);
+    tc::bar_init(bar_sent, 1);
     tc::bar_init(bar_end, 1);
     tc::bar_fence_init();
   }
@@ -421,7 +437,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     const int i = (warp & 3) * 32 + lane, part = warp >> 2;  // token of the chunk, part of the columns
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
-    const bool wide = (reinterpret_cast<uintptr_t>(jb.out) & 31) == 0;
     int step = 0;
     for (int it = 0; it < nch && ok; ++it) {
       const int t0 = first(it), n = count(t0), ks = ksteps(n), krows = ks * 16;
@@ -519,47 +534,45 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         __syncwarp();
         if (lane == 0) tc::bar_arrive(bar_y);
         if (!full || r0 > 0) continue;
-        // the outputs: a row's 32-byte sectors from its own thread.  (Through shared memory and
-        // TMA the store waits behind the ring's loads: 2500 cycles at d = 128.)
+        // the outputs, as a tile that B sends by TMA (an SM's own stores leave at about 20 bytes a
+        // cycle, which held A for 1500 cycles a chunk at d = 128); padding rows are zeros
         const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
         const uint64_t g2 = tc::pack2(g, g);
-        __nv_bfloat16* dst = out + (size_t)(t0 + i) * p.H * D;
         if (!wait(bar_o, it)) break;
 #pragma unroll 1
         for (int c = part * CO; c < (part + 1) * CO; c += G) {
-          uint32_t a[G], e[G], o[G / 2];
+          uint32_t a[G], e[G];
           tc::lda(lanes + S::cO1 + c, a);
           tc::lda(lanes + S::cO2 + c, e);
           tc::wait_ld(a, e);
 #pragma unroll
-          for (int k = 0; k < G; k += 2) {
-            float x, y;
-            tc::unpack2(tc::fma2(g2, tc::pack2(__uint_as_float(e[k]), __uint_as_float(e[k + 1])),
-                                 tc::pack2(__uint_as_float(a[k]), __uint_as_float(a[k + 1]))),
-                        x, y);
-            o[k / 2] = tc::bf2(x, y);
-          }
-          if (i >= n) continue;
-          if (G >= 16 && wide) {
+          for (int k = 0; k < G; k += 8) {
+            uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < G / 2; k += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + c + 2 * k), "r"(o[k % (G / 2)]),
-                           "r"(o[(k + 1) % (G / 2)]), "r"(o[(k + 2) % (G / 2)]), "r"(o[(k + 3) % (G / 2)]),
-                           "r"(o[(k + 4) % (G / 2)]), "r"(o[(k + 5) % (G / 2)]), "r"(o[(k + 6) % (G / 2)]),
-                           "r"(o[(k + 7) % (G / 2)])
-                           : "memory");
-          } else {
-#pragma unroll
-            for (int k = 0; k < G / 2; k += 4)
-              *reinterpret_cast<uint4*>(dst + c + 2 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int q = 0; q < 4; ++q) {
+              const int j = k + 2 * q;
+              float x, y;
+              tc::unpack2(tc::fma2(g2, tc::pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
+                                   tc::pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
+                          x, y);
+              o[q] = tc::bf2(x, y);
+            }
+            const uint32_t off = (uint32_t)((c + k) / 64) * S::kBox + i * S::RB + (c + k) % 64 * 2;
+            *reinterpret_cast<uint4*>(sm + S::oOut + (off ^ ((off >> 3) & (S::RB - 16)))) =
+                i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
           }
         }
+        tc::fence_smem_to_async();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar_out);
       }
     }
     if (full) {
-      // padding: zeros, shared out over the runs
-      for (long long k = (long long)seg * (WA * 32) + tid; k < (long long)(p.T - rn.len) * (D / 8); k += p.nseg * (WA * 32))
-        *reinterpret_cast<uint4*>(out + (size_t)(rn.len + k / (D / 8)) * p.H * D + k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      // chunks of padding: zeros, shared out over the runs
+      const int from = min(rn.chunks * C, p.T);
+      for (long long k = (long long)seg * (WA * 32) + tid; k < (long long)(p.T - from) * (D / 8); k += p.nseg * (WA * 32))
+        *reinterpret_cast<uint4*>(out + (size_t)(from + k / (D / 8)) * p.H * D + k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     }
   } else {
     // ---- B: the state ----
@@ -601,6 +614,15 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       tc::fence_before();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(bar_s);
+      if (full && wb == 0) {                                 // send this chunk's outputs
+        if (!wait(bar_out, it)) break;
+        if (lane == 0) {
+          for (uint32_t x = 0; x < S::NB; ++x)
+            tc::tma_store_4d(&args.out[job], sm + S::oOut + x * S::kBox, x * 64, h, first(it), b);
+          tc::bulk_commit();
+        }
+        __syncwarp();
+      }
       const int n = count(first(it)), krows = ksteps(n) * 16, rows = rows_of(terms_of(it));
       for (int r0 = 0; r0 < krows; r0 += rows, ++step)
         if (!wait(bar_u, step)) break;
@@ -620,8 +642,18 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           tc::unpack2(tc::fma2(lx, s2, v), st[c + k], st[c + k + 1]);
         }
       }
-      if (full && !wait(bar_o, it)) break;                   // O2 has read S
+      if (full) {                                            // O2 has read S; the outputs are read
+        if (wb == 0) {
+          if (lane == 0) {
+            tc::bulk_wait_read();
+            tc::bar_arrive(bar_sent);
+          }
+          __syncwarp();
+        }
+        if (!wait(S::kOutS ? bar_sent : bar_o, it)) break;
+      }
     }
+    if (full && wb == 0 && lane == 0) tc::bulk_wait_all();
     float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D
                  : seg == p.nseg - 1 && jb.s_out ? jb.s_out + (size_t)bh * D * D : nullptr;
     if (dst && mine) {
