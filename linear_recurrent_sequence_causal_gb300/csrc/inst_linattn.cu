@@ -17,11 +17,11 @@ cudaError_t launch_fma_t(const LinattnArgs& a, cudaStream_t s) {
   const unsigned bh = (unsigned)(a.B * a.H * S::NSL);
   if (a.nseg > 1) {
     p.phase = 1;
-    fn<<<dim3(bh * (a.nseg - 1), a.njobs), S::NT, S::bytes, s>>>(p);
+    fn<<<bh * (a.nseg - 1) * a.njobs, S::NT, S::bytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   p.phase = 0;
-  fn<<<dim3(bh * a.nseg, a.njobs), S::NT, S::bytes, s>>>(p);
+  fn<<<bh * a.nseg * a.njobs, S::NT, S::bytes, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -19,7 +19,8 @@
 // chunks.  A first launch computes each run's own contribution D_r to the state (from zero),
 // and the full pass of run s starts from
 //   S_s = lambda^(done_s) S_0 + sum_{r<s} lambda^(done_s - done_(r+1)) D_r
-// with done_s the tokens processed before run s.  Every D_r is read from the workspace by
+// with done_s the tokens processed before run s.  Tokens that have decayed below 2^-126, fp32's
+// smallest normal number, by the end of their run add nothing to D_r and are not read for it.  Every D_r is read from the workspace by
 // the CTAs that need it, so no further launch joins them.
 #pragma once
 
@@ -73,6 +74,10 @@ struct Decay {
     l2 = ld * 1.4426950408889634f;
   }
   __device__ __forceinline__ float pow(int n) const { return exp2f((float)n * l2); }
+  // Chunks of C tokens, from the end (the last may be short), that still count for 2^-bits there.
+  __device__ __forceinline__ int reach(float bits, int C) const {
+    return l2 < 0.f ? 2 + (int)fminf(bits / (-l2 * C), 1e6f) : 0x7ffffff;
+  }
   // lambda^n in two terms, for the factor that the state meets once a chunk: a slow decay's
   // rounding error would be the same in every chunk and add up over the 1 / (1 - lambda^n)
   // chunks of its memory (4e-6 of the state at lambda = 1 - 2^-11 with one fp32 term).  Near 1,
@@ -127,7 +132,10 @@ __device__ __forceinline__ void linattn_start(float* st, const LinattnArgs& p, c
   if (jb.s_in) add(jb.s_in + (size_t)bh * D * D + (jb.in_t ? y * D + z : z * D + y), dc.pow(d), jb.in_t ? D : 1);
   const float* g = p.seg + ((size_t)job * p.B * p.H + bh) * (p.nseg - 1) * D * D + z * D + y;
 #pragma unroll 1
-  for (int r = 0; r < seg; ++r) add(g + (size_t)r * D * D, dc.pow(d - rn.done((r + 1) * p.seg_chunks)), 1);
+  for (int r = 0; r < seg; ++r) {
+    const float f = dc.pow(d - rn.done((r + 1) * p.seg_chunks));
+    if (f != 0.f) add(g + (size_t)r * D * D, f, 1);
+  }
 }
 
 // ---- fp32, on the CUDA cores ----
@@ -158,10 +166,10 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   constexpr int C = S::C, BZ = S::BZ, LD = S::LD, LZ = S::LZ, LP = S::LP;
   extern __shared__ __align__(16) float fma_sm[];
   float *sx = fma_sm, *sy = sx + C * LD, *sz = sy + C * LD, *sp = sz + C * LZ, *ss = sp + C * LP, *sw = ss + BZ * LD;
-  const int job = blockIdx.y;
+  const int job = blockIdx.x % p.njobs, item = blockIdx.x / p.njobs;
   const LinattnJob& jb = p.job[job];
   const int runs = p.phase == 1 ? p.nseg - 1 : p.nseg;
-  const int slice = blockIdx.x % S::NSL, seg = blockIdx.x / S::NSL % runs, bh = blockIdx.x / S::NSL / runs;
+  const int slice = item % S::NSL, seg = item / S::NSL % runs, bh = item / S::NSL / runs;
   const int b = bh / p.H, h = bh % p.H, z0 = slice * BZ, tid = threadIdx.x;
   const LinattnRuns rn(p, b, jb.rev, C);
   const Decay dc(__ldg(p.log_decay + h));
@@ -180,7 +188,8 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   const float* gy = static_cast<const float*>(jb.y) + b * jb.ys[0] + h * D;
   const float* gz = static_cast<const float*>(jb.z) + b * jb.zs[0] + h * D + z0;
   float* out = static_cast<float*>(jb.out) + ((size_t)b * p.T * p.H + h) * D + z0;
-  const int i0 = seg * p.seg_chunks, i1 = min(i0 + p.seg_chunks, rn.chunks);
+  const int i1 = min((seg + 1) * p.seg_chunks, rn.chunks);
+  const int i0 = full ? seg * p.seg_chunks : max(seg * p.seg_chunks, i1 - dc.reach(126.f, C));
   const int ti = tid / 16 * 2, tj = tid % 16;
   for (int it = i0; it < i1; ++it) {
     const int c = jb.rev ? rn.chunks - 1 - it : it, t0 = c * C, n = min(C, rn.len - t0);

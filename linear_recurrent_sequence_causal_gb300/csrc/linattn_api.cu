@@ -91,16 +91,17 @@ int check_linattn(const prism_linattn_dims* d) {
   if (d->dtype != PRISM_F32 && d->dtype != PRISM_BF16) return PRISM_ERR_INVALID_ARG;
   if (d->B <= 0 || d->T <= 0 || d->H <= 0 || d->d <= 0 || d->flags) return PRISM_ERR_INVALID_ARG;
   if (!good_head_dim(d->d)) return PRISM_ERR_UNSUPPORTED;
-  if ((long long)d->B * d->T > (1LL << 31) - 1 || (long long)d->B * d->H > (1LL << 24)) return PRISM_ERR_UNSUPPORTED;
+  if ((long long)d->B * d->T > (1LL << 31) - 1 || (long long)d->B * d->H > (1LL << 22)) return PRISM_ERR_UNSUPPORTED;
   return PRISM_OK;
 }
 
 // Runs that each sequence is cut into.  The CTAs of a launch take ceil(CTAs / resident) turns of
 // their run's chunks; cutting adds a first launch over the runs' states (all but the last run)
-// whose chunks cost about kStateChunk of a full one, and each CTA about kStart chunks of setting
-// up.  The cheapest count wins; runs keep at least two chunks.
+// whose chunks cost about kStateChunk of a full one, each CTA about kStart chunks of setting up,
+// and a run reads the states of all before it, kJoin chunks each.  The cheapest count wins; runs
+// keep at least two chunks.
 constexpr int kSMs = 152;
-constexpr double kStateChunk = 0.6, kStart = 1.5;
+constexpr double kStateChunk = 0.4, kStart = 1.5, kJoin = 0.2;
 void plan_runs(const prism_linattn_dims* d, int njobs, prism::LinattnArgs& a) {
   const bool tc = d->dtype == PRISM_BF16;
   const int C = tc ? 128 : 32, slices = !tc && d->d > 32 ? d->d / 32 : 1;
@@ -110,7 +111,7 @@ void plan_runs(const prism_linattn_dims* d, int njobs, prism::LinattnArgs& a) {
   double least = 0.;
   for (int n = 1; n <= prism::kLinattnMaxSeg && n <= (chunks + 1) / 2; ++n) {
     const int per = (chunks + n - 1) / n;
-    const double turns = (double)((ctas * n + resident - 1) / resident) * (per + kStart);
+    const double turns = (double)((ctas * n + resident - 1) / resident) * (per + kStart + kJoin * (n - 1));
     const double states = n == 1 ? 0. : (double)((ctas * (n - 1) + resident - 1) / resident) * (kStateChunk * per + kStart);
     if (n == 1 || turns + states < least) {
       least = turns + states;

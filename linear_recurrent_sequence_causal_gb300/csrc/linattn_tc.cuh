@@ -5,10 +5,10 @@
 //   O2 = X S^T                      M 128             N D               K D
 //   U  = Z^T Yd                     M D (rows of S)   N D               K 128, once a term of Yd
 // out_i = O1_i + so lambda^e(i) O2_i in fp32 and S <- lambda^n S + U in fp32 registers; S enters
-// O2 rounded to bf16 once.  Yd_j = su lambda^f(j) y_j is split into bf16 terms, each holding what
-// the ones before cut off: two (16 bits) where the state only feeds outputs, which the
+// O2 rounded to bf16 once.  Yd_j = su lambda^f(j) y_j is split into bf16 terms, each rounding what
+// the ones before left: two (16 bits) where the state only feeds outputs, which the
 // roundings of S and of the scores bound anyway; three (24 bits) where the caller gets the
-// state and it still remembers the chunk (lambda^rest >= 1/16, rest the tokens that follow).
+// state and it still remembers the chunk (by more than a quarter, lambda^rest >= 1/4).
 // Three terms go in two steps of 64 tokens, so that they need no more shared memory.
 //
 // Roles.  The last warp copies the x, y and z tiles by TMA into a ring of five slots; the one
@@ -56,7 +56,7 @@ struct LinattnTc {
   static constexpr uint32_t oPow = oRing + SLOTS * kTile + (kOutS ? 0 : kTile);   // lambda^k at k + C, 0 for k < 0
   static constexpr uint32_t oApart = oPow + (2 * C + 4) * 4;    // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
-  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 10) * 8 + 8;
+  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 15) * 8 + 8;
   // TMEM columns.  D = 64: U takes the half of P that the bf16 scores leave free, so that two
   // CTAs share an SM's 512 columns.
   static constexpr bool kShareU = D == 64;
@@ -196,11 +196,6 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {
   return u;
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-// the upper half of an fp32 value, as a bf16, and of two
-__device__ __forceinline__ float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
-__device__ __forceinline__ uint32_t top2(float a, float b) {
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
 __device__ __forceinline__ void tma_store_4d(const void* map, const void* src, int c0, int c1, int c2, int c3) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -208,6 +203,11 @@ __device__ __forceinline__ void tma_store_4d(const void* map, const void* src, i
                : "memory");
 }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t round2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return bf2(a, b);
+}
 }  // namespace tc
 
 template <int D>
@@ -224,30 +224,35 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_qk = bar_empty + SLOTS;      // P is there
   uint64_t* bar_p = bar_qk + 1;              // its bf16 scores are, and O of the last chunk is read
   uint64_t* bar_o = bar_qk + 2;              // O1 and O2 are there
-  uint64_t* bar_y = bar_qk + 3;              // a step's terms of Yd are in shared memory
-  uint64_t* bar_u = bar_qk + 4;              // their products are in U
-  uint64_t* bar_s = bar_qk + 5;              // S is in shared memory, U of the last chunk is read
-  uint64_t* bar_z = bar_qk + 6;              // padding rows of y and z are zeros (once a sequence)
-  uint64_t* bar_out = bar_qk + 7;            // the outputs are in shared memory
-  uint64_t* bar_sent = bar_qk + 8;           // and have been read there
-  uint64_t* bar_end = bar_qk + 9;            // every MMA issued is done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 10) * 8);
+  uint64_t* bar_z = bar_qk + 3;              // padding rows of y and z are zeros (once a sequence)
+  uint64_t* bar_out = bar_qk + 4;            // the outputs are in shared memory
+  uint64_t* bar_sent = bar_qk + 5;           // and have been read there
+  uint64_t* bar_end = bar_qk + 6;            // every MMA issued is done
+  // two each, used in turn, so that a role that is a chunk behind still tells the phases apart
+  uint64_t* bar_t = bar_qk + 7;              // [2] a step's terms are in U
+  uint64_t* bar_u = bar_qk + 9;              // [2] a chunk's U is there
+  uint64_t* bar_y = bar_qk + 11;             // [2] a step's terms of Yd are in shared memory
+  uint64_t* bar_s = bar_qk + 13;             // [2] S is in shared memory, U of the last chunk is read
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 15) * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int job = blockIdx.y;
+  const int job = blockIdx.x % p.njobs, item = blockIdx.x / p.njobs;   // a head's passes share its tiles in L2
   const LinattnJob& jb = p.job[job];
   const bool full = p.phase == 0, rev = jb.rev != 0;
   const int runs = full ? p.nseg : p.nseg - 1;
-  const int seg = blockIdx.x % runs, bh = blockIdx.x / runs, b = bh / p.H, h = bh % p.H;
+  const int seg = item % runs, bh = item / runs, b = bh / p.H, h = bh % p.H;
   const LinattnRuns rn(p, b, jb.rev, C);
-  const int i0 = seg * p.seg_chunks, nch = max(min(i0 + p.seg_chunks, rn.chunks) - i0, 0);
   const Decay dc(__ldg(p.log_decay + h));
+  // a run's own state starts where lambda^rest is above fp32's smallest number
+  const int i1 = min((seg + 1) * p.seg_chunks, rn.chunks);
+  const int i0 = full ? seg * p.seg_chunks : max(seg * p.seg_chunks, i1 - dc.reach(126.f, C));
+  const int nch = max(i1 - i0, 0);
   // chunk of step it: its first token and how many are there
   auto first = [&](int it) { return (rev ? rn.chunks - 1 - (i0 + it) : i0 + it) * C; };
   auto count = [&](int t0) { return min(C, rn.len - t0); };
   // terms of Yd in step it's chunk; rows of y in a step
-  const int near = !jb.s_out ? -1 : dc.ld < 0.f ? (int)fminf(-2.7725887f / dc.ld, 1e9f) : 0x7fffffff;   // ln 16
-  auto terms_of = [&](int it) { return (long long)(rn.chunks - 1 - i0 - it) * C <= near ? 3 : 2; };
+  const int near = jb.s_out ? dc.reach(2.f, C) : 0;
+  auto terms_of = [&](int it) { return rn.chunks - (i0 + it) <= near ? 3 : 2; };
   auto rows_of = [&](int terms) { return terms == 3 ? C / 2 : C; };
   // K-steps of 16 tokens with tokens in them; whether the last has padding of this sequence
   auto ksteps = [&](int n) { return (n + 15) / 16; };
@@ -261,9 +266,12 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     tc::bar_init(bar_qk, 1);
     tc::bar_init(bar_p, WA);
     tc::bar_init(bar_o, 1);
-    tc::bar_init(bar_y, WA);
-    tc::bar_init(bar_u, 1);
-    tc::bar_init(bar_s, WB);
+    for (int i = 0; i < 2; ++i) {
+      tc::bar_init(bar_t + i, 1);
+      tc::bar_init(bar_y + i, WA);
+      tc::bar_init(bar_u + i, 1);
+      tc::bar_init(bar_s + i, WB);
+    }
     tc::bar_init(bar_z, WA);
     tc::bar_init(bar_out, WA);
     tc::bar_init(bar_sent, 1);
@@ -315,8 +323,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const int len = __shfl_sync(0xffffffffu, rn.len, 0), chunks = (len + C - 1) / C;
-      const int steps = max(min(i0 + p.seg_chunks, chunks) - i0, 0);
-      auto first = [&](int it) { return (rev ? chunks - 1 - (i0 + it) : i0 + it) * C; };
+      const int steps = __shfl_sync(0xffffffffu, nch, 0), i0u = __shfl_sync(0xffffffffu, i0, 0);
+      auto first = [&](int it) { return (rev ? chunks - 1 - (i0u + it) : i0u + it) * C; };
       auto count = [&](int t0) { return min(C, len - t0); };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, tc::bar_wait_long(bar, parity & 1));
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         if (!wait(bar_full + tx % SLOTS, tx / SLOTS) || !wait(bar_full + ty % SLOTS, ty / SLOTS)) return;
         const int t0 = first(it);
         if (ragged(t0, count(t0)) && !wait(bar_z, 0)) return;
-        if (S::kShareU && !wait(bar_s, it)) return;          // U of the last chunk is read
+        if (S::kShareU && !wait(bar_s + it % 2, it / 2)) return;          // U of the last chunk is read
         if (tc::elect()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             }
           }
           __syncwarp();
-          if (!wait(bar_s, it)) break;
+          if (!wait(bar_s + it % 2, it / 2)) break;
           if (tc::elect()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           }
           __syncwarp();
         } else {
-          if (it > 0 && !wait(bar_s, it)) break;             // U of the last chunk is read
+          if (it > 1 && !wait(bar_s + (it - 1) % 2, (it - 1) / 2)) break;         // the U that lay here before is read
           if (ragged(t0, n) && !wait(bar_z, 0)) break;
         }
         // the next chunk's scores before this one's U, if their tiles are there: A needs them
@@ -392,36 +400,40 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             scores();
         }
         const int terms = __shfl_sync(0xffffffffu, terms_of(it), 0), rows = rows_of(terms);
-        const uint32_t d_mid = tc::desc_lo(base + S::oMid, rows * S::RB);
+        const uint32_t d_mid = tc::desc_lo(base + S::oMid, rows * S::RB), d_out = tc::desc_lo(base + S::oOut, rows * S::RB);
         for (int r0 = 0; r0 < ks * 16; r0 += rows, ++step) {
-          if (!wait(bar_y, step)) break;
+          if (!wait(bar_y + step % 2, step / 2)) break;
           const uint32_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
           const int kn = min(ks - r0 / 16, rows / 16);
+          // alone, the states have two places for terms and for U, so that a chunk's split, its
+          // products and the last one's sum run at the same time
+          const uint32_t dm = !full && step % 2 == 1 ? d_out : d_mid, du = tm + (!full && it % 2 == 1 ? S::cO1 : S::cU);
           if (tc::elect()) {
 #pragma unroll 1
             for (int t = 0; t < terms; ++t) {
-              const uint32_t d = t == 0 ? dy : d_mid + (t - 1) * (S::kTile / 32);
+              const uint32_t d = t == 0 ? dy : dm + (t - 1) * (S::kTile / 32);
               if (kn == rows / 16) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  tc::mma_ss<S::RB>(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                  tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
                 if (kn == 8) {
 #pragma unroll
                   for (int kk = 4; kk < 8; ++kk)
-                    tc::mma_ss<S::RB>(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, true);
+                    tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, true);
                 }
               } else {
 #pragma unroll 1
                 for (int kk = 0; kk < kn; ++kk)
-                  tc::mma_ss<S::RB>(tm + S::cU, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                  tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
               }
             }
-            tc::commit(bar_u);
+            tc::commit(bar_t + step % 2);
           }
           __syncwarp();
         }
         if (!ok) break;
         if (tc::elect()) {
+          tc::commit(bar_u + it % 2);
           tc::commit(bar_empty + ty % SLOTS);
           tc::commit(bar_empty + tz % SLOTS);
         }
@@ -485,14 +497,16 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       const int terms = terms_of(it), rows = rows_of(terms);
 #pragma unroll 1
       for (int r0 = 0; r0 < krows; r0 += rows, ++step) {
-        if (step > 0 && !wait(bar_u, step - 1)) break;       // the last step's terms are read
+        // the terms that lay here before are read
+        const int back = full ? 1 : 2;
+        if (step >= back && !wait(bar_t + (step - back) % 2, (step - back) / 2)) break;
         // 16-byte pieces of the rows of this step, box by box.  Rows past n hold zeros, or are in
         // no K-step.
         constexpr int RI = WA * 32 * 16 / S::RB;             // rows that A takes at once
         const int r1 = r0 + tid / (S::RB / 16);
         const float* wp = pw + (rev ? r1 + 1 : n - 1 - r1);
         unsigned char* y = ys + r0 * S::RB + tid * 16;
-        unsigned char* m = sm + S::oMid + tid * 16;
+        unsigned char* m = sm + (full || step % 2 == 0 ? S::oMid : S::oOut) + tid * 16;
 #pragma unroll 1
         for (uint32_t box = 0; box < S::NB; ++box, y += S::kBox, m += rows * S::RB) {
 #pragma unroll 2
@@ -506,24 +520,17 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             uint64_t left[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // each term takes the upper half of the fp32 value, the next what that cuts off
               const uint64_t v = tc::mul2(tc::pack2(tc::bf_lo(in[e]), tc::bf_hi(in[e])), w2);
-              float a, c;
-              tc::unpack2(v, a, c);
-              hi[e] = tc::top2(a, c);
-              left[e] = tc::fma2(tc::pack2(tc::top(a), tc::top(c)), minus, v);
-              tc::unpack2(left[e], a, c);
-              mid[e] = tc::top2(a, c);
+              hi[e] = tc::round2(v);
+              left[e] = tc::fma2(tc::pack2(tc::bf_lo(hi[e]), tc::bf_hi(hi[e])), minus, v);
+              mid[e] = tc::round2(left[e]);
             }
             *reinterpret_cast<uint4*>(y + r * S::RB) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(m + r * S::RB) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
             if (terms == 3) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float a, c;
-                tc::unpack2(left[e], a, c);
-                tc::unpack2(tc::fma2(tc::pack2(tc::top(a), tc::top(c)), minus, left[e]), a, c);
-                lo[e] = tc::top2(a, c);
+                lo[e] = tc::round2(tc::fma2(tc::pack2(tc::bf_lo(mid[e]), tc::bf_hi(mid[e])), minus, left[e]));
               }
               *reinterpret_cast<uint4*>(m + S::kTile / 2 + r * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         tc::fence_smem_to_async();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(bar_y);
+        if (lane == 0) tc::bar_arrive(bar_y + step % 2);
         if (!full || r0 > 0) continue;
         // the outputs, as a tile that B sends by TMA (an SM's own stores leave at about 20 bytes a
         // cycle, which held A for 1500 cycles a chunk at d = 128); padding rows are zeros
@@ -590,7 +597,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       for (int c = 0; c < NS; ++c) st[c] = 0.f;
     }
     const float2 whole = dc.step(C);
-    int step = 0;
 #pragma unroll 1
     for (int it = 0; it < nch; ++it) {
       // hand the state over: bf16 rows of S, K-major; U of the last chunk is read
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::bar_arrive(bar_s);
+      if (lane == 0) tc::bar_arrive(bar_s + it % 2);
       if (full && wb == 0) {                                 // send this chunk's outputs
         if (!wait(bar_out, it)) break;
         if (lane == 0) {
@@ -623,17 +629,15 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         }
         __syncwarp();
       }
-      const int n = count(first(it)), krows = ksteps(n) * 16, rows = rows_of(terms_of(it));
-      for (int r0 = 0; r0 < krows; r0 += rows, ++step)
-        if (!wait(bar_u, step)) break;
-      if (!ok) break;
+      const int n = count(first(it));
+      if (!wait(bar_u + it % 2, it / 2)) break;
       const float2 ln = n == C ? whole : dc.step(n);
       const uint64_t lx = tc::pack2(ln.x, ln.x), ly = tc::pack2(ln.y, ln.y);
       constexpr int G = NS >= 16 ? 16 : NS;
 #pragma unroll
       for (int c = 0; c < NS; c += G) {
         uint32_t u[G];
-        tc::lda(lanes + S::cU + y0 + c, u);
+        tc::lda(lanes + (!full && it % 2 == 1 ? S::cO1 : S::cU) + y0 + c, u);
         tc::wait_ld(u);
 #pragma unroll
         for (int k = 0; k < G; k += 2) {
@@ -685,11 +689,11 @@ cudaError_t launch_linattn_tc_t(const LinattnTcArgs& a, cudaStream_t s) {
   const unsigned bh = (unsigned)(a.a.B * a.a.H);
   if (a.a.nseg > 1) {
     p.a.phase = 1;
-    fn<<<dim3(bh * (a.a.nseg - 1), a.a.njobs), S::NT, S::bytes, s>>>(p);
+    fn<<<bh * (a.a.nseg - 1) * a.a.njobs, S::NT, S::bytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   p.a.phase = 0;
-  fn<<<dim3(bh * a.a.nseg, a.a.njobs), S::NT, S::bytes, s>>>(p);
+  fn<<<bh * a.a.nseg * a.a.njobs, S::NT, S::bytes, s>>>(p);
   return cudaGetLastError();
 }
 
