@@ -6,13 +6,13 @@
 
 namespace prism {
 
-static long long rope_blocks(const RopeArgs& a, int side) {
-  return (long long)a.B * a.T * ((a.side[side].heads + kRopeRows - 1) / kRopeRows);
+static long long rope_blocks(const RopeArgs& a, int side, int rows) {
+  return (long long)a.B * a.T * ((a.side[side].heads + rows - 1) / rows);
 }
 
 template <class E, int D>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
-  const long long bq = rope_blocks(a, 0), n = bq + rope_blocks(a, 1);
+  const long long bq = rope_blocks(a, 0, kRopeRows), n = bq + rope_blocks(a, 1, kRopeRows);
   const long long grid = (n + kRopeThreads / (D / 8) - 1) / (kRopeThreads / (D / 8));
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (a.interleaved)
@@ -24,10 +24,12 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
 
 template <class E, int D>
 cudaError_t launch_rope_backward_t(const RopeArgs& a, cudaStream_t s) {
-  const long long bq = rope_blocks(a, 0), bk = rope_blocks(a, 1);
+  const long long bq = rope_blocks(a, 0, kRopeBackRows<E>), bk = rope_blocks(a, 1, kRopeBackRows<E>);
   const int ng = kRopeThreads / (D / 8);
+  static_assert(152 * kRopeBackCtas <= kRopeMaxCtas, "the workspace has a row for each CTA");
   long long grid = ((bq > bk ? bq : bk) + ng - 1) / ng;
-  if (grid > kRopeMaxCtas) grid = kRopeMaxCtas;
+  const int most = 152 * kRopeBackCtas;       // resident at once
+  if (grid > most) grid = most;
   if (a.interleaved)
     rope_backward_kernel<E, D, true><<<(unsigned)grid, kRopeThreads, 0, s>>>(a, bq, bk);
   else
@@ -37,7 +39,7 @@ cudaError_t launch_rope_backward_t(const RopeArgs& a, cudaStream_t s) {
   // launched while the first kernel drains; it waits for it before it reads
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

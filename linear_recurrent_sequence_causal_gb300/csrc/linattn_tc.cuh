@@ -112,25 +112,6 @@ __device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
                : "memory");
   return ok;
 }
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // True in one lane of a converged warp, always the same.  A branch on it (and not on a lane
 // number) in a warp whose number and loop counts the compiler knows to be the same in every
 // lane lets the operands of the MMAs inside stay in uniform registers; moved there one by one
@@ -514,15 +495,15 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             if (RI > 64 && r1 - r0 + r >= rows) continue;    // D = 16, 32: a step has fewer rows than A takes
             const uint4 u = *reinterpret_cast<const uint4*>(y + r * S::RB);
             const float w = jb.su * wp[rev ? r : -r];
-            const uint64_t w2 = tc::pack2(w, w), minus = tc::pack2(-1.f, -1.f);
+            const uint64_t w2 = pack2(w, w), minus = pack2(-1.f, -1.f);
             const uint32_t in[4] = {u.x, u.y, u.z, u.w};
             uint32_t hi[4], mid[4], lo[4];
             uint64_t left[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint64_t v = tc::mul2(tc::pack2(tc::bf_lo(in[e]), tc::bf_hi(in[e])), w2);
+              const uint64_t v = mul2(pack2(tc::bf_lo(in[e]), tc::bf_hi(in[e])), w2);
               hi[e] = tc::round2(v);
-              left[e] = tc::fma2(tc::pack2(tc::bf_lo(hi[e]), tc::bf_hi(hi[e])), minus, v);
+              left[e] = fma2(pack2(tc::bf_lo(hi[e]), tc::bf_hi(hi[e])), minus, v);
               mid[e] = tc::round2(left[e]);
             }
             *reinterpret_cast<uint4*>(y + r * S::RB) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -530,7 +511,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             if (terms == 3) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                lo[e] = tc::round2(tc::fma2(tc::pack2(tc::bf_lo(mid[e]), tc::bf_hi(mid[e])), minus, left[e]));
+                lo[e] = tc::round2(fma2(pack2(tc::bf_lo(mid[e]), tc::bf_hi(mid[e])), minus, left[e]));
               }
               *reinterpret_cast<uint4*>(m + S::kTile / 2 + r * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
@@ -544,7 +525,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         // the outputs, as a tile that B sends by TMA (an SM's own stores leave at about 20 bytes a
         // cycle, which held A for 1500 cycles a chunk at d = 128); padding rows are zeros
         const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
-        const uint64_t g2 = tc::pack2(g, g);
+        const uint64_t g2 = pack2(g, g);
         if (!wait(bar_o, it)) break;
 #pragma unroll 1
         for (int c = part * CO; c < (part + 1) * CO; c += G) {
@@ -559,8 +540,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             for (int q = 0; q < 4; ++q) {
               const int j = k + 2 * q;
               float x, y;
-              tc::unpack2(tc::fma2(g2, tc::pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
-                                   tc::pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
+              unpack2(fma2(g2, pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
+                                   pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
                           x, y);
               o[q] = tc::bf2(x, y);
             }
@@ -632,7 +613,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       const int n = count(first(it));
       if (!wait(bar_u + it % 2, it / 2)) break;
       const float2 ln = n == C ? whole : dc.step(n);
-      const uint64_t lx = tc::pack2(ln.x, ln.x), ly = tc::pack2(ln.y, ln.y);
+      const uint64_t lx = pack2(ln.x, ln.x), ly = pack2(ln.y, ln.y);
       constexpr int G = NS >= 16 ? 16 : NS;
 #pragma unroll
       for (int c = 0; c < NS; c += G) {
@@ -641,9 +622,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         tc::wait_ld(u);
 #pragma unroll
         for (int k = 0; k < G; k += 2) {
-          const uint64_t s2 = tc::pack2(st[c + k], st[c + k + 1]);
-          const uint64_t v = tc::fma2(ly, s2, tc::pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
-          tc::unpack2(tc::fma2(lx, s2, v), st[c + k], st[c + k + 1]);
+          const uint64_t s2 = pack2(st[c + k], st[c + k + 1]);
+          const uint64_t v = fma2(ly, s2, pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
+          unpack2(fma2(lx, s2, v), st[c + k], st[c + k + 1]);
         }
       }
       if (full) {                                            // O2 has read S; the outputs are read
