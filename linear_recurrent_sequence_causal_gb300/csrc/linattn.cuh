@@ -40,7 +40,7 @@ struct LinattnJob {
   int in_t, out_t;                        // the state in memory is [d_y][d_z]
 };
 
-constexpr int kLinattnMaxSeg = 16;
+constexpr int kLinattnMaxSeg = 64;
 
 struct LinattnArgs {
   LinattnJob job[3];

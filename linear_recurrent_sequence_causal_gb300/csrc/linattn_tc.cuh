@@ -268,6 +268,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  // the full passes' launch may start setting up on SMs that this one leaves free
+  if (!full) asm volatile("griddepcontrol.launch_dependents;\n");
   const uint32_t tmem = *tslot;
   const uint32_t base = tc::smem_addr(sm);
   bool ok = true;
@@ -572,71 +574,78 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     const bool mine = D >= 32 || lane < D;                   // D = 16: lanes 16.. repeat
     float st[NS];
     if (full) {
+      if (p.nseg > 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the runs' states are written
       linattn_start<D, NS>(st, p, jb, job, bh, seg, rn, dc, row, y0);
     } else {
 #pragma unroll
       for (int c = 0; c < NS; ++c) st[c] = 0.f;
     }
     const float2 whole = dc.step(C);
+    // step -1 hands the first state over; step it adds its chunk's U and hands the next one over
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
-      // hand the state over: bf16 rows of S, K-major; U of the last chunk is read
-      if (full && mine) {
-        if constexpr (NS >= 8) {
-#pragma unroll
-          for (int c = 0; c < NS; c += 8) {
-            const int q = (y0 + c) / 8;                      // 16-byte piece of the row
-            const uint32_t off = (uint32_t)(q / 8) * S::kSBox + row * S::RB + (q % 8) * 16;
-            *reinterpret_cast<uint4*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
-                make_uint4(tc::bf2(st[c], st[c + 1]), tc::bf2(st[c + 2], st[c + 3]), tc::bf2(st[c + 4], st[c + 5]),
-                           tc::bf2(st[c + 6], st[c + 7]));
-          }
-        } else {
-          const uint32_t off = row * S::RB + y0 * 2;
-          *reinterpret_cast<uint2*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
-              make_uint2(tc::bf2(st[0], st[1]), tc::bf2(st[2], st[3]));
-        }
-        tc::fence_smem_to_async();
-      }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(bar_s + it % 2);
-      if (full && wb == 0) {                                 // send this chunk's outputs
-        if (!wait(bar_out, it)) break;
-        if (lane == 0) {
-          for (uint32_t x = 0; x < S::NB; ++x)
-            tc::tma_store_4d(&args.out[job], sm + S::oOut + x * S::kBox, x * 64, h, first(it), b);
-          tc::bulk_commit();
-        }
-        __syncwarp();
-      }
-      const int n = count(first(it));
-      if (!wait(bar_u + it % 2, it / 2)) break;
-      const float2 ln = n == C ? whole : dc.step(n);
-      const uint64_t lx = pack2(ln.x, ln.x), ly = pack2(ln.y, ln.y);
-      constexpr int G = NS >= 16 ? 16 : NS;
-#pragma unroll
-      for (int c = 0; c < NS; c += G) {
-        uint32_t u[G];
-        tc::lda(lanes + (!full && it % 2 == 1 ? S::cO1 : S::cU) + y0 + c, u);
-        tc::wait_ld(u);
-#pragma unroll
-        for (int k = 0; k < G; k += 2) {
-          const uint64_t s2 = pack2(st[c + k], st[c + k + 1]);
-          const uint64_t v = fma2(ly, s2, pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
-          unpack2(fma2(lx, s2, v), st[c + k], st[c + k + 1]);
-        }
-      }
-      if (full) {                                            // O2 has read S; the outputs are read
-        if (wb == 0) {
+    for (int it = -1; it < nch; ++it) {
+      float2 ln = make_float2(1.f, 0.f);
+      if (it >= 0) {
+        if (full && wb == 0) {                               // send this chunk's outputs
+          if (!wait(bar_out, it)) break;
           if (lane == 0) {
-            tc::bulk_wait_read();
-            tc::bar_arrive(bar_sent);
+            for (uint32_t x = 0; x < S::NB; ++x)
+              tc::tma_store_4d(&args.out[job], sm + S::oOut + x * S::kBox, x * 64, h, first(it), b);
+            tc::bulk_commit();
           }
           __syncwarp();
         }
-        if (!wait(S::kOutS ? bar_sent : bar_o, it)) break;
+        const int n = count(first(it));
+        ln = n == C ? whole : dc.step(n);
+        if (!wait(bar_u + it % 2, it / 2)) break;
+        if (full) {                                          // O2 has read S; the outputs are read
+          if (wb == 0) {
+            if (lane == 0) {
+              tc::bulk_wait_read();
+              tc::bar_arrive(bar_sent);
+            }
+            __syncwarp();
+          }
+          if (!wait(S::kOutS ? bar_sent : bar_o, it)) break;
+        }
       }
+      const uint64_t lx = pack2(ln.x, ln.x), ly = pack2(ln.y, ln.y);
+      const uint32_t at = lanes + (!full && (it & 1) ? S::cO1 : S::cU) + y0;
+      constexpr int G = NS >= 16 ? 16 : NS;
+#pragma unroll
+      for (int c = 0; c < NS; c += G) {
+        if (it >= 0) {
+          uint32_t u[G];
+          tc::lda(at + c, u);
+          tc::wait_ld(u);
+#pragma unroll
+          for (int k = 0; k < G; k += 2) {
+            const uint64_t s2 = pack2(st[c + k], st[c + k + 1]);
+            const uint64_t v = fma2(ly, s2, pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
+            unpack2(fma2(lx, s2, v), st[c + k], st[c + k + 1]);
+          }
+        }
+        if (full && mine) {                                  // bf16 rows of S, K-major
+          if constexpr (NS >= 8) {
+#pragma unroll
+            for (int k = c; k < c + G; k += 8) {
+              const int q = (y0 + k) / 8;                    // 16-byte piece of the row
+              const uint32_t off = (uint32_t)(q / 8) * S::kSBox + row * S::RB + (q % 8) * 16;
+              *reinterpret_cast<uint4*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
+                  make_uint4(tc::bf2(st[k], st[k + 1]), tc::bf2(st[k + 2], st[k + 3]), tc::bf2(st[k + 4], st[k + 5]),
+                             tc::bf2(st[k + 6], st[k + 7]));
+            }
+          } else {
+            const uint32_t off = row * S::RB + y0 * 2;
+            *reinterpret_cast<uint2*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
+                make_uint2(tc::bf2(st[0], st[1]), tc::bf2(st[2], st[3]));
+          }
+        }
+      }
+      if (full) tc::fence_smem_to_async();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(bar_s + ((it + 1) & 1));
     }
     if (full && wb == 0 && lane == 0) tc::bulk_wait_all();
     float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D
@@ -674,8 +683,21 @@ cudaError_t launch_linattn_tc_t(const LinattnTcArgs& a, cudaStream_t s) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   p.a.phase = 0;
-  fn<<<bh * a.a.nseg * a.a.njobs, S::NT, S::bytes, s>>>(p);
-  return cudaGetLastError();
+  if (a.a.nseg == 1) {
+    fn<<<bh * a.a.njobs, S::NT, S::bytes, s>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(bh * a.a.nseg * a.a.njobs);
+  cfg.blockDim = dim3(S::NT);
+  cfg.dynamicSmemBytes = S::bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 }  // namespace prism
