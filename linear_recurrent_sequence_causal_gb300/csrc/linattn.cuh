@@ -37,7 +37,7 @@ struct LinattnJob {
   float* s_out;                           // [B][H][D][D] or null
   float sp, su, so;
   int rev;                                // backwards
-  int in_t, out_t;                        // the state in memory is [d_y][d_z]
+  int in_t;                               // s_in is [d_y][d_z]
 };
 
 constexpr int kLinattnMaxSeg = 64;
@@ -300,13 +300,12 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D
                : seg == p.nseg - 1 && jb.s_out ? jb.s_out + (size_t)bh * D * D : nullptr;
   if (!dst) return;
-  const bool tr = full && jb.out_t;
 #pragma unroll
   for (int r = 0; r < RPT; ++r)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int z = z0 + zr + r, y = yc + q;
-      dst[tr ? y * D + z : z * D + y] = st[r][q];
+      dst[z * D + y] = st[r][q];
     }
 }
 

@@ -101,7 +101,7 @@ int check_linattn(const prism_linattn_dims* d) {
 // and a run reads the states of all before it, kJoin chunks each.  The cheapest count wins; runs
 // keep at least two chunks.
 constexpr int kSMs = 152;
-constexpr double kStateChunk = 0.4, kStart = 1.5, kJoin = 0.2;
+constexpr double kStateChunk = 0.4, kStart = 1.5, kJoin = 0.4;
 void plan_runs(const prism_linattn_dims* d, int njobs, prism::LinattnArgs& a) {
   const bool tc = d->dtype == PRISM_BF16;
   const int C = tc ? 128 : 32, slices = !tc && d->d > 32 ? d->d / 32 : 1;
@@ -203,7 +203,7 @@ int run_linattn(const prism_linattn_dims* d, prism::LinattnArgs& a, const Operan
 }
 
 prism::LinattnJob make_job(const Operand* in, int x, int y, int z, void* out, const float* s_in, int in_t,
-                           float* s_out, int out_t, float sp, float su, float so, int rev) {
+                           float* s_out, float sp, float su, float so, int rev) {
   prism::LinattnJob j;
   j.x = in[x].p; j.y = in[y].p; j.z = in[z].p;
   for (int i = 0; i < 2; ++i) {
@@ -213,7 +213,7 @@ prism::LinattnJob make_job(const Operand* in, int x, int y, int z, void* out, co
   }
   j.xi = x; j.yi = y; j.zi = z;
   j.out = out;
-  j.s_in = s_in; j.in_t = in_t; j.s_out = s_out; j.out_t = out_t;
+  j.s_in = s_in; j.in_t = in_t; j.s_out = s_out;
   j.sp = sp; j.su = su; j.so = so; j.rev = rev;
   return j;
 }
@@ -304,7 +304,7 @@ extern "C" PRISM_API int prism_linattn_forward(const prism_linattn_dims* dims, c
   prism::LinattnArgs a;
   plan_runs(dims, 1, a);
   const float c = dims->scale;
-  a.job[0] = make_job(in, 0, 1, 2, out, initial_state, 0, final_state, 0, c, 1.f, c, 0);
+  a.job[0] = make_job(in, 0, 1, 2, out, initial_state, 0, final_state, c, 1.f, c, 0);
   return run_linattn(dims, a, in, 3, log_decay, seq_lens, workspace, workspace_bytes, stream);
 }
 
@@ -328,9 +328,9 @@ extern "C" PRISM_API int prism_linattn_backward(const prism_linattn_dims* dims, 
   plan_runs(dims, 3, a);
   const float c = dims->scale;
   // the state of dq's pass is S^T [d_k][d_v], that of dv's H [d_v][d_k], that of dk's H^T
-  a.job[0] = make_job(in, 3, 2, 1, dq, initial_state, 1, nullptr, 0, c, 1.f, c, 0);
-  a.job[1] = make_job(in, 1, 0, 3, dv, d_final_state, 0, d_initial_state, 0, c, c, 1.f, 1);
-  a.job[2] = make_job(in, 2, 3, 0, dk, d_final_state, 1, nullptr, 0, c, c, 1.f, 1);
+  a.job[0] = make_job(in, 3, 2, 1, dq, initial_state, 1, nullptr, c, 1.f, c, 0);
+  a.job[1] = make_job(in, 1, 0, 3, dv, d_final_state, 0, d_initial_state, c, c, 1.f, 1);
+  a.job[2] = make_job(in, 2, 3, 0, dk, d_final_state, 1, nullptr, c, c, 1.f, 1);
   return run_linattn(dims, a, in, 4, log_decay, seq_lens, workspace, workspace_bytes, stream);
 }
 

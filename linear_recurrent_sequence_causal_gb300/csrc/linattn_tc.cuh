@@ -9,7 +9,7 @@
 // the ones before left: two (16 bits) where the state only feeds outputs, which the
 // roundings of S and of the scores bound anyway; three (24 bits) where the caller gets the
 // state and it still remembers the chunk (by more than a quarter, lambda^rest >= 1/4).
-// Three terms go in two steps of 64 tokens, so that they need no more shared memory.
+// Three terms go in two steps of 64 tokens at d >= 64, so that they need no more shared memory.
 //
 // Roles.  The last warp copies the x, y and z tiles by TMA into a ring of five slots; the one
 // before issues the MMAs; A turns P into bf16 scores in place in TMEM, splits y, and
@@ -41,19 +41,22 @@ struct LinattnTcArgs {
 
 template <int D_>
 struct LinattnTc {
-  static constexpr int D = D_, C = 128, SLOTS = D == 128 ? 5 : D == 64 ? 4 : 8;
+  static constexpr int D = D_, C = 128, SLOTS = D == 128 ? 5 : D == 64 ? 4 : 6;
   static constexpr int WA = 8, WB = D == 128 ? 8 : 4;           // warps of A and of B
   static constexpr int NT = (WA + WB + 2) * 32;
   static constexpr uint32_t RB = D >= 64 ? 128 : 2 * D;         // bytes of a tile row in one box
   static constexpr uint32_t NB = 2 * D / RB;                    // boxes of a tile
   static constexpr uint32_t kTile = C * 2 * D, kBox = C * RB;
+  // three terms: in two steps of half the rows, or in one with a tile for each further term
+  static constexpr int kRows3 = D >= 64 ? C / 2 : C;
+  static constexpr uint32_t kLo = kRows3 * 2 * D, kMid = D >= 64 ? kTile : 2 * kTile;
   static constexpr uint32_t kState = D * 2 * D, kSBox = D * RB;
-  static constexpr uint32_t oS = 0, oMid = (kState + 1023) & ~1023u, oRing = oMid + kTile;
+  static constexpr uint32_t oS = 0, oMid = (kState + 1023) & ~1023u, oRing = oMid + kMid;
   // outputs on their way out: at D = 128 in S's tile, which is as large and free from O2 to the
   // next state
   static constexpr bool kOutS = D == 128;
   static constexpr uint32_t oOut = kOutS ? oS : oRing + SLOTS * kTile;
-  static constexpr uint32_t oPow = oRing + SLOTS * kTile + (kOutS ? 0 : kTile);   // lambda^k at k + C, 0 for k < 0
+  static constexpr uint32_t oPow = oRing + SLOTS * kTile + (kOutS ? 0 : kMid);   // lambda^k at k + C, 0 for k < 0
   static constexpr uint32_t oApart = oPow + (2 * C + 4) * 4;    // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
   static constexpr uint32_t bytes = oBar + (2 * SLOTS + 15) * 8 + 8;
@@ -234,12 +237,14 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   // terms of Yd in step it's chunk; rows of y in a step
   const int near = jb.s_out ? dc.reach(2.f, C) : 0;
   auto terms_of = [&](int it) { return rn.chunks - (i0 + it) <= near ? 3 : 2; };
-  auto rows_of = [&](int terms) { return terms == 3 ? C / 2 : C; };
+  auto rows_of = [&](int terms) { return terms == 3 ? S::kRows3 : C; };
   // K-steps of 16 tokens with tokens in them; whether the last has padding of this sequence
   auto ksteps = [&](int n) { return (n + 15) / 16; };
   auto ragged = [&](int t0, int n) { return (n & 15) != 0 && t0 + n < p.T; };
 
-  if (tid == 0) {
+  // tiles a chunk: x, y, z (or y, z): the i-th tile of the run lies in slot i % SLOTS
+  const int per = full ? 3 : 2;
+  if (warp == WA + WB + 1 && lane == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       tc::bar_init(bar_full + i, 1);
       tc::bar_init(bar_empty + i, 1);
@@ -258,19 +263,27 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     tc::bar_init(bar_sent, 1);
     tc::bar_init(bar_end, 1);
     tc::bar_fence_init();
+    tc::fence_smem_to_async();
   }
-  for (int k = tid; k <= 2 * C; k += S::NT) {
-    const int x = rev ? C - k : k - C;                       // tokens apart, backwards or forwards
-    apart[k] = x >= 0 ? jb.sp * dc.pow(x) : 0.f;
-    pw[k - C] = k >= C ? dc.pow(k - C) : 0.f;
+  // the copying warp tells the others and goes ahead: the first tiles are on their way while
+  // the tables are made
+  if (warp == WA + WB + 1) {
+    __syncwarp();
+    asm volatile("bar.arrive 1, %0;\n" ::"n"(S::NT) : "memory");
+  } else {
+    for (int k = tid; k <= 2 * C; k += S::NT - 32) {
+      const int x = rev ? C - k : k - C;                     // tokens apart, backwards or forwards
+      apart[k] = x >= 0 ? jb.sp * dc.pow(x) : 0.f;
+      pw[k - C] = k >= C ? dc.pow(k - C) : 0.f;
+    }
+    if (warp == WA + WB) tc::alloc(tslot, S::kCols);
+    tc::fence_before();
+    asm volatile("bar.sync 1, %0;\n" ::"n"(S::NT) : "memory");
+    tc::fence_after();
   }
-  if (warp == WA + WB) tc::alloc(tslot, S::kCols);
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
   // the full passes' launch may start setting up on SMs that this one leaves free
   if (!full) asm volatile("griddepcontrol.launch_dependents;\n");
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = warp == WA + WB + 1 ? 0 : *tslot;
   const uint32_t base = tc::smem_addr(sm);
   bool ok = true;
   // after a wait that gave up a role issues no more work and ends
@@ -279,27 +292,21 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     tc::fence_after();
     return ok;
   };
-  // tiles a chunk: x, y, z (or y, z): the i-th tile of the run lies in slot i % SLOTS
-  const int per = full ? 3 : 2;
 
   if (warp == WA + WB + 1) {
     // ---- copies ----
     if (lane == 0) {
       int tile = 0;
-      for (int it = 0; it < nch && ok; ++it) {
-        const int t0 = first(it);
-        for (int k = 0; k < per && ok; ++k, ++tile) {
-          const int which = full ? k : k + 1;
-          const CUtensorMap* m = &args.map[which == 0 ? jb.xi : which == 1 ? jb.yi : jb.zi];
-          const int s = tile % SLOTS;
-          if (tile >= SLOTS && !wait(bar_empty + s, tile / SLOTS - 1)) break;
-          tc::bar_expect_tx(bar_full + s, S::kTile);
-          for (uint32_t x = 0; x < S::NB; ++x)
-            tc::tma_load_4d(sm + S::oRing + s * S::kTile + x * S::kBox, m, x * 64, h, t0, b, bar_full + s);
-        }
+      for (; tile < nch * per; ++tile) {
+        const int s = tile % SLOTS, which = full ? tile % 3 : tile % 2 + 1;
+        const CUtensorMap* m = &args.map[which == 0 ? jb.xi : which == 1 ? jb.yi : jb.zi];
+        if (tile >= SLOTS && !(ok = tc::bar_wait_long(bar_empty + s, (tile / SLOTS - 1) & 1))) break;
+        tc::bar_expect_tx(bar_full + s, S::kTile);
+        for (uint32_t x = 0; x < S::NB; ++x)
+          tc::tma_load_4d(sm + S::oRing + s * S::kTile + x * S::kBox, m, x * 64, h, first(tile / per), b, bar_full + s);
       }
       // a copy still in flight may not outlive the CTA
-      for (int i = max(tile - SLOTS, 0); i < tile; ++i) ok &= tc::bar_wait(bar_full + i % SLOTS, (i / SLOTS) & 1);
+      for (int i = max(tile - SLOTS, 0); i < tile; ++i) ok &= tc::bar_wait_long(bar_full + i % SLOTS, (i / SLOTS) & 1);
     }
   } else if (warp == WA + WB) {
     // ---- MMAs: the whole warp runs, one lane issues ----
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           if (tc::elect()) {
 #pragma unroll 1
             for (int t = 0; t < terms; ++t) {
-              const uint32_t d = t == 0 ? dy : dm + (t - 1) * (S::kTile / 32);
+              const uint32_t d = t == 0 ? dy : dm + (t - 1) * (S::kLo / 16);
               if (kn == rows / 16) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       }
       if (tc::elect()) tc::commit(bar_end);
       __syncwarp();
-      ok &= tc::bar_wait(bar_end, 0);
+      ok &= tc::bar_wait_long(bar_end, 0);
     }
   } else if (warp < WA) {
     // ---- A: scores, the terms of y, outputs ----
@@ -515,7 +522,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
               for (int e = 0; e < 4; ++e) {
                 lo[e] = tc::round2(fma2(pack2(tc::bf_lo(mid[e]), tc::bf_hi(mid[e])), minus, left[e]));
               }
-              *reinterpret_cast<uint4*>(m + S::kTile / 2 + r * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(m + S::kLo + r * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
           }
         }
@@ -647,21 +654,26 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       __syncwarp();
       if (lane == 0) tc::bar_arrive(bar_s + ((it + 1) & 1));
     }
-    if (full && wb == 0 && lane == 0) tc::bulk_wait_all();
     float* dst = !full ? p.seg + (((size_t)job * p.B * p.H + bh) * (p.nseg - 1) + seg) * D * D
                  : seg == p.nseg - 1 && jb.s_out ? jb.s_out + (size_t)bh * D * D : nullptr;
-    if (dst && mine) {
-      const bool tr = full && jb.out_t;
+    if (dst && ok && D == 128) {
+      // each thread's 256 bytes of a row, from the ring (every tile is used up) by its own bulk
+      // copy: stored from the threads, 64 KB took 7000 cycles
+      constexpr uint32_t kPad = NS * 4 + 16;                 // rows apart by an odd number of 16 bytes
+      static_assert(D < 128 || S::WB * 32 * kPad <= S::SLOTS * S::kTile, "the ring holds the padded state");
+      unsigned char* part = sm + S::oRing + (tid - WA * 32) * kPad;
 #pragma unroll
-      for (int c = 0; c < NS; c += 4) {
-        if (tr) {
+      for (int c = 0; c < NS; c += 4)
+        *reinterpret_cast<float4*>(part + c * 4) = make_float4(st[c], st[c + 1], st[c + 2], st[c + 3]);
+      tc::fence_smem_to_async();
+      tc::bulk_s2g(dst + row * D + y0, part, NS * 4);
+      tc::bulk_commit();
+    } else if (dst && ok && mine) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dst[(y0 + c + k) * D + row] = st[c + k];
-        } else {
-          *reinterpret_cast<float4*>(dst + row * D + y0 + c) = make_float4(st[c], st[c + 1], st[c + 2], st[c + 3]);
-        }
-      }
+      for (int c = 0; c < NS; c += 4)
+        *reinterpret_cast<float4*>(dst + row * D + y0 + c) = make_float4(st[c], st[c + 1], st[c + 2], st[c + 3]);
     }
+    tc::bulk_wait_read();
   }
   if (!ok) atomicOr(p.status, 1);
   tc::fence_before();
