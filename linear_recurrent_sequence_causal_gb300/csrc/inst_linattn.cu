@@ -11,7 +11,8 @@ template <int D>
 cudaError_t launch_fma_t(const LinattnArgs& a, cudaStream_t s) {
   using S = LinattnFma<D>;
   auto fn = linattn_fma_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(fn, S::bytes, done);
   if (e != cudaSuccess) return e;
   LinattnArgs p = a;
   const unsigned bh = (unsigned)(a.B * a.H * S::NSL);

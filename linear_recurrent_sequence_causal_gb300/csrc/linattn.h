@@ -5,7 +5,21 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace prism {
+
+// cudaFuncAttributeMaxDynamicSharedMemorySize, set on the first launch of a kernel on each device:
+// `done` (one word a kernel) has a bit a device.  Devices past the 64th are set every time.
+template <class F>
+cudaError_t allow_smem(F* fn, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
 
 struct RopeArgs;
 struct LinattnArgs;

@@ -29,6 +29,7 @@
 #include <cuda.h>
 
 #include "linattn.cuh"
+#include "linattn.h"
 #include "tc_common.cuh"
 
 namespace prism {
@@ -685,7 +686,8 @@ template <int D>
 cudaError_t launch_linattn_tc_t(const LinattnTcArgs& a, cudaStream_t s) {
   using S = LinattnTc<D>;
   auto fn = linattn_tc_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(fn, S::bytes, done);
   if (e != cudaSuccess) return e;
   LinattnTcArgs p = a;
   const unsigned bh = (unsigned)(a.a.B * a.a.H);

@@ -101,6 +101,11 @@ def _strided(name, t):
     return t.data_ptr()
 
 
+def _out(t):
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _stream(t, stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
 
@@ -162,9 +167,9 @@ def prism_qk_norm_rope(q, k, table, *, q_weight=None, k_weight=None, q_scale=1.0
     keep, dims, _ = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape, interleaved,
                             eps, q_scale, k_scale, None, None)
     if q_out is None:
-        q_out = torch.empty(qs, dtype=dt, device=q.device)
+        q_out = _out(q)
     if k_out is None:
-        k_out = torch.empty(ks, dtype=dt, device=q.device)
+        k_out = _out(k)
     D = qs[3:]
     _check(load().prism_qk_norm_rope(
         dims, _strided("q", q), _strided("k", k), _whole("q_weight", q_weight, D, torch.float32),
@@ -190,11 +195,9 @@ def prism_qk_norm_rope_backward(q, k, table, dq_out, dk_out, *, q_weight=None, k
                                  interleaved, eps, q_scale, k_scale, dq_out.stride(), dk_out.stride())
     dev, D = q.device, qs[3:]
     g = dict(grads) if grads else {}
-    for n, shape, of, want in (("q", qs, dt, True), ("k", ks, dt, True),
-                               ("q_weight", D, torch.float32, q_weight is not None),
-                               ("k_weight", D, torch.float32, k_weight is not None)):
+    for n, t in (("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight)):
         if g.get(n) is None:
-            g[n] = torch.empty(shape, dtype=of, device=dev) if want else None
+            g[n] = None if t is None else _out(t)
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(load().prism_qk_norm_rope_backward(
@@ -225,7 +228,7 @@ def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, 
     keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), None)
     ss = _state_shape(qs)
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=q.device)
+        out = _out(q)
     if final_state is None and want_state:
         final_state = torch.empty(ss, dtype=torch.float32, device=q.device)
     if workspace is None and nbytes:
@@ -252,9 +255,9 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
     keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), d_out.stride())
     ss, dev = _state_shape(qs), q.device
     g = dict(grads) if grads else {}
-    for n in ("q", "k", "v"):
+    for n, t in (("q", q), ("k", k), ("v", v)):
         if g.get(n) is None:
-            g[n] = torch.empty(qs, dtype=dt, device=dev)
+            g[n] = _out(t)
     if g.get("initial_state") is None:
         g["initial_state"] = None if initial_state is None else torch.empty(ss, dtype=torch.float32, device=dev)
     if workspace is None and nbytes:
@@ -282,7 +285,7 @@ def prism_linattn_decode_step(q, k, v, log_decay, state, *, scale=1.0, slots=Non
     keep, dims = _decode_dims(qs, dt, scale, q.stride(), k.stride(), v.stride())
     N = state.shape[0]
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=q.device)
+        out = _out(q)
     _check(load().prism_linattn_decode_step(
         dims, _strided("q", q), _strided("k", k), _strided("v", v),
         _whole("log_decay", log_decay, qs[1:2], torch.float32),
