@@ -91,7 +91,6 @@ struct Decay {
     return make_float2(pow(n), 0.f);
   }
 };
-__device__ __forceinline__ float decayed(float2 l, float s) { return fmaf(l.x, s, l.y * s); }
 
 // A sequence cut into runs: run s takes the chunks first..last-1 in processing order.
 struct LinattnRuns {
@@ -140,23 +139,47 @@ __device__ __forceinline__ void linattn_start(float* st, const LinattnArgs& p, c
 
 // ---- fp32, on the CUDA cores ----
 //
-// One CTA per (b, h, run, 32 rows of the state): rows of S and columns of the output are
-// independent.  Chunks of 32 tokens; x, y, z, the scores and S's rows in shared memory, S
-// itself in registers.  Bound by the shared-memory reads of the products.
+// One CTA per (b, h, run, pass, up to 64 rows of the state): rows of S and columns of the output
+// are independent.  Chunks of 32 tokens; x, y, z, the scores and S^T in shared memory, S itself
+// in registers; below d = 128 the next chunk's tiles come in (cp.async) while one is worked on.
+// Bound by the shared-memory reads of the products and the waits between them, hence 4 x 4
+// tiles of S, 2 x 4 tiles of the output, packed arithmetic, and one CTA for all columns
+// where that fits (32-row slices with 2 x 2 tiles and no tiles ahead took 1.5 times as long).
 template <int D_>
 struct LinattnFma {
-  static constexpr int D = D_, C = 32, BZ = D < 32 ? D : 32, NSL = D / BZ, NT = 256;
+  static constexpr int D = D_, C = 32, BZ = D < 64 ? D : 64, NSL = D / BZ, NT = 256;
   static constexpr int LD = D + 4, LZ = BZ + 4, LP = C + 4;
-  static constexpr size_t bytes = sizeof(float) * (2 * C * LD + C * LZ + C * LP + BZ * LD + C);
+  static constexpr int kSets = D < 128 ? 2 : 1;        // sets of tiles (two of them leave one CTA an SM at d = 128)
+  static constexpr int kSet = 2 * C * LD + C * LZ;
+  static constexpr size_t bytes = sizeof(float) * (kSets * kSet + C * LP + D * LZ + 2 * C);
 };
 
+// Starts the copy of 32 rows of N floats into shared memory; rows from n on become zeros.
 template <int N, int LDS>
 __device__ __forceinline__ void linattn_tile(float* dst, const float* src, long long stride, int n) {
   for (int i = threadIdx.x; i < 32 * N / 4; i += 256) {
     const int r = i / (N / 4), c = i % (N / 4) * 4;
-    *reinterpret_cast<float4*>(dst + r * LDS + c) =
-        r < n ? __ldg(reinterpret_cast<const float4*>(src + r * stride + c))
-              : make_float4(0.f, 0.f, 0.f, 0.f);       // padding, whatever it holds
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst + r * LDS + c)),
+                 "l"(src + (r < n ? r : 0) * stride + c), "r"(r < n ? 16 : 0)
+                 : "memory");
+  }
+}
+// acc (N / 2 pairs of columns) += a * row[0..N)
+template <int N>
+__device__ __forceinline__ void linattn_axpy(uint64_t (&acc)[N / 2 < 1 ? 1 : N / 2], float a, const float* row) {
+  const uint64_t a2 = pack2(a, a);
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(row + c);
+      acc[c / 2] = fma2(a2, pack2(v.x, v.y), acc[c / 2]);
+      acc[c / 2 + 1] = fma2(a2, pack2(v.z, v.w), acc[c / 2 + 1]);
+    }
+  } else if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(row);
+    acc[0] = fma2(a2, pack2(v.x, v.y), acc[0]);
+  } else {
+    acc[0] = fma2(a2, pack2(row[0], 0.f), acc[0]);
   }
 }
 
@@ -165,7 +188,7 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   using S = LinattnFma<D>;
   constexpr int C = S::C, BZ = S::BZ, LD = S::LD, LZ = S::LZ, LP = S::LP;
   extern __shared__ __align__(16) float fma_sm[];
-  float *sx = fma_sm, *sy = sx + C * LD, *sz = sy + C * LD, *sp = sz + C * LZ, *ss = sp + C * LP, *sw = ss + BZ * LD;
+  float *sp = fma_sm + S::kSets * S::kSet, *st_sm = sp + C * LP, *sw = st_sm + D * LZ;
   const int job = blockIdx.x % p.njobs, item = blockIdx.x / p.njobs;
   const LinattnJob& jb = p.job[job];
   const int runs = p.phase == 1 ? p.nseg - 1 : p.nseg;
@@ -178,11 +201,13 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   constexpr int DG = D / 4, NGR = 256 / DG, RPT = BZ > NGR ? BZ / NGR : 1;
   const int zr = tid / DG * RPT, yc = tid % DG * 4;
   const bool owner = zr < BZ;
-  float st[RPT][4];
+  uint64_t st[RPT][2];
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
-    st[r][0] = st[r][1] = st[r][2] = st[r][3] = 0.f;
-    if (full && owner) linattn_start<D, 4>(st[r], p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc);
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (full && owner) linattn_start<D, 4>(f, p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc);
+    st[r][0] = pack2(f[0], f[1]);
+    st[r][1] = pack2(f[2], f[3]);
   }
   const float* gx = static_cast<const float*>(jb.x) + b * jb.xs[0] + h * D;
   const float* gy = static_cast<const float*>(jb.y) + b * jb.ys[0] + h * D;
@@ -191,20 +216,46 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   const int i1 = min((seg + 1) * p.seg_chunks, rn.chunks);
   const int i0 = full ? seg * p.seg_chunks : max(seg * p.seg_chunks, i1 - dc.reach(126.f, C));
   const int ti = tid / 16 * 2, tj = tid % 16;
-  for (int it = i0; it < i1; ++it) {
-    const int c = jb.rev ? rn.chunks - 1 - it : it, t0 = c * C, n = min(C, rn.len - t0);
+  auto first = [&](int it) { return (jb.rev ? rn.chunks - 1 - it : it) * C; };
+  auto fetch = [&](int it) {
+    float* sx = fma_sm + (S::kSets == 2 && (it & 1) ? S::kSet : 0);
+    const int t0 = first(it), n = min(C, rn.len - t0);
     if (full) linattn_tile<D, LD>(sx, gx + t0 * jb.xs[1], jb.xs[1], n);
-    linattn_tile<D, LD>(sy, gy + t0 * jb.ys[1], jb.ys[1], n);
-    linattn_tile<BZ, LZ>(sz, gz + t0 * jb.zs[1], jb.zs[1], n);
+    linattn_tile<D, LD>(sx + C * LD, gy + t0 * jb.ys[1], jb.ys[1], n);
+    linattn_tile<BZ, LZ>(sx + 2 * C * LD, gz + t0 * jb.zs[1], jb.zs[1], n);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  if (i0 < i1) fetch(i0);
+  for (int it = i0; it < i1; ++it) {
+    const int t0 = first(it), n = min(C, rn.len - t0);
+    float *sx = fma_sm + (S::kSets == 2 && (it & 1) ? S::kSet : 0), *sy = sx + C * LD, *sz = sy + C * LD;
+    if (S::kSets == 2 && it + 1 < i1) fetch(it + 1);
     if (tid < C) sw[tid] = tid < n ? jb.su * dc.pow(jb.rev ? tid + 1 : n - 1 - tid) : 0.f;
-    if (full && owner) {
+    if (full && owner) {                             // S^T, for the output's products
+      float f[RPT][4];
 #pragma unroll
-      for (int r = 0; r < RPT; ++r)
-        *reinterpret_cast<float4*>(ss + (zr + r) * LD + yc) = make_float4(st[r][0], st[r][1], st[r][2], st[r][3]);
+      for (int r = 0; r < RPT; ++r) {
+        unpack2(st[r][0], f[r][0], f[r][1]);
+        unpack2(st[r][1], f[r][2], f[r][3]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if constexpr (RPT >= 4) {
+#pragma unroll
+          for (int r = 0; r < RPT; r += 4)
+            *reinterpret_cast<float4*>(st_sm + (yc + q) * LZ + zr + r) = make_float4(f[r][q], f[r + 1][q], f[r + 2][q], f[r + 3][q]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) st_sm[(yc + q) * LZ + zr + r] = f[r][q];
+        }
     }
+    if (S::kSets == 2 && it + 1 < i1)
+      asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncthreads();
     if (full) {
-      float a[2][2] = {{0.f, 0.f}, {0.f, 0.f}};      // scores of rows ti, ti+1 and columns tj, tj+16
+      uint64_t a[2][2] = {{0, 0}, {0, 0}};           // scores of rows ti, ti+1 and columns tj, tj+16, even and odd d
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
         float4 xv[2], yv[2];
@@ -217,10 +268,8 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            a[e][f] = fmaf(xv[e].x, yv[f].x, a[e][f]);
-            a[e][f] = fmaf(xv[e].y, yv[f].y, a[e][f]);
-            a[e][f] = fmaf(xv[e].z, yv[f].z, a[e][f]);
-            a[e][f] = fmaf(xv[e].w, yv[f].w, a[e][f]);
+            a[e][f] = fma2(pack2(xv[e].x, xv[e].y), pack2(yv[f].x, yv[f].y), a[e][f]);
+            a[e][f] = fma2(pack2(xv[e].z, xv[e].w), pack2(yv[f].z, yv[f].w), a[e][f]);
           }
       }
 #pragma unroll
@@ -228,36 +277,41 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const int k = jb.rev ? tj + 16 * f - ti - e : ti + e - tj - 16 * f;   // tokens apart
-          sp[(ti + e) * LP + tj + 16 * f] = k >= 0 ? a[e][f] * (jb.sp * dc.pow(k)) : 0.f;
+          float lo, hi;
+          unpack2(a[e][f], lo, hi);
+          sp[(ti + e) * LP + tj + 16 * f] = k >= 0 ? (lo + hi) * (jb.sp * dc.pow(k)) : 0.f;
         }
       __syncthreads();
-      constexpr int NC2 = BZ / 16;                   // columns tj, tj+16
-      float o[2][NC2], oi[2][NC2];
+      constexpr int NC = BZ / 16, NP = NC / 2 < 1 ? 1 : NC / 2;   // columns NC tj.. of rows ti, ti+1
+      uint64_t o[2][NP], oi[2][NP];
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int f = 0; f < NC2; ++f) o[e][f] = oi[e][f] = 0.f;
-#pragma unroll 8
-      for (int j = 0; j < C; ++j)
+        for (int f = 0; f < NP; ++f) o[e][f] = oi[e][f] = 0;
+#pragma unroll 2
+      for (int j = 0; j < C; j += 4) {
+        float4 pv[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int f = 0; f < NC2; ++f) o[e][f] = fmaf(sp[(ti + e) * LP + j], sz[j * LZ + tj + 16 * f], o[e][f]);
-#pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 sv[NC2];
-#pragma unroll
-        for (int f = 0; f < NC2; ++f) sv[f] = *reinterpret_cast<const float4*>(ss + (tj + 16 * f) * LD + d);
+        for (int e = 0; e < 2; ++e) pv[e] = *reinterpret_cast<const float4*>(sp + (ti + e) * LP + j);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float4 xv = *reinterpret_cast<const float4*>(sx + (ti + e) * LD + d);
+          linattn_axpy<NC>(o[e], pv[e].x, sz + j * LZ + tj * NC);
+          linattn_axpy<NC>(o[e], pv[e].y, sz + (j + 1) * LZ + tj * NC);
+          linattn_axpy<NC>(o[e], pv[e].z, sz + (j + 2) * LZ + tj * NC);
+          linattn_axpy<NC>(o[e], pv[e].w, sz + (j + 3) * LZ + tj * NC);
+        }
+      }
+#pragma unroll 2
+      for (int d = 0; d < D; d += 4) {
+        float4 xv[2];
 #pragma unroll
-          for (int f = 0; f < NC2; ++f) {
-            oi[e][f] = fmaf(xv.x, sv[f].x, oi[e][f]);
-            oi[e][f] = fmaf(xv.y, sv[f].y, oi[e][f]);
-            oi[e][f] = fmaf(xv.z, sv[f].z, oi[e][f]);
-            oi[e][f] = fmaf(xv.w, sv[f].w, oi[e][f]);
-          }
+        for (int e = 0; e < 2; ++e) xv[e] = *reinterpret_cast<const float4*>(sx + (ti + e) * LD + d);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          linattn_axpy<NC>(oi[e], xv[e].x, st_sm + d * LZ + tj * NC);
+          linattn_axpy<NC>(oi[e], xv[e].y, st_sm + (d + 1) * LZ + tj * NC);
+          linattn_axpy<NC>(oi[e], xv[e].z, st_sm + (d + 2) * LZ + tj * NC);
+          linattn_axpy<NC>(oi[e], xv[e].w, st_sm + (d + 3) * LZ + tj * NC);
         }
       }
 #pragma unroll
@@ -265,32 +319,51 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
         const int i = ti + e;
         if (i >= n) continue;
         const float g = jb.so * dc.pow(jb.rev ? n - 1 - i : i + 1);
+        float v[2 * NP];
 #pragma unroll
-        for (int f = 0; f < NC2; ++f)
-          out[(size_t)(t0 + i) * p.H * D + tj + 16 * f] = fmaf(g, oi[e][f], o[e][f]);
+        for (int f = 0; f < NP; ++f) unpack2(fma2(pack2(g, g), oi[e][f], o[e][f]), v[2 * f], v[2 * f + 1]);
+        float* dst = out + (size_t)(t0 + i) * p.H * D + tj * NC;
+        if constexpr (NC == 4) {
+          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        } else if constexpr (NC == 2) {
+          *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
+        } else {
+          *dst = v[0];
+        }
       }
     }
     if (owner) {
       const float2 ln = dc.step(n);
+      const uint64_t lx = pack2(ln.x, ln.x), ly = pack2(ln.y, ln.y);
 #pragma unroll
       for (int r = 0; r < RPT; ++r)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) st[r][q] = decayed(ln, st[r][q]);
-#pragma unroll 4
+        for (int q = 0; q < 2; ++q) st[r][q] = fma2(lx, st[r][q], mul2(ly, st[r][q]));
+#pragma unroll 2
       for (int j = 0; j < C; ++j) {
-        const float w = sw[j];
         const float4 yv = *reinterpret_cast<const float4*>(sy + j * LD + yc);
+        const uint64_t w2 = pack2(sw[j], sw[j]), ya = mul2(w2, pack2(yv.x, yv.y)), yb = mul2(w2, pack2(yv.z, yv.w));
+        float zv[RPT];
+        if constexpr (RPT >= 4) {
+#pragma unroll
+          for (int r = 0; r < RPT; r += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(sz + j * LZ + zr + r);
+            zv[r] = v.x; zv[r + 1] = v.y; zv[r + 2] = v.z; zv[r + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) zv[r] = sz[j * LZ + zr + r];
+        }
 #pragma unroll
         for (int r = 0; r < RPT; ++r) {
-          const float zv = sz[j * LZ + zr + r] * w;
-          st[r][0] = fmaf(zv, yv.x, st[r][0]);
-          st[r][1] = fmaf(zv, yv.y, st[r][1]);
-          st[r][2] = fmaf(zv, yv.z, st[r][2]);
-          st[r][3] = fmaf(zv, yv.w, st[r][3]);
+          const uint64_t z2 = pack2(zv[r], zv[r]);
+          st[r][0] = fma2(z2, ya, st[r][0]);
+          st[r][1] = fma2(z2, yb, st[r][1]);
         }
       }
     }
     __syncthreads();
+    if (S::kSets == 1 && it + 1 < i1) fetch(it + 1);
   }
   if (full) {                                        // padding: zeros, shared out over the runs
     for (long long i = (long long)seg * 256 + tid; i < (long long)(p.T - rn.len) * BZ; i += p.nseg * 256)
@@ -301,12 +374,12 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
                : seg == p.nseg - 1 && jb.s_out ? jb.s_out + (size_t)bh * D * D : nullptr;
   if (!dst) return;
 #pragma unroll
-  for (int r = 0; r < RPT; ++r)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int z = z0 + zr + r, y = yc + q;
-      dst[z * D + y] = st[r][q];
-    }
+  for (int r = 0; r < RPT; ++r) {
+    float f[4];
+    unpack2(st[r][0], f[0], f[1]);
+    unpack2(st[r][1], f[2], f[3]);
+    *reinterpret_cast<float4*>(dst + (size_t)(z0 + zr + r) * D + yc) = make_float4(f[0], f[1], f[2], f[3]);
+  }
 }
 
 // ---- one token of every sequence ----

@@ -98,20 +98,21 @@ int check_linattn(const prism_linattn_dims* d) {
 // Runs that each sequence is cut into.  The CTAs of a launch take ceil(CTAs / resident) turns of
 // their run's chunks; cutting adds a first launch over the runs' states (all but the last run)
 // whose chunks cost about kStateChunk of a full one, each CTA about kStart chunks of setting up,
-// and a run reads the states of all before it, kJoin chunks each.  The cheapest count wins; runs
+// and a run reads the states of all before it, a chunk's join each.  The cheapest count wins; runs
 // keep at least two chunks.
 constexpr int kSMs = 152;
-constexpr double kStateChunk = 0.4, kStart = 1.5, kJoin = 0.4;
+constexpr double kStateChunk = 0.4, kStart = 1.5;
 void plan_runs(const prism_linattn_dims* d, int njobs, prism::LinattnArgs& a) {
   const bool tc = d->dtype == PRISM_BF16;
-  const int C = tc ? 128 : 32, slices = !tc && d->d > 32 ? d->d / 32 : 1;
-  const long long resident = (long long)kSMs * (tc ? (d->d == 128 ? 1 : 2) : 3);
+  const int C = tc ? 128 : 32, slices = !tc && d->d > 64 ? d->d / 64 : 1;
+  const double join = tc ? 0.4 : 0.8;             // the fp32 chunk is shorter
+  const long long resident = (long long)kSMs * (tc ? (d->d == 128 ? 1 : 2) : d->d == 128 ? 2 : d->d == 64 ? 3 : 4);
   const long long ctas = (long long)d->B * d->H * slices * njobs;
   const int chunks = (d->T + C - 1) / C;
   double least = 0.;
   for (int n = 1; n <= prism::kLinattnMaxSeg && n <= (chunks + 1) / 2; ++n) {
     const int per = (chunks + n - 1) / n;
-    const double turns = (double)((ctas * n + resident - 1) / resident) * (per + kStart + kJoin * (n - 1));
+    const double turns = (double)((ctas * n + resident - 1) / resident) * (per + kStart + join * (n - 1));
     const double states = n == 1 ? 0. : (double)((ctas * (n - 1) + resident - 1) / resident) * (kStateChunk * per + kStart);
     if (n == 1 || turns + states < least) {
       least = turns + states;
