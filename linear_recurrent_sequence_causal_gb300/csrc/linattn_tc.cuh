@@ -60,7 +60,7 @@ struct LinattnTc {
   static constexpr uint32_t oPow = oRing + SLOTS * kTile + (kOutS ? 0 : kMid);   // lambda^k at k + C, 0 for k < 0
   static constexpr uint32_t oApart = oPow + (2 * C + 4) * 4;    // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
-  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 15) * 8 + 8;
+  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 17) * 8 + 8;
   // TMEM columns.  D = 64: U takes the half of P that the bf16 scores leave free, so that two
   // CTAs share an SM's 512 columns.
   static constexpr bool kShareU = D == 64;
@@ -217,8 +217,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_t = bar_qk + 7;              // [2] a step's terms are in U
   uint64_t* bar_u = bar_qk + 9;              // [2] a chunk's U is there
   uint64_t* bar_y = bar_qk + 11;             // [2] a step's terms of Yd are in shared memory
-  uint64_t* bar_s = bar_qk + 13;             // [2] S is in shared memory, U of the last chunk is read
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 15) * 8);
+  uint64_t* bar_s = bar_qk + 13;             // [2] S is in shared memory
+  uint64_t* bar_r = bar_qk + 15;             // [2] a chunk's U is read
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 17) * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int job = blockIdx.x % p.njobs, item = blockIdx.x / p.njobs;   // a head's passes share its tiles in L2
@@ -258,6 +259,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       tc::bar_init(bar_y + i, WA);
       tc::bar_init(bar_u + i, 1);
       tc::bar_init(bar_s + i, WB);
+      tc::bar_init(bar_r + i, WB);
     }
     tc::bar_init(bar_z, WA);
     tc::bar_init(bar_out, WA);
@@ -317,11 +319,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       const int steps = __shfl_sync(0xffffffffu, nch, 0), i0u = __shfl_sync(0xffffffffu, i0, 0);
       auto first = [&](int it) { return (rev ? chunks - 1 - (i0u + it) : i0u + it) * C; };
       auto count = [&](int t0) { return min(C, len - t0); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, tc::bar_wait_long(bar, parity & 1));
-        tc::fence_after();
-        return ok;
-      };
       constexpr uint32_t id_p = tc::idesc_bf16(128, false, false), id_s = tc::idesc_bf16(D, false, false);
       constexpr uint32_t id_o = tc::idesc_bf16(D, false, true), id_u = tc::idesc_bf16(D, true, true);
       constexpr uint32_t kStepMn = 16 * S::RB / 16;          // 16 tokens of an MN-major tile, in 16 bytes
@@ -331,104 +328,118 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       auto at = [](int tile) { return (uint32_t)(tile % SLOTS) * (S::kTile / 16); };
       // K-step kk (16 columns) in a K-major tile whose boxes are `box` bytes, in 16 bytes
       auto kstep = [](int kk, uint32_t box) { return (uint32_t)(kk / 4) * (box / 16) + (uint32_t)(kk % 4) * 2; };
-      int scored = 0;                                        // chunks whose scores are issued
-      auto scores = [&]() {
-        const int it = scored, tx = 3 * it, ty = tx + 1;
-        const uint32_t dx = d_ring + at(tx), dy = d_ring + at(ty);
-        if (!wait(bar_full + tx % SLOTS, tx / SLOTS) || !wait(bar_full + ty % SLOTS, ty / SLOTS)) return;
-        const int t0 = first(it);
-        if (ragged(t0, count(t0)) && !wait(bar_z, 0)) return;
-        if (S::kShareU && !wait(bar_s + it % 2, it / 2)) return;          // U of the last chunk is read
-        if (tc::elect()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss<S::RB>(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
-          tc::commit(bar_qk);
-        }
-        __syncwarp();
-        ++scored;
-      };
+      auto done = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, tc::bar_test(bar, phase & 1)) != 0; };
+      auto landed = [&](int tile) { return done(bar_full + tile % SLOTS, tile / SLOTS); };
+      // What a chunk needs issued, each as soon as its operands are there: PV (scores x Z), XS (X x
+      // state), U's steps, and QK, the next chunk's scores.  (In a fixed order one late operand, the
+      // state after a long sum or a tile on its way, held back all that follow: 5700 cycles a
+      // chunk at d = 128.)  Products on one accumulator, and a product and the ones that overwrite
+      // its operands in TMEM, stay in order because the tensor core runs them in order.
       int step = 0;                                          // steps of Yd so far
-      for (int it = 0; it < steps && ok; ++it) {
+      for (int it = full ? -1 : 0; it < steps && ok; ++it) {
         const int ty = per * it + per - 2, tz = ty + 1;
-        const int t0 = first(it), n = count(t0), ks = ksteps(n);
-        if (full && scored == it) scores();
-        if (!wait(bar_full + tz % SLOTS, tz / SLOTS)) break;
-        if (full) {
-          const uint32_t dz = d_ring + at(tz), dx = d_ring + at(ty - 1);
-          if (!wait(bar_p, it)) break;
-          if (tc::elect()) {
-            if (ks == 8) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
-            } else {
-#pragma unroll 1
-              for (int kk = 0; kk < ks; ++kk)
-                tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
-            }
-          }
-          __syncwarp();
-          if (!wait(bar_s + it % 2, it / 2)) break;
-          if (tc::elect()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_ss<S::RB>(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
-            tc::commit(bar_o);
-            tc::commit(bar_empty + (ty - 1) % SLOTS);
-          }
-          __syncwarp();
-        } else {
-          if (it > 1 && !wait(bar_s + (it - 1) % 2, (it - 1) / 2)) break;         // the U that lay here before is read
-          if (ragged(t0, n) && !wait(bar_z, 0)) break;
-        }
-        // the next chunk's scores before this one's U, if their tiles are there: A needs them
-        // first, and U waits for A
-        if (full && !S::kShareU && it + 1 < steps) {
-          const int ux = 3 * it + 3, uy = ux + 1, u0 = first(it + 1);
-          if (!ragged(u0, count(u0)) && __all_sync(0xffffffffu, tc::bar_test(bar_full + ux % SLOTS, ux / SLOTS & 1) &&
-                                                                    tc::bar_test(bar_full + uy % SLOTS, uy / SLOTS & 1)))
-            scores();
-        }
-        const int terms = __shfl_sync(0xffffffffu, terms_of(it), 0), rows = rows_of(terms);
+        const int t0 = it < 0 ? 0 : first(it), n = it < 0 ? 0 : count(t0), ks = ksteps(n);
+        const int terms = it < 0 ? 2 : __shfl_sync(0xffffffffu, terms_of(it), 0), rows = rows_of(terms);
         const uint32_t d_mid = tc::desc_lo(base + S::oMid, rows * S::RB), d_out = tc::desc_lo(base + S::oOut, rows * S::RB);
-        for (int r0 = 0; r0 < ks * 16; r0 += rows, ++step) {
-          if (!wait(bar_y + step % 2, step / 2)) break;
-          const uint32_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
-          const int kn = min(ks - r0 / 16, rows / 16);
-          // alone, the states have two places for terms and for U, so that a chunk's split, its
-          // products and the last one's sum run at the same time
-          const uint32_t dm = !full && step % 2 == 1 ? d_out : d_mid, du = tm + (!full && it % 2 == 1 ? S::cO1 : S::cU);
-          if (tc::elect()) {
-#pragma unroll 1
-            for (int t = 0; t < terms; ++t) {
-              const uint32_t d = t == 0 ? dy : dm + (t - 1) * (S::kLo / 16);
-              if (kn == rows / 16) {
+        const int u0 = it + 1 < steps ? first(it + 1) : 0;
+        const bool z1 = it + 1 < steps && ragged(u0, count(u0)), z0 = !full && ragged(t0, n);
+        bool need_pv = full && it >= 0, need_xs = need_pv, need_qk = full && it + 1 < steps, need_u = it >= 0;
+        int r0 = 0;
+        for (uint32_t polls = 0; (need_pv || need_xs || need_qk || need_u) && ok; ++polls) {
+          bool moved = false;
+          if (need_pv && landed(tz) && done(bar_p, it)) {
+            tc::fence_after();
+            const uint32_t dz = d_ring + at(tz);
+            if (tc::elect()) {
+              if (ks == 8) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
-                if (kn == 8) {
-#pragma unroll
-                  for (int kk = 4; kk < 8; ++kk)
-                    tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, true);
-                }
+                for (int kk = 0; kk < 8; ++kk)
+                  tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
               } else {
 #pragma unroll 1
-                for (int kk = 0; kk < kn; ++kk)
-                  tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                for (int kk = 0; kk < ks; ++kk)
+                  tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
               }
             }
-            tc::commit(bar_t + step % 2);
+            __syncwarp();
+            need_pv = false;
+            moved = true;
           }
-          __syncwarp();
+          // (A has read O of the last chunk when its scores are there, so O2 comes after PV too)
+          if (need_xs && !need_pv && done(bar_s + it % 2, it / 2)) {
+            tc::fence_after();
+            const uint32_t dx = d_ring + at(ty - 1);
+            if (tc::elect()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_ss<S::RB>(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
+              tc::commit(bar_o);
+              tc::commit(bar_empty + (ty - 1) % SLOTS);
+            }
+            __syncwarp();
+            need_xs = false;
+            moved = true;
+          }
+          // (over P: behind PV; where U lies in P, behind U's last step and its reading)
+          if (need_qk && !need_pv && (!S::kShareU || it < 0 || (!need_u && done(bar_r + it % 2, it / 2))) &&
+              landed(per * it + per) && landed(per * it + per + 1) && (!z1 || done(bar_z, 0))) {
+            tc::fence_after();
+            const uint32_t dx = d_ring + at(per * it + per), dy = d_ring + at(per * it + per + 1);
+            if (tc::elect()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_ss<S::RB>(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
+              tc::commit(bar_qk);
+            }
+            __syncwarp();
+            need_qk = false;
+            moved = true;
+          }
+          // U: alone, the states have two places for terms and for U, so that a chunk's split, its
+          // products and the last one's sum run at the same time
+          const int last = full ? it - 1 : it - 2;           // the chunk whose U lies there
+          if (need_u && !need_pv && done(bar_y + step % 2, step / 2) && (last < 0 || r0 > 0 || done(bar_r + last % 2, last / 2)) &&
+              (full || (landed(tz) && (!z0 || done(bar_z, 0))))) {
+            tc::fence_after();
+            const uint32_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
+            const int kn = min(ks - r0 / 16, rows / 16);
+            const uint32_t dm = !full && step % 2 == 1 ? d_out : d_mid, du = tm + (!full && it % 2 == 1 ? S::cO1 : S::cU);
+            const bool end = r0 + rows >= ks * 16;
+            if (tc::elect()) {
+#pragma unroll 1
+              for (int t = 0; t < terms; ++t) {
+                const uint32_t d = t == 0 ? dy : dm + (t - 1) * (S::kLo / 16);
+                if (kn == rows / 16) {
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                  if (kn == 8) {
+#pragma unroll
+                    for (int kk = 4; kk < 8; ++kk)
+                      tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, true);
+                  }
+                } else {
+#pragma unroll 1
+                  for (int kk = 0; kk < kn; ++kk)
+                    tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
+                }
+              }
+              tc::commit(bar_t + step % 2);
+              if (end) {
+                tc::commit(bar_u + it % 2);
+                tc::commit(bar_empty + ty % SLOTS);
+                tc::commit(bar_empty + tz % SLOTS);
+              }
+            }
+            __syncwarp();
+            need_u = !end;
+            r0 += rows;
+            ++step;
+            moved = true;
+          }
+          if (moved) polls = 0;
+          if (polls > (1u << 22)) ok = false;                // seconds without an operand
         }
-        if (!ok) break;
-        if (tc::elect()) {
-          tc::commit(bar_u + it % 2);
-          tc::commit(bar_empty + ty % SLOTS);
-          tc::commit(bar_empty + tz % SLOTS);
-        }
-        __syncwarp();
       }
       if (tc::elect()) tc::commit(bar_end);
       __syncwarp();
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     }
   } else if (warp < WA) {
     // ---- A: scores, the terms of y, outputs ----
-    constexpr int PA = WA / 4, JB = 4 / PA, CO = D / PA, G = CO < 32 ? CO : 32;
+    constexpr int PA = WA / 4, JB = 4 / PA, CO = D / PA, G = CO < 16 ? CO : 16;
     const int i = (warp & 3) * 32 + lane, part = warp >> 2;  // token of the chunk, part of the columns
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
@@ -606,6 +617,26 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         const int n = count(first(it));
         ln = n == C ? whole : dc.step(n);
         if (!wait(bar_u + it % 2, it / 2)) break;
+      }
+      constexpr int G = NS >= 16 ? 16 : NS;
+      if (it >= 0) {
+        const uint64_t lx = pack2(ln.x, ln.x), ly = pack2(ln.y, ln.y);
+        const uint32_t at = lanes + (!full && (it & 1) ? S::cO1 : S::cU) + y0;
+#pragma unroll
+        for (int c = 0; c < NS; c += G) {
+          uint32_t u[G];
+          tc::lda(at + c, u);
+          tc::wait_ld(u);
+#pragma unroll
+          for (int k = 0; k < G; k += 2) {
+            const uint64_t s2 = pack2(st[c + k], st[c + k + 1]);
+            const uint64_t v = fma2(ly, s2, pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
+            unpack2(fma2(lx, s2, v), st[c + k], st[c + k + 1]);
+          }
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(bar_r + (it & 1));
         if (full) {                                          // O2 has read S; the outputs are read
           if (wb == 0) {
             if (lane == 0) {
@@ -617,41 +648,24 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           if (!wait(S::kOutS ? bar_sent : bar_o, it)) break;
         }
       }
-      const uint64_t lx = pack2(ln.x, ln.x), ly = pack2(ln.y, ln.y);
-      const uint32_t at = lanes + (!full && (it & 1) ? S::cO1 : S::cU) + y0;
-      constexpr int G = NS >= 16 ? 16 : NS;
+      if (!full) continue;
+      if (mine) {                                            // bf16 rows of S, K-major
+        if constexpr (NS >= 8) {
 #pragma unroll
-      for (int c = 0; c < NS; c += G) {
-        if (it >= 0) {
-          uint32_t u[G];
-          tc::lda(at + c, u);
-          tc::wait_ld(u);
-#pragma unroll
-          for (int k = 0; k < G; k += 2) {
-            const uint64_t s2 = pack2(st[c + k], st[c + k + 1]);
-            const uint64_t v = fma2(ly, s2, pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
-            unpack2(fma2(lx, s2, v), st[c + k], st[c + k + 1]);
+          for (int k = 0; k < NS; k += 8) {
+            const int q = (y0 + k) / 8;                      // 16-byte piece of the row
+            const uint32_t off = (uint32_t)(q / 8) * S::kSBox + row * S::RB + (q % 8) * 16;
+            *reinterpret_cast<uint4*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
+                make_uint4(tc::bf2(st[k], st[k + 1]), tc::bf2(st[k + 2], st[k + 3]), tc::bf2(st[k + 4], st[k + 5]),
+                           tc::bf2(st[k + 6], st[k + 7]));
           }
-        }
-        if (full && mine) {                                  // bf16 rows of S, K-major
-          if constexpr (NS >= 8) {
-#pragma unroll
-            for (int k = c; k < c + G; k += 8) {
-              const int q = (y0 + k) / 8;                    // 16-byte piece of the row
-              const uint32_t off = (uint32_t)(q / 8) * S::kSBox + row * S::RB + (q % 8) * 16;
-              *reinterpret_cast<uint4*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
-                  make_uint4(tc::bf2(st[k], st[k + 1]), tc::bf2(st[k + 2], st[k + 3]), tc::bf2(st[k + 4], st[k + 5]),
-                             tc::bf2(st[k + 6], st[k + 7]));
-            }
-          } else {
-            const uint32_t off = row * S::RB + y0 * 2;
-            *reinterpret_cast<uint2*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
-                make_uint2(tc::bf2(st[0], st[1]), tc::bf2(st[2], st[3]));
-          }
+        } else {
+          const uint32_t off = row * S::RB + y0 * 2;
+          *reinterpret_cast<uint2*>(sm + S::oS + (off ^ ((off >> 3) & (S::RB - 16)))) =
+              make_uint2(tc::bf2(st[0], st[1]), tc::bf2(st[2], st[3]));
         }
       }
-      if (full) tc::fence_smem_to_async();
-      tc::fence_before();
+      tc::fence_smem_to_async();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(bar_s + ((it + 1) & 1));
     }
