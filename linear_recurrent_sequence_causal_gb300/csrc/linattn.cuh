@@ -106,34 +106,42 @@ struct LinattnRuns {
   }
 };
 
-// Elements (z, y..y+N-1) of the state that run `seg` of (b, h) starts from.
-template <int D, int N>
-__device__ __forceinline__ void linattn_start(float* st, const LinattnArgs& p, const LinattnJob& jb, int job, int bh,
+// Elements (z + r, y..y+N-1), r < R, of the state that run `seg` of (b, h) starts from.  A run's
+// elements are loaded together: their latency is paid once a run, not once a row.
+template <int D, int R, int N>
+__device__ __forceinline__ void linattn_start(float (&st)[R][N], const LinattnArgs& p, const LinattnJob& jb, int job, int bh,
                                               int seg, const LinattnRuns& rn, const Decay& dc, int z, int y) {
   const int d = rn.done(seg * p.seg_chunks);
 #pragma unroll
-  for (int c = 0; c < N; ++c) st[c] = 0.f;
-  auto add = [&](const float* g, float f, int step) {
-    if (step == 1) {
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < N; ++c) st[r][c] = 0.f;
+  if (jb.s_in) {
+    const float* g = jb.s_in + (size_t)bh * D * D;
+    const float f = dc.pow(d);
+    const int zs = jb.in_t ? 1 : D, ys = jb.in_t ? D : 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < N; ++c) st[r][c] = f * g[(z + r) * zs + (y + c) * ys];
+  }
+  const float* g = p.seg + ((size_t)job * p.B * p.H + bh) * (p.nseg - 1) * D * D + z * D + y;
+  constexpr int kAtOnce = R * N <= 16 ? 4 : R * N <= 32 ? 2 : 1;     // runs whose loads are in flight together
+#pragma unroll kAtOnce
+  for (int s = 0; s < seg; ++s) {
+    const float f = dc.pow(d - rn.done((s + 1) * p.seg_chunks));
+    if (f == 0.f) continue;
+    const float* gs = g + (size_t)s * D * D;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < N; c += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(g + c);
-        st[c] = fmaf(f, v.x, st[c]);
-        st[c + 1] = fmaf(f, v.y, st[c + 1]);
-        st[c + 2] = fmaf(f, v.z, st[c + 2]);
-        st[c + 3] = fmaf(f, v.w, st[c + 3]);
+        const float4 v = *reinterpret_cast<const float4*>(gs + r * D + c);
+        st[r][c] = fmaf(f, v.x, st[r][c]);
+        st[r][c + 1] = fmaf(f, v.y, st[r][c + 1]);
+        st[r][c + 2] = fmaf(f, v.z, st[r][c + 2]);
+        st[r][c + 3] = fmaf(f, v.w, st[r][c + 3]);
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < N; ++c) st[c] = fmaf(f, g[c * D], st[c]);
-    }
-  };
-  if (jb.s_in) add(jb.s_in + (size_t)bh * D * D + (jb.in_t ? y * D + z : z * D + y), dc.pow(d), jb.in_t ? D : 1);
-  const float* g = p.seg + ((size_t)job * p.B * p.H + bh) * (p.nseg - 1) * D * D + z * D + y;
-#pragma unroll 1
-  for (int r = 0; r < seg; ++r) {
-    const float f = dc.pow(d - rn.done((r + 1) * p.seg_chunks));
-    if (f != 0.f) add(g + (size_t)r * D * D, f, 1);
   }
 }
 
@@ -202,12 +210,14 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
   const int zr = tid / DG * RPT, yc = tid % DG * 4;
   const bool owner = zr < BZ;
   uint64_t st[RPT][2];
+  {
+    float f[RPT][4] = {};
+    if (full && owner) linattn_start<D, RPT, 4>(f, p, jb, job, bh, seg, rn, dc, z0 + zr, yc);
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (full && owner) linattn_start<D, 4>(f, p, jb, job, bh, seg, rn, dc, z0 + zr + r, yc);
-    st[r][0] = pack2(f[0], f[1]);
-    st[r][1] = pack2(f[2], f[3]);
+    for (int r = 0; r < RPT; ++r) {
+      st[r][0] = pack2(f[r][0], f[r][1]);
+      st[r][1] = pack2(f[r][2], f[r][3]);
+    }
   }
   const float* gx = static_cast<const float*>(jb.x) + b * jb.xs[0] + h * D;
   const float* gy = static_cast<const float*>(jb.y) + b * jb.ys[0] + h * D;

@@ -591,10 +591,11 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     const int row = ((wb & 3) * 32 + lane) % D;              // row of S (TMEM lane l holds row l % D)
     const int y0 = (D == 128 ? wb >> 2 : D == 64 ? wb >> 1 : wb) * NS;
     const bool mine = D >= 32 || lane < D;                   // D = 16: lanes 16.. repeat
-    float st[NS];
+    float rows_st[1][NS];
+    float (&st)[NS] = rows_st[0];
     if (full) {
       if (p.nseg > 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the runs' states are written
-      linattn_start<D, NS>(st, p, jb, job, bh, seg, rn, dc, row, y0);
+      linattn_start<D, 1, NS>(rows_st, p, jb, job, bh, seg, rn, dc, row, y0);
     } else {
 #pragma unroll
       for (int c = 0; c < NS; ++c) st[c] = 0.f;
