@@ -11,8 +11,8 @@
 // So the rotation needs no exchange between lanes and the norm only log2(D/8) shuffles.  A
 // lane group takes up to kRopeRows heads of one token: their loads are in flight together, and
 // the token's angles and the weights are read once for all of them.  Padding is not read.
-// Forward, 8 x 4096 tokens, 16 + 16 heads of 128, bf16: 91 us, 0.88 of the copy rate (95 us with scalar arithmetic, which
-// filled the issue slots).
+// Forward, 8 x 4096 tokens, 16 + 16 heads of 128, bf16: 89 us, 0.90 of the copy rate (95 us with scalar arithmetic, which
+// filled the issue slots; 91 us with four CTAs an SM).
 #pragma once
 
 #include "prism_common.cuh"
@@ -137,7 +137,7 @@ struct RopeToken {
 
 // Forward.  Grid: the lane groups of all blocks, queries' first.
 template <class E, int D, bool IL>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs p, long long blocks_q, long long blocks) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(E) == 2 ? 5 : 3) rope_kernel(RopeArgs p, long long blocks_q, long long blocks) {
   constexpr int G = D / 8;
   const int u = threadIdx.x % G;
   long long blk = (long long)blockIdx.x * (kRopeThreads / G) + threadIdx.x / G;
