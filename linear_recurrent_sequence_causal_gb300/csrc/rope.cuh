@@ -307,8 +307,6 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBackCtas) rope_backward_ker
         if (mine) rope_put<IL>(out + (now.h0 + i) * D, un, t);
       }
     }
-    // the sum's launch may start on what this one leaves free
-    if (side == 1) asm volatile("griddepcontrol.launch_dependents;\n");
     float sum[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
