@@ -11,14 +11,27 @@
 // state and it still remembers the chunk (by more than a quarter, lambda^rest >= 1/4).
 // Three terms go in two steps of 64 tokens at d >= 64, so that they need no more shared memory.
 //
-// Roles.  The last warp copies the x, y and z tiles by TMA into a ring of five slots; the one
-// before issues the MMAs; A turns P into bf16 scores in place in TMEM, splits y, and
-// writes the outputs; B keeps the state (for D < 128 the MMA repeats Z^T down its
-// 128 rows, and the warps share the columns of a row).  The chain from chunk to chunk is
-// U -> state -> O2; the scores of the next chunk, its copies and this chunk's outputs run beside
-// it.  The element-wise work is bound by latency and instruction fetch, not by issue slots: hence
-// eight warps in A, no long-lived registers there, and short loops (D = 128 took 18 000 cycles
-// a chunk unrolled and with four warps each in A and B).
+// Roles.  The last warp copies the x, y and z tiles by TMA into a ring of 5 tiles at d = 128 (4 at
+// 64, 6 below); the one before issues the MMAs; A turns P into bf16 scores in place in TMEM,
+// splits y, and writes the outputs; B keeps the state (for D < 128 the MMA repeats Z^T down its
+// 128 rows, and the warps share the columns of a row) and sends the outputs by TMA.  The chain
+// from chunk to chunk is U -> state -> O2; the scores of the next chunk, its copies and this
+// chunk's outputs run beside it.
+//
+// What bounds it at d = 128: a chunk takes about 5500 cycles, alone on the GPU or not (16 or 128
+// heads of 4096 tokens: 102 and 106 us with two terms), so neither DRAM nor its latency.  It moves 576 KB through
+// shared memory (operands of the MMAs 288, copies in 96, the split of y 96, S 32, outputs 64),
+// 4600 cycles at 128 bytes a cycle.  The tensor core alone would need 2600 cycles, DRAM 3900 for an SM's
+// share of its rate.  Tried without gain: four more warps for the split (5900 cycles a chunk, for its terms
+// then wait for their tile), A's operand kept in the tensor core for the second term of U, the
+// split shared with B, sixteen warps in A.  One term instead of two would save 96 KB a chunk
+// and is not taken: two keep the state's error below that of S's rounding.
+// The element-wise work is latency and instruction fetch: hence eight warps in A, no long-lived
+// registers there, and short loops (unrolled and with four warps each in A and B a chunk took 18 000 cycles).
+// Measured, d = 128: 8 x 4096 tokens, 16 heads: 127 us, 4.3 TB/s (three terms in the heads that
+// remember most of the sequence; two: 106 us); its gradient 290 us; 65536 tokens, 32 heads:
+// the runs' states 145 us, the passes 405 us.  d = 32, 512 x 200 tokens, 2 heads: 28 us, of which 1.7 us is each
+// CTA's set-up.
 //
 // Tiles lie in shared memory as TMA writes them with a swizzle as wide as a row (32, 64, 128
 // bytes; D = 128 is two boxes of 64 columns): K-major as X, Y and S are read, MN-major as Z
@@ -409,20 +422,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
 #pragma unroll 1
               for (int t = 0; t < terms; ++t) {
                 const uint32_t d = t == 0 ? dy : dm + (t - 1) * (S::kLo / 16);
-                if (kn == rows / 16) {
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
-                  if (kn == 8) {
-#pragma unroll
-                    for (int kk = 4; kk < 8; ++kk)
-                      tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, true);
-                  }
-                } else {
-#pragma unroll 1
-                  for (int kk = 0; kk < kn; ++kk)
-                    tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
-                }
+#pragma unroll 2
+                for (int kk = 0; kk < kn; ++kk)
+                  tc::mma_ss<S::RB>(du, dz + kk * kStepMn, d + kk * kStepMn, id_u, r0 + t + kk > 0);
               }
               tc::commit(bar_t + step % 2);
               if (end) {
