@@ -11,8 +11,8 @@
 // So the rotation needs no exchange between lanes and the norm only log2(D/8) shuffles.  A
 // lane group takes up to kRopeRows heads of one token: their loads are in flight together, and
 // the token's angles and the weights are read once for all of them.  Padding is not read.
-// Forward, 8 x 4096 tokens, 16 + 16 heads of 128, bf16: 89 us, 0.90 of the copy rate (95 us with scalar arithmetic, which
-// filled the issue slots; 91 us with four CTAs an SM).
+// Forward, 8 x 4096 tokens, 16 + 16 heads of 128, bf16: 89 us, 0.90 of the copy rate (95 us with
+// scalar arithmetic, which filled the issue slots; 91 us with four CTAs an SM).
 #pragma once
 
 #include "prism_common.cuh"
