@@ -544,40 +544,40 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(bar_y + step % 2);
-        if (!full || r0 > 0) continue;
-        // the outputs, as a tile that B sends by TMA (an SM's own stores leave at about 20 bytes a
-        // cycle, which held A for 1500 cycles a chunk at d = 128); padding rows are zeros
-        const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
-        const uint64_t g2 = pack2(g, g);
-        if (!wait(bar_o, it)) break;
-#pragma unroll 1
-        for (int c = part * CO; c < (part + 1) * CO; c += G) {
-          uint32_t a[G], e[G];
-          tc::lda(lanes + S::cO1 + c, a);
-          tc::lda(lanes + S::cO2 + c, e);
-          tc::wait_ld(a, e);
-#pragma unroll
-          for (int k = 0; k < G; k += 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int j = k + 2 * q;
-              float x, y;
-              unpack2(fma2(g2, pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
-                                   pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
-                          x, y);
-              o[q] = tc::bf2(x, y);
-            }
-            const uint32_t off = (uint32_t)((c + k) / 64) * S::kBox + i * S::RB + (c + k) % 64 * 2;
-            *reinterpret_cast<uint4*>(sm + S::oOut + (off ^ ((off >> 3) & (S::RB - 16)))) =
-                i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
-          }
-        }
-        tc::fence_smem_to_async();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(bar_out);
       }
+      if (!full || !ok) continue;
+      // the outputs, as a tile that B sends by TMA (an SM's own stores leave at about 20 bytes a
+      // cycle, which held A for 1500 cycles a chunk at d = 128); padding rows are zeros
+      const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
+      const uint64_t g2 = pack2(g, g);
+      if (!wait(bar_o, it)) break;
+#pragma unroll 1
+      for (int c = part * CO; c < (part + 1) * CO; c += G) {
+        uint32_t a[G], e[G];
+        tc::lda(lanes + S::cO1 + c, a);
+        tc::lda(lanes + S::cO2 + c, e);
+        tc::wait_ld(a, e);
+#pragma unroll
+        for (int k = 0; k < G; k += 8) {
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int j = k + 2 * q;
+            float x, y;
+            unpack2(fma2(g2, pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
+                                 pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
+                        x, y);
+            o[q] = tc::bf2(x, y);
+          }
+          const uint32_t off = (uint32_t)((c + k) / 64) * S::kBox + i * S::RB + (c + k) % 64 * 2;
+          *reinterpret_cast<uint4*>(sm + S::oOut + (off ^ ((off >> 3) & (S::RB - 16)))) =
+              i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc::fence_smem_to_async();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(bar_out);
     }
     if (full) {
       // chunks of padding: zeros, shared out over the runs

@@ -180,23 +180,23 @@ class Model:
                 yield
                 self.b["y", step % 2].arrive()
                 step += 1
-                if not self.full or k > 0:
-                    continue
-                yield from self.wait("o", c)
-                where = "S" if self.out_s else "out"
-                old = self.hold.get(where)
-                assert old in (None, ("used", c), ("sent", c - 1), ("part out", c)), f"{where} is overwritten: {old}"
-                if w == 0:
-                    self.want("O1", ("O", c))
-                    self.want("O2", ("O", c))
-                done = self.split.setdefault(("O", c), set())
-                done.add(w)
-                self.put(where, ("out" if len(done) == self.wa else "part out", c))
-                if len(done) == self.wa:
-                    self.put("O1", ("read", c))
-                    self.put("O2", ("read", c))
-                yield
-                self.b["out"].arrive()
+            if not self.full:
+                continue
+            yield from self.wait("o", c)
+            where = "S" if self.out_s else "out"
+            old = self.hold.get(where)
+            assert old in (None, ("used", c), ("sent", c - 1), ("part out", c)), f"{where} is overwritten: {old}"
+            if w == 0:
+                self.want("O1", ("O", c))
+                self.want("O2", ("O", c))
+            done = self.split.setdefault(("O", c), set())
+            done.add(w)
+            self.put(where, ("out" if len(done) == self.wa else "part out", c))
+            if len(done) == self.wa:
+                self.put("O1", ("read", c))
+                self.put("O2", ("read", c))
+            yield
+            self.b["out"].arrive()
 
     def b_warp(self, w):
         for c in range(-1, self.n):
