@@ -112,6 +112,25 @@ def test_ragged_and_empty(D, T, dtype):
     check_backward(x, c, lens=lens)
 
 
+@pytest.mark.parametrize("ragged", [True, False])
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+def test_more_sequences_than_are_resident(D, ragged):
+    """Many short sequences, in several turns of the SMs: shared memory and TMEM still hold what the
+    last CTA left there, and nothing of it reaches a short chunk or an empty sequence."""
+    B, T = (100, 140) if D == 128 else (160, 140)
+    x = make(B, T, 2, D, "bf16", state=True, seed=ragged)
+    c = gpu(x)
+    lens = None
+    if ragged:
+        g = torch.Generator().manual_seed(D)
+        lens = torch.where(torch.rand(B, generator=g) < 0.2, torch.zeros(B), torch.rand(B, generator=g) * (T + 1)).long()
+        for n in ("q", "k", "v", "do"):
+            for b, k in enumerate(lens.tolist()):
+                c[n][b, k:] = float("nan")
+    check_forward(x, c, lens=lens)
+    check_backward(x, c, lens=lens)
+
+
 def test_lengths_are_clamped():
     x = make(2, 40, 1, 32, "bf16")
     c = gpu(x)
