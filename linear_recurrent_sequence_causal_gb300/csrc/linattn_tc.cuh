@@ -28,9 +28,9 @@
 // and is not taken: two keep the state's error below that of S's rounding.
 // The element-wise work is latency and instruction fetch: hence eight warps in A, no long-lived
 // registers there, and short loops (unrolled and with four warps each in A and B a chunk took 18 000 cycles).
-// Measured, d = 128: 8 x 4096 tokens, 16 heads: 127 us, 4.3 TB/s (three terms in the heads that
-// remember most of the sequence; two: 106 us); its gradient 290 us; 65536 tokens, 32 heads:
-// the runs' states 145 us, the passes 405 us.  d = 32, 512 x 200 tokens, 2 heads: 28 us, of which 1.7 us is each
+// Measured, d = 128: 8 x 4096 tokens, 16 heads: 124 us, 4.4 TB/s (three terms in the heads that
+// remember most of the sequence; two: 106 us); its gradient 283 us; 65536 tokens, 32 heads:
+// the runs' states 134 us, the passes 400 us.  d = 32, 512 x 200 tokens, 2 heads: 28 us, of which 1.7 us is each
 // CTA's set-up.
 //
 // Tiles lie in shared memory as TMA writes them with a swizzle as wide as a row (32, 64, 128
@@ -504,39 +504,52 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         // the terms that lay here before are read
         const int back = full ? 1 : 2;
         if (step >= back && !wait(bar_t + (step - back) % 2, (step - back) / 2)) break;
-        // 16-byte pieces of the rows of this step, box by box.  Rows past n hold zeros, or are in
-        // no K-step.
+        // 16-byte pieces of the rows of this step, two of a thread loaded before the first is
+        // stored (behind it they waited: 290 -> 283 us for the gradient of 8 x 4096 tokens, 16 heads of 128).  Rows past
+        // n hold zeros, or are in no K-step.
         constexpr int RI = WA * 32 * 16 / S::RB;             // rows that A takes at once
+        constexpr int PF = S::NB == 1 && S::kRows3 > RI ? 2 : 1;
         const int r1 = r0 + tid / (S::RB / 16);
         const float* wp = pw + (rev ? r1 + 1 : n - 1 - r1);
         unsigned char* y = ys + r0 * S::RB + tid * 16;
         unsigned char* m = sm + (full || step % 2 == 0 ? S::oMid : S::oOut) + tid * 16;
+        const uint32_t mbox = rows * S::RB;
+        const uint64_t minus = pack2(-1.f, -1.f);
 #pragma unroll 1
-        for (uint32_t box = 0; box < S::NB; ++box, y += S::kBox, m += rows * S::RB) {
-#pragma unroll 2
-          for (int r = 0; r < min(rows, krows - r0); r += RI) {
-            if (RI > 64 && r1 - r0 + r >= rows) continue;    // D = 16, 32: a step has fewer rows than A takes
-            const uint4 u = *reinterpret_cast<const uint4*>(y + r * S::RB);
-            const float w = jb.su * wp[rev ? r : -r];
-            const uint64_t w2 = pack2(w, w), minus = pack2(-1.f, -1.f);
-            const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-            uint32_t hi[4], mid[4], lo[4];
-            uint64_t left[4];
+        for (int r = 0; r < min(rows, krows - r0); r += PF * RI, y += PF * RI * S::RB, m += PF * RI * S::RB) {
+          uint4 u[PF][S::NB];
+          float w[PF];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint64_t v = mul2(pack2(tc::bf_lo(in[e]), tc::bf_hi(in[e])), w2);
-              hi[e] = tc::round2(v);
-              left[e] = fma2(pack2(tc::bf_lo(hi[e]), tc::bf_hi(hi[e])), minus, v);
-              mid[e] = tc::round2(left[e]);
-            }
-            *reinterpret_cast<uint4*>(y + r * S::RB) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(m + r * S::RB) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-            if (terms == 3) {
+          for (int f = 0; f < PF; ++f) {
+#pragma unroll
+            for (uint32_t box = 0; box < S::NB; ++box)
+              u[f][box] = *reinterpret_cast<const uint4*>(y + box * S::kBox + f * RI * S::RB);
+            w[f] = jb.su * wp[rev ? r + f * RI : -r - f * RI];
+          }
+#pragma unroll
+          for (int f = 0; f < PF; ++f) {
+            const uint64_t w2 = pack2(w[f], w[f]);
+#pragma unroll
+            for (uint32_t box = 0; box < S::NB; ++box) {
+              const uint32_t in[4] = {u[f][box].x, u[f][box].y, u[f][box].z, u[f][box].w};
+              uint32_t hi[4], mid[4], lo[4];
+              uint64_t left[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                lo[e] = tc::round2(fma2(pack2(tc::bf_lo(mid[e]), tc::bf_hi(mid[e])), minus, left[e]));
+                const uint64_t v = mul2(pack2(tc::bf_lo(in[e]), tc::bf_hi(in[e])), w2);
+                hi[e] = tc::round2(v);
+                left[e] = fma2(pack2(tc::bf_lo(hi[e]), tc::bf_hi(hi[e])), minus, v);
+                mid[e] = tc::round2(left[e]);
               }
-              *reinterpret_cast<uint4*>(m + S::kLo + r * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(y + box * S::kBox + f * RI * S::RB) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(m + box * mbox + f * RI * S::RB) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+              if (terms == 3) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  lo[e] = tc::round2(fma2(pack2(tc::bf_lo(mid[e]), tc::bf_hi(mid[e])), minus, left[e]));
+                }
+                *reinterpret_cast<uint4*>(m + S::kLo + box * mbox + f * RI * S::RB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              }
             }
           }
         }
