@@ -364,15 +364,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             tc::fence_after();
             const uint32_t dz = d_ring + at(tz);
             if (tc::elect()) {
-              if (ks == 8) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
-              } else {
-#pragma unroll 1
-                for (int kk = 0; kk < ks; ++kk)
-                  tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
-              }
+#pragma unroll 2
+              for (int kk = 0; kk < ks; ++kk)
+                tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
             }
             __syncwarp();
             need_pv = false;
@@ -383,7 +377,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             tc::fence_after();
             const uint32_t dx = d_ring + at(ty - 1);
             if (tc::elect()) {
-#pragma unroll
+#pragma unroll 4
               for (int kk = 0; kk < D / 16; ++kk)
                 tc::mma_ss<S::RB>(tm + S::cO2, dx + kstep(kk, S::kBox), d_s + kstep(kk, S::kSBox), id_s, kk > 0);
               tc::commit(bar_o);
@@ -399,7 +393,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             tc::fence_after();
             const uint32_t dx = d_ring + at(per * it + per), dy = d_ring + at(per * it + per + 1);
             if (tc::elect()) {
-#pragma unroll
+#pragma unroll 4
               for (int kk = 0; kk < D / 16; ++kk)
                 tc::mma_ss<S::RB>(tm + S::cP, dx + kstep(kk, S::kBox), dy + kstep(kk, S::kBox), id_p, kk > 0);
               tc::commit(bar_qk);
