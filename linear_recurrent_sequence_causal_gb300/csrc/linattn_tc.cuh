@@ -12,26 +12,26 @@
 // Three terms go in two steps of 64 tokens at d >= 64, so that they need no more shared memory.
 //
 // Roles.  The last warp copies the x, y and z tiles by TMA into a ring of 5 tiles at d = 128 (4 at
-// 64, 6 below); the one before issues the MMAs; A turns P into bf16 scores in place in TMEM,
-// splits y, and writes the outputs; B keeps the state (for D < 128 the MMA repeats Z^T down its
-// 128 rows, and the warps share the columns of a row) and sends the outputs by TMA.  The chain
-// from chunk to chunk is U -> state -> O2; the scores of the next chunk, its copies and this
-// chunk's outputs run beside it.
+// 64, 6 below); the one before issues the MMAs; A turns P into bf16 scores in place in TMEM and
+// splits y; B keeps the state (for D < 128 the MMA repeats Z^T down its 128 rows, and the warps
+// share the columns of a row), writes the outputs to a tile and sends them by TMA.  The chain
+// from chunk to chunk is U -> state -> O2; the scores and the split of the next chunk, its copies
+// and this chunk's outputs run beside it.
 //
-// What bounds it at d = 128: a chunk takes about 5500 cycles, alone on the GPU or not (16 or 128
-// heads of 4096 tokens: 102 and 106 us with two terms), so neither DRAM nor its latency.  It moves 576 KB through
-// shared memory (operands of the MMAs 288, copies in 96, the split of y 96, S 32, outputs 64),
-// 4600 cycles at 128 bytes a cycle.  The tensor core alone would need 2600 cycles, DRAM 3900 for an SM's
-// share of its rate.  Tried without gain: four more warps for the split (5900 cycles a chunk, for its terms
-// then wait for their tile), A's operand kept in the tensor core for the second term of U, the
-// split shared with B, sixteen warps in A.  One term instead of two would save 96 KB a chunk
-// and is not taken: two keep the state's error below that of S's rounding.
-// The element-wise work is latency and instruction fetch: hence eight warps in A, no long-lived
-// registers there, and short loops (unrolled and with four warps each in A and B a chunk took 18 000 cycles).
-// Measured, d = 128: 8 x 4096 tokens, 16 heads: 124 us, 4.4 TB/s (three terms in the heads that
-// remember most of the sequence; two: 106 us); its gradient 283 us; 65536 tokens, 32 heads:
-// the runs' states 134 us, the passes 400 us.  d = 32, 512 x 200 tokens, 2 heads: 28 us, of which 1.7 us is each
-// CTA's set-up.
+// What bounds it at d = 128: a chunk takes about 5300 cycles, alone on the GPU or not (16 or 128
+// heads of 4096 tokens: 107 and 108 us with two terms), so neither DRAM nor its latency.  It moves
+// 576 KB through shared memory (operands of the MMAs 288, copies in 96, the split of y 96, S 32,
+// outputs 64): 4600 cycles at 128 bytes a cycle.  The tensor core alone would need 2600, an SM's
+// share of DRAM 3900.  One term instead of two would save 96 KB a chunk and is not taken: two keep
+// the state's error below that of S's rounding.
+// The element-wise work is latency and instruction fetch: hence eight warps in A, few registers
+// there, and short loops (unrolled and with four warps each in A and B a chunk took 18 000 cycles).
+// Slower or no faster: warps of their own for the split, sixteen warps in A or in B, the split
+// shared with B, outputs by A (8 x 4096 tokens 121 us instead of 114) or by both (118), A's operand
+// of U kept in the tensor core for the second term, polling instead of sleeping in A and B.
+// Measured, d = 128: 8 x 4096 tokens, 16 heads: 114 us, 4.8 TB/s; its gradient 284 us; 65536
+// tokens, 32 heads: the runs' states 133 us, the passes 389 us.  d = 32, 512 x 200 tokens, 2
+// heads: 28 us.
 //
 // Tiles lie in shared memory as TMA writes them with a swizzle as wide as a row (32, 64, 128
 // bytes; D = 128 is two boxes of 64 columns): K-major as X, Y and S are read, MN-major as Z
@@ -220,10 +220,10 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(sm + S::oBar);
   uint64_t* bar_empty = bar_full + SLOTS;
   uint64_t* bar_qk = bar_empty + SLOTS;      // P is there
-  uint64_t* bar_p = bar_qk + 1;              // its bf16 scores are, and O of the last chunk is read
+  uint64_t* bar_p = bar_qk + 1;              // its bf16 scores are
   uint64_t* bar_o = bar_qk + 2;              // O1 and O2 are there
   uint64_t* bar_z = bar_qk + 3;              // padding rows of y and z are zeros (once a sequence)
-  uint64_t* bar_out = bar_qk + 4;            // the outputs are in shared memory
+  uint64_t* bar_out = bar_qk + 4;            // the outputs are in shared memory, O is read
   uint64_t* bar_sent = bar_qk + 5;           // and have been read there
   uint64_t* bar_end = bar_qk + 6;            // every MMA issued is done
   // two each, used in turn, so that a role that is a chunk behind still tells the phases apart
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       tc::bar_init(bar_r + i, WB);
     }
     tc::bar_init(bar_z, WA);
-    tc::bar_init(bar_out, WA);
+    tc::bar_init(bar_out, WB);
     tc::bar_init(bar_sent, 1);
     tc::bar_init(bar_end, 1);
     tc::bar_fence_init();
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         int r0 = 0;
         for (uint32_t polls = 0; (need_pv || need_xs || need_qk || need_u) && ok; ++polls) {
           bool moved = false;
-          if (need_pv && landed(tz) && done(bar_p, it)) {
+          if (need_pv && landed(tz) && done(bar_p, it) && (it == 0 || done(bar_out, it - 1))) {
             tc::fence_after();
             const uint32_t dz = d_ring + at(tz);
             if (tc::elect()) {
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             need_pv = false;
             moved = true;
           }
-          // (A has read O of the last chunk when its scores are there, so O2 comes after PV too)
+          // (after PV: then O of the last chunk is read)
           if (need_xs && !need_pv && done(bar_s + it % 2, it / 2)) {
             tc::fence_after();
             const uint32_t dx = d_ring + at(ty - 1);
@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       ok &= tc::bar_wait_long(bar_end, 0);
     }
   } else if (warp < WA) {
-    // ---- A: scores, the terms of y, outputs ----
-    constexpr int PA = WA / 4, JB = 4 / PA, CO = D / PA, G = CO < 16 ? CO : 16;
+    // ---- A: scores, the terms of y ----
+    constexpr int PA = WA / 4, JB = 4 / PA;
     const int i = (warp & 3) * 32 + lane, part = warp >> 2;  // token of the chunk, part of the columns
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(jb.out) + ((size_t)b * p.T * p.H + h) * D;
@@ -552,39 +552,6 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         __syncwarp();
         if (lane == 0) tc::bar_arrive(bar_y + step % 2);
       }
-      if (!full || !ok) continue;
-      // the outputs, as a tile that B sends by TMA (an SM's own stores leave at about 20 bytes a
-      // cycle, which held A for 1500 cycles a chunk at d = 128); padding rows are zeros
-      const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
-      const uint64_t g2 = pack2(g, g);
-      if (!wait(bar_o, it)) break;
-#pragma unroll 1
-      for (int c = part * CO; c < (part + 1) * CO; c += G) {
-        uint32_t a[G], e[G];
-        tc::lda(lanes + S::cO1 + c, a);
-        tc::lda(lanes + S::cO2 + c, e);
-        tc::wait_ld(a, e);
-#pragma unroll
-        for (int k = 0; k < G; k += 8) {
-          uint32_t o[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int j = k + 2 * q;
-            float x, y;
-            unpack2(fma2(g2, pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
-                                 pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
-                        x, y);
-            o[q] = tc::bf2(x, y);
-          }
-          const uint32_t off = (uint32_t)((c + k) / 64) * S::kBox + i * S::RB + (c + k) % 64 * 2;
-          *reinterpret_cast<uint4*>(sm + S::oOut + (off ^ ((off >> 3) & (S::RB - 16)))) =
-              i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
-        }
-      }
-      tc::fence_smem_to_async();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(bar_out);
     }
     if (full) {
       // chunks of padding: zeros, shared out over the runs
@@ -597,7 +564,11 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     constexpr int NS = S::NS;
     const int wb = warp - WA;
     const uint32_t lanes = tmem + ((uint32_t)((wb & 3) * 32) << 16);
-    const int row = ((wb & 3) * 32 + lane) % D;              // row of S (TMEM lane l holds row l % D)
+    // columns of the outputs of a warp, and at once (beside 64 registers of state 16 would spill: 129 us
+    // instead of 114 for 8 x 4096 tokens)
+    constexpr int CO = D / (WB / 4), GO = D == 128 ? 8 : CO < 16 ? CO : 16;
+    const int i = (wb & 3) * 32 + lane;                      // token of the chunk
+    const int row = i % D;                                   // row of S (TMEM lane l holds row l % D)
     const int y0 = (D == 128 ? wb >> 2 : D == 64 ? wb >> 1 : wb) * NS;
     const bool mine = D >= 32 || lane < D;                   // D = 16: lanes 16.. repeat
     float rows_st[1][NS];
@@ -615,16 +586,50 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     for (int it = -1; it < nch; ++it) {
       float2 ln = make_float2(1.f, 0.f);
       if (it >= 0) {
-        if (full && wb == 0) {                               // send this chunk's outputs
-          if (!wait(bar_out, it)) break;
-          if (lane == 0) {
-            for (uint32_t x = 0; x < S::NB; ++x)
-              tc::tma_store_4d(&args.out[job], sm + S::oOut + x * S::kBox, x * 64, h, first(it), b);
-            tc::bulk_commit();
-          }
-          __syncwarp();
-        }
         const int n = count(first(it));
+        if (full) {
+          // the outputs, as a tile that goes by TMA (an SM's own stores leave at about 20 bytes a cycle:
+          // 1500 cycles a chunk at d = 128); padding rows are zeros
+          const float g = i < n ? jb.so * pw[rev ? n - 1 - i : i + 1] : 0.f;
+          const uint64_t g2 = pack2(g, g);
+          if (!wait(bar_o, it)) break;
+#pragma unroll 1
+          for (int c = (wb >> 2) * CO; c < ((wb >> 2) + 1) * CO; c += GO) {
+            uint32_t a[GO], e[GO];
+            tc::lda(lanes + S::cO1 + c, a);
+            tc::lda(lanes + S::cO2 + c, e);
+            tc::wait_ld(a, e);
+#pragma unroll
+            for (int k = 0; k < GO; k += 8) {
+              uint32_t o[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int j = k + 2 * q;
+                float x, y;
+                unpack2(fma2(g2, pack2(__uint_as_float(e[j]), __uint_as_float(e[j + 1])),
+                                     pack2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))),
+                            x, y);
+                o[q] = tc::bf2(x, y);
+              }
+              const uint32_t off = (uint32_t)((c + k) / 64) * S::kBox + i * S::RB + (c + k) % 64 * 2;
+              *reinterpret_cast<uint4*>(sm + S::oOut + (off ^ ((off >> 3) & (S::RB - 16)))) =
+                  i < n ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
+            }
+          }
+          tc::fence_smem_to_async();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(bar_out);
+          if (wb == 0) {
+            if (!wait(bar_out, it)) break;
+            if (lane == 0) {
+              for (uint32_t x = 0; x < S::NB; ++x)
+                tc::tma_store_4d(&args.out[job], sm + S::oOut + x * S::kBox, x * 64, h, first(it), b);
+              tc::bulk_commit();
+            }
+            __syncwarp();
+          }
+        }
         ln = n == C ? whole : dc.step(n);
         if (!wait(bar_u + it % 2, it / 2)) break;
       }
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             }
             __syncwarp();
           }
-          if (!wait(S::kOutS ? bar_sent : bar_o, it)) break;
+          if (S::kOutS && !wait(bar_sent, it)) break;
         }
       }
       if (!full) continue;

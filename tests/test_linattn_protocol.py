@@ -36,8 +36,7 @@ class Model:
         self.steps, self.ragged = steps, ragged                 # steps a chunk; the ragged chunk or -1
         b = self.b = {k: Bar(1) for k in ("qk", "o", "sent", "end")}
         self.wa, self.wb = 2, 2
-        for k in ("p", "z", "out"):
-            b[k] = Bar(self.wa)
+        b["p"], b["z"], b["out"] = Bar(self.wa), Bar(self.wa), Bar(self.wb)
         for i in (0, 1):
             b["t", i], b["u", i], b["y", i] = Bar(1), Bar(1), Bar(self.wa)
             b["s", i], b["r", i] = Bar(self.wb), Bar(self.wb)
@@ -126,7 +125,7 @@ class Model:
             last = c - 1 if self.full else c - 2
             while pv or xs or qk or u:
                 yield
-                if pv and landed(ty + 1) and self.b["p"].passed(c):
+                if pv and landed(ty + 1) and self.b["p"].passed(c) and (c == 0 or self.b["out"].passed(c - 1)):
                     self.issue(("pv", c))
                     pv = False
                 if xs and not pv and self.b["s", c % 2].passed(c // 2):
@@ -180,27 +179,29 @@ class Model:
                 yield
                 self.b["y", step % 2].arrive()
                 step += 1
-            if not self.full:
-                continue
-            yield from self.wait("o", c)
-            where = "S" if self.out_s else "out"
-            old = self.hold.get(where)
-            assert old in (None, ("used", c), ("sent", c - 1), ("part out", c)), f"{where} is overwritten: {old}"
-            if w == 0:
-                self.want("O1", ("O", c))
-                self.want("O2", ("O", c))
-            done = self.split.setdefault(("O", c), set())
-            done.add(w)
-            self.put(where, ("out" if len(done) == self.wa else "part out", c))
-            if len(done) == self.wa:
-                self.put("O1", ("read", c))
-                self.put("O2", ("read", c))
-            yield
-            self.b["out"].arrive()
+
+    def outputs(self, w, c):
+        yield from self.wait("o", c)
+        where = "S" if self.out_s else "out"
+        old = self.hold.get(where)
+        assert old in (None, ("used", c), ("sent", c - 1), ("part out", c)), f"{where} is overwritten: {old}"
+        if w == 0:
+            self.want("O1", ("O", c))
+            self.want("O2", ("O", c))
+        done = self.split.setdefault(("O", c), set())
+        done.add(w)
+        self.put(where, ("out" if len(done) == self.wb else "part out", c))
+        if len(done) == self.wb:
+            self.put("O1", ("read", c))
+            self.put("O2", ("read", c))
+        yield
+        self.b["out"].arrive()
 
     def b_warp(self, w):
         for c in range(-1, self.n):
             if c >= 0:
+                if self.full:
+                    yield from self.outputs(w, c)
                 if self.full and w == 0:
                     yield from self.wait("out", c)
                     self.want("S" if self.out_s else "out", ("out", c))
@@ -222,7 +223,8 @@ class Model:
                             yield
                         self.b["sent"].arrive()
                         yield
-                    yield from self.wait("sent" if self.out_s else "o", c)
+                    if self.out_s:
+                        yield from self.wait("sent", c)
             if self.full:
                 old = self.hold.get("S")
                 ok = (None, ("part state", c + 1), ("sent", c)) if self.out_s else (None, ("part state", c + 1), ("used", c))
