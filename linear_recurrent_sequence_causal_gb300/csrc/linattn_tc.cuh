@@ -499,8 +499,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         const int back = full ? 1 : 2;
         if (step >= back && !wait(bar_t + (step - back) % 2, (step - back) / 2)) break;
         // 16-byte pieces of the rows of this step, two of a thread loaded before the first is
-        // stored (behind it they waited: 290 -> 283 us for the gradient of 8 x 4096 tokens, 16 heads of 128).  Rows past
-        // n hold zeros, or are in no K-step.
+        // stored (behind the store the second load waited: 290 us instead of 283 for the gradient
+        // of 8 x 4096 tokens, 16 heads of 128).  Rows past n hold zeros, or are in no K-step.
         constexpr int RI = WA * 32 * 16 / S::RB;             // rows that A takes at once
         constexpr int PF = S::NB == 1 && S::kRows3 > RI ? 2 : 1;
         const int r1 = r0 + tid / (S::RB / 16);
