@@ -73,9 +73,9 @@ struct LinattnTc {
   static constexpr uint32_t oPow = oRing + SLOTS * kTile + (kOutS ? 0 : kMid);   // lambda^k at k + C, 0 for k < 0
   static constexpr uint32_t oApart = oPow + (2 * C + 4) * 4;    // sp lambda^|x| at x = i - j + C, 0 on the masked side
   static constexpr uint32_t oBar = oApart + (2 * C + 4) * 4;
-  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 17) * 8 + 8;
-  // TMEM columns.  D = 64: U takes the half of P that the bf16 scores leave free, so that two
-  // CTAs share an SM's 512 columns.
+  static constexpr uint32_t bytes = oBar + (2 * SLOTS + 18) * 8 + 8;
+  // TMEM columns.  D = 64: U takes P's columns 64..127, the second half of the bf16 scores (64..95)
+  // among them, once PV has read those, so that two CTAs share an SM's 512 columns.
   static constexpr bool kShareU = D == 64;
   static constexpr uint32_t cP = 0, cO1 = 128, cO2 = 128 + D, cU = kShareU ? 64 : 128 + 2 * D;
   static constexpr uint32_t kCols = D == 128 ? 512 : 256;
@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   uint64_t* bar_y = bar_qk + 11;             // [2] a step's terms of Yd are in shared memory
   uint64_t* bar_s = bar_qk + 13;             // [2] S is in shared memory
   uint64_t* bar_r = bar_qk + 15;             // [2] a chunk's U is read
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 17) * 8);
+  uint64_t* bar_pv = bar_qk + 17;            // PV is done: its scores are read
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::oBar + (2 * SLOTS + 18) * 8);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int job = blockIdx.x % p.njobs, item = blockIdx.x / p.njobs;   // a head's passes share its tiles in L2
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     tc::bar_init(bar_out, WB);
     tc::bar_init(bar_sent, 1);
     tc::bar_init(bar_end, 1);
+    tc::bar_init(bar_pv, 1);
     tc::bar_fence_init();
     tc::fence_smem_to_async();
   }
@@ -346,8 +348,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       // What a chunk needs issued, each as soon as its operands are there: PV (scores x Z), XS (X x
       // state), U's steps, and QK, the next chunk's scores.  (In a fixed order one late operand, the
       // state after a long sum or a tile on its way, held back all that follow: 5700 cycles a
-      // chunk at d = 128.)  Products on one accumulator, and a product and the ones that overwrite
-      // its operands in TMEM, stay in order because the tensor core runs them in order.
+      // chunk at d = 128.)  Products of one shape on one accumulator run in the order of their issue;
+      // no other two do, so what overwrites PV's scores (QK, and U where it lies in P) waits for bar_pv.
       int step = 0;                                          // steps of Yd so far
       for (int it = full ? -1 : 0; it < steps && ok; ++it) {
         const int ty = per * it + per - 2, tz = ty + 1;
@@ -367,6 +369,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
 #pragma unroll 2
               for (int kk = 0; kk < ks; ++kk)
                 tc::mma_ts<S::RB>(tm + S::cO1, tm + S::score(kk), dz + kk * kStepMn, id_o, kk > 0);
+              tc::commit(bar_pv);
             }
             __syncwarp();
             need_pv = false;
@@ -387,9 +390,10 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             need_xs = false;
             moved = true;
           }
-          // (over P: behind PV; where U lies in P, behind U's last step and its reading)
-          if (need_qk && !need_pv && (!S::kShareU || it < 0 || (!need_u && done(bar_r + it % 2, it / 2))) &&
-              landed(per * it + per) && landed(per * it + per + 1) && (!z1 || done(bar_z, 0))) {
+          // (over P: after PV; where U lies in P, after U's last step and its reading)
+          if (need_qk && !need_pv && (it < 0 || done(bar_pv, it)) &&
+              (!S::kShareU || it < 0 || (!need_u && done(bar_r + it % 2, it / 2))) && landed(per * it + per) &&
+              landed(per * it + per + 1) && (!z1 || done(bar_z, 0))) {
             tc::fence_after();
             const uint32_t dx = d_ring + at(per * it + per), dy = d_ring + at(per * it + per + 1);
             if (tc::elect()) {
@@ -405,7 +409,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           // U: alone, the states have two places for terms and for U, so that a chunk's split, its
           // products and the last one's sum run at the same time
           const int last = full ? it - 1 : it - 2;           // the chunk whose U lies there
-          if (need_u && !need_pv && done(bar_y + step % 2, step / 2) && (last < 0 || r0 > 0 || done(bar_r + last % 2, last / 2)) &&
+          if (need_u && !need_pv && (!S::kShareU || !full || done(bar_pv, it)) && done(bar_y + step % 2, step / 2) &&
+              (last < 0 || r0 > 0 || done(bar_r + last % 2, last / 2)) &&
               (full || (landed(tz) && (!z0 || done(bar_z, 0))))) {
             tc::fence_after();
             const uint32_t dz = d_zt + at(tz) + (r0 / 16) * kStepMn, dy = d_ring + at(ty) + (r0 / 16) * kStepMn;
