@@ -4,6 +4,11 @@ Argument checks and marshalling only, as in ``prism``: the work runs in libprism
 kernels, and a missing library raises.  Token inputs (q, k, v and the gradients that come in)
 are [B,T,H,D] tensors whose heads are contiguous; sequences and tokens may be strided, so
 slices of one fused projection serve as they are.  Everything else is contiguous.
+
+A call runs on ``stream`` (default: the current one), ordered after what is there already.  Where
+that is not the current stream, what the call allocates comes from that stream's memory, and
+the tensors of the call are recorded on the streams that use them, so that none is handed out
+again before its kernels are done.
 """
 from __future__ import annotations
 
@@ -101,13 +106,48 @@ def _strided(name, t):
     return t.data_ptr()
 
 
-def _out(t):
-    """A contiguous tensor of t's shape and type."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
 def _stream(t, stream):
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
+    """The handle of the call's stream, and the stream itself where it is not the current one."""
+    if not t.is_cuda:
+        raise PrismError(1, "q must be a CUDA tensor")
+    here = torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream is None or stream.cuda_stream == here:
+        return here, None
+    return stream.cuda_stream, stream
+
+
+def _scratch(nbytes, device, side):
+    """Memory for this call alone.  It goes back to the stream that it came from: the call's own."""
+    if side is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(side):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _new(shape, dtype, device, side):
+    """An output: written on the call's stream, read by the caller on the current one."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(caller)
+    return t
+
+
+def _out(t, side):
+    """A contiguous tensor of t's shape and type."""
+    if side is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _new(t.shape, t.dtype, t.device, side)
+
+
+def _used(side, *tensors):
+    """The call's tensors, which may be dropped once it returns, are used on its stream."""
+    if side is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(side)
 
 
 # The checked dims of a call by shapes, strides and settings: a layer calls with the same ones
@@ -166,17 +206,19 @@ def prism_qk_norm_rope(q, k, table, *, q_weight=None, k_weight=None, q_scale=1.0
         raise PrismError(1, f"q and k must have one type, got {dt} and {k.dtype}")
     keep, dims, _ = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape, interleaved,
                             eps, q_scale, k_scale, None, None)
+    raw, side = _stream(q, stream)
+    _used(side, q, k, table, q_weight, k_weight, positions, seq_lens, q_out, k_out)
     if q_out is None:
-        q_out = _out(q)
+        q_out = _out(q, side)
     if k_out is None:
-        k_out = _out(k)
+        k_out = _out(k, side)
     D = qs[3:]
     _check(load().prism_qk_norm_rope(
         dims, _strided("q", q), _strided("k", k), _whole("q_weight", q_weight, D, torch.float32),
         _whole("k_weight", k_weight, D, torch.float32),
         None if table is None else _whole("table", table, table.shape, torch.float32),
         _whole("positions", positions, qs[:2], torch.int32), _whole("seq_lens", seq_lens, qs[:1], torch.int32),
-        _whole("q_out", q_out, qs, dt), _whole("k_out", k_out, ks, dt), _stream(q, stream)))
+        _whole("q_out", q_out, qs, dt), _whole("k_out", k_out, ks, dt), raw))
     return q_out, k_out
 
 
@@ -193,13 +235,15 @@ def prism_qk_norm_rope_backward(q, k, table, dq_out, dk_out, *, q_weight=None, k
     _like("dk_out", dk_out, ks, dt)
     keep, dims, nbytes = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape,
                                  interleaved, eps, q_scale, k_scale, dq_out.stride(), dk_out.stride())
-    dev, D = q.device, qs[3:]
+    raw, side = _stream(q, stream)
+    D = qs[3:]
     g = dict(grads) if grads else {}
+    _used(side, q, k, table, dq_out, dk_out, q_weight, k_weight, positions, seq_lens, workspace, *g.values())
     for n, t in (("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight)):
         if g.get(n) is None:
-            g[n] = None if t is None else _out(t)
+            g[n] = None if t is None else _out(t, side)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _scratch(nbytes, q.device, side)
     _check(load().prism_qk_norm_rope_backward(
         dims, _strided("q", q), _strided("k", k), _whole("q_weight", q_weight, D, torch.float32),
         _whole("k_weight", k_weight, D, torch.float32),
@@ -208,7 +252,7 @@ def prism_qk_norm_rope_backward(q, k, table, dq_out, dk_out, *, q_weight=None, k
         _strided("dq_out", dq_out), _strided("dk_out", dk_out), _whole("grads['q']", g["q"], qs, dt),
         _whole("grads['k']", g["k"], ks, dt), _whole("grads['q_weight']", g["q_weight"], D, torch.float32),
         _whole("grads['k_weight']", g["k_weight"], D, torch.float32), workspace.data_ptr(), workspace.numel(),
-        _stream(q, stream)))
+        raw))
     return g
 
 
@@ -226,20 +270,22 @@ def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, 
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
     keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), None)
+    raw, side = _stream(q, stream)
     ss = _state_shape(qs)
+    _used(side, q, k, v, log_decay, initial_state, out, final_state, seq_lens, workspace)
     if out is None:
-        out = _out(q)
+        out = _out(q, side)
     if final_state is None and want_state:
-        final_state = torch.empty(ss, dtype=torch.float32, device=q.device)
+        final_state = _new(ss, torch.float32, q.device, side)
     if workspace is None and nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(nbytes, q.device, side)
     _check(load().prism_linattn_forward(
         dims, _strided("q", q), _strided("k", k), _strided("v", v),
         _whole("log_decay", log_decay, qs[2:3], torch.float32),
         _whole("initial_state", initial_state, ss, torch.float32), _whole("out", out, qs, dt),
         _whole("final_state", final_state, ss, torch.float32), _whole("seq_lens", seq_lens, qs[:1], torch.int32),
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        _stream(q, stream)))
+        raw))
     return out, final_state
 
 
@@ -253,15 +299,17 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
     _like("v", v, qs, dt)
     _like("d_out", d_out, qs, dt)
     keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), d_out.stride())
-    ss, dev = _state_shape(qs), q.device
+    raw, side = _stream(q, stream)
+    ss = _state_shape(qs)
     g = dict(grads) if grads else {}
+    _used(side, q, k, v, log_decay, d_out, initial_state, d_final_state, seq_lens, workspace, *g.values())
     for n, t in (("q", q), ("k", k), ("v", v)):
         if g.get(n) is None:
-            g[n] = _out(t)
+            g[n] = _out(t, side)
     if g.get("initial_state") is None:
-        g["initial_state"] = None if initial_state is None else torch.empty(ss, dtype=torch.float32, device=dev)
+        g["initial_state"] = None if initial_state is None else _new(ss, torch.float32, q.device, side)
     if workspace is None and nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _scratch(nbytes, q.device, side)
     _check(load().prism_linattn_backward(
         dims, _strided("q", q), _strided("k", k), _strided("v", v),
         _whole("log_decay", log_decay, qs[2:3], torch.float32),
@@ -271,7 +319,7 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
         _whole("grads['initial_state']", g["initial_state"], ss, torch.float32),
         _whole("seq_lens", seq_lens, qs[:1], torch.int32),
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        _stream(q, stream)))
+        raw))
     return g
 
 
@@ -283,14 +331,16 @@ def prism_linattn_decode_step(q, k, v, log_decay, state, *, scale=1.0, slots=Non
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
     keep, dims = _decode_dims(qs, dt, scale, q.stride(), k.stride(), v.stride())
+    raw, side = _stream(q, stream)
     N = state.shape[0]
+    _used(side, q, k, v, log_decay, state, slots, out)
     if out is None:
-        out = _out(q)
+        out = _out(q, side)
     _check(load().prism_linattn_decode_step(
         dims, _strided("q", q), _strided("k", k), _strided("v", v),
         _whole("log_decay", log_decay, qs[1:2], torch.float32),
         _whole("state", state, (N, qs[1], qs[2], qs[2]), torch.float32), N,
-        _whole("slots", slots, qs[:1], torch.int32), _whole("out", out, qs, dt), _stream(q, stream)))
+        _whole("slots", slots, qs[:1], torch.int32), _whole("out", out, qs, dt), raw))
     return out
 
 
