@@ -3,7 +3,8 @@
 Argument checks and marshalling only, as in ``prism``: the work runs in libprism.so's
 kernels, and a missing library raises.  Token inputs (q, k, v and the gradients that come in)
 are [B,T,H,D] tensors whose heads are contiguous; sequences and tokens may be strided, so
-slices of one fused projection serve as they are.  Everything else is contiguous.
+slices of one fused projection serve as they are.  Everything else is contiguous.  All tensors of a
+call lie on q's device, which need not be the current one.
 
 A call runs on ``stream`` (default: the current one), ordered after what is there already.  Where
 that is not the current stream, what the call allocates comes from that stream's memory, and
@@ -89,31 +90,53 @@ def _like(name, t, shape, dtype):
         raise PrismError(1, f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
 
 
-def _whole(name, t, shape, dtype):
-    """The address of an optional contiguous tensor of this shape and type."""
+def _whole(name, t, shape, dtype, dev):
+    """The address of an optional contiguous tensor of this shape and type on device ``dev``."""
     if t is None:
         return None
     if t.dtype != dtype or t.shape != shape:
         raise PrismError(1, f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise PrismError(1, f"{name} must be a contiguous CUDA tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise PrismError(1, f"{name} must be a contiguous CUDA tensor on q's device")
     return t.data_ptr()
 
 
-def _strided(name, t):
-    if not t.is_cuda:
-        raise PrismError(1, f"{name} must be a CUDA tensor")
+def _strided(name, t, dev):
+    if t.get_device() != dev:
+        raise PrismError(1, f"{name} must be a CUDA tensor on q's device")
     return t.data_ptr()
+
+
+def _room(t, dev):
+    """Address and bytes of an optional workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise PrismError(1, "workspace must be a contiguous CUDA tensor on q's device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _stream(t, stream):
-    """The handle of the call's stream, and the stream itself where it is not the current one."""
-    if not t.is_cuda:
+    """The call's device, the handle of its stream, and the stream itself where it is not the
+    device's current one."""
+    dev = t.get_device()
+    if dev < 0:
         raise PrismError(1, "q must be a CUDA tensor")
-    here = torch._C._cuda_getCurrentRawStream(t.get_device())
-    if stream is None or stream.cuda_stream == here:
-        return here, None
-    return stream.cuda_stream, stream
+    here = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is None:
+        return dev, here, None
+    if stream.device.index != dev:
+        raise PrismError(1, f"stream is on device {stream.device.index}, q on device {dev}")
+    return dev, stream.cuda_stream, None if stream.cuda_stream == here else stream
+
+
+def _call(dev, f, *args):
+    """f on device ``dev``: the library launches on the current one."""
+    if torch._C._cuda_getDevice() == dev:
+        _check(f(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args))
 
 
 def _scratch(nbytes, device, side):
@@ -144,10 +167,9 @@ def _out(t, side):
 
 def _used(side, *tensors):
     """The call's tensors, which may be dropped once it returns, are used on its stream."""
-    if side is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(side)
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(side)
 
 
 # The checked dims of a call by shapes, strides and settings: a layer calls with the same ones
@@ -206,19 +228,20 @@ def prism_qk_norm_rope(q, k, table, *, q_weight=None, k_weight=None, q_scale=1.0
         raise PrismError(1, f"q and k must have one type, got {dt} and {k.dtype}")
     keep, dims, _ = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape, interleaved,
                             eps, q_scale, k_scale, None, None)
-    raw, side = _stream(q, stream)
-    _used(side, q, k, table, q_weight, k_weight, positions, seq_lens, q_out, k_out)
+    dev, raw, side = _stream(q, stream)
+    if side is not None:
+        _used(side, q, k, table, q_weight, k_weight, positions, seq_lens, q_out, k_out)
     if q_out is None:
         q_out = _out(q, side)
     if k_out is None:
         k_out = _out(k, side)
     D = qs[3:]
-    _check(load().prism_qk_norm_rope(
-        dims, _strided("q", q), _strided("k", k), _whole("q_weight", q_weight, D, torch.float32),
-        _whole("k_weight", k_weight, D, torch.float32),
-        None if table is None else _whole("table", table, table.shape, torch.float32),
-        _whole("positions", positions, qs[:2], torch.int32), _whole("seq_lens", seq_lens, qs[:1], torch.int32),
-        _whole("q_out", q_out, qs, dt), _whole("k_out", k_out, ks, dt), raw))
+    _call(
+        dev, load().prism_qk_norm_rope, dims, _strided("q", q, dev), _strided("k", k, dev),
+        _whole("q_weight", q_weight, D, torch.float32, dev), _whole("k_weight", k_weight, D, torch.float32, dev),
+        None if table is None else _whole("table", table, table.shape, torch.float32, dev),
+        _whole("positions", positions, qs[:2], torch.int32, dev), _whole("seq_lens", seq_lens, qs[:1], torch.int32, dev),
+        _whole("q_out", q_out, qs, dt, dev), _whole("k_out", k_out, ks, dt, dev), raw)
     return q_out, k_out
 
 
@@ -235,24 +258,24 @@ def prism_qk_norm_rope_backward(q, k, table, dq_out, dk_out, *, q_weight=None, k
     _like("dk_out", dk_out, ks, dt)
     keep, dims, nbytes = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape,
                                  interleaved, eps, q_scale, k_scale, dq_out.stride(), dk_out.stride())
-    raw, side = _stream(q, stream)
+    dev, raw, side = _stream(q, stream)
     D = qs[3:]
     g = dict(grads) if grads else {}
-    _used(side, q, k, table, dq_out, dk_out, q_weight, k_weight, positions, seq_lens, workspace, *g.values())
+    if side is not None:
+        _used(side, q, k, table, dq_out, dk_out, q_weight, k_weight, positions, seq_lens, workspace, *g.values())
     for n, t in (("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight)):
         if g.get(n) is None:
             g[n] = None if t is None else _out(t, side)
     if workspace is None:
         workspace = _scratch(nbytes, q.device, side)
-    _check(load().prism_qk_norm_rope_backward(
-        dims, _strided("q", q), _strided("k", k), _whole("q_weight", q_weight, D, torch.float32),
-        _whole("k_weight", k_weight, D, torch.float32),
-        None if table is None else _whole("table", table, table.shape, torch.float32),
-        _whole("positions", positions, qs[:2], torch.int32), _whole("seq_lens", seq_lens, qs[:1], torch.int32),
-        _strided("dq_out", dq_out), _strided("dk_out", dk_out), _whole("grads['q']", g["q"], qs, dt),
-        _whole("grads['k']", g["k"], ks, dt), _whole("grads['q_weight']", g["q_weight"], D, torch.float32),
-        _whole("grads['k_weight']", g["k_weight"], D, torch.float32), workspace.data_ptr(), workspace.numel(),
-        raw))
+    _call(
+        dev, load().prism_qk_norm_rope_backward, dims, _strided("q", q, dev), _strided("k", k, dev),
+        _whole("q_weight", q_weight, D, torch.float32, dev), _whole("k_weight", k_weight, D, torch.float32, dev),
+        None if table is None else _whole("table", table, table.shape, torch.float32, dev),
+        _whole("positions", positions, qs[:2], torch.int32, dev), _whole("seq_lens", seq_lens, qs[:1], torch.int32, dev),
+        _strided("dq_out", dq_out, dev), _strided("dk_out", dk_out, dev), _whole("grads['q']", g["q"], qs, dt, dev),
+        _whole("grads['k']", g["k"], ks, dt, dev), _whole("grads['q_weight']", g["q_weight"], D, torch.float32, dev),
+        _whole("grads['k_weight']", g["k_weight"], D, torch.float32, dev), *_room(workspace, dev), raw)
     return g
 
 
@@ -270,22 +293,22 @@ def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, 
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
     keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), None)
-    raw, side = _stream(q, stream)
+    dev, raw, side = _stream(q, stream)
     ss = _state_shape(qs)
-    _used(side, q, k, v, log_decay, initial_state, out, final_state, seq_lens, workspace)
+    if side is not None:
+        _used(side, q, k, v, log_decay, initial_state, out, final_state, seq_lens, workspace)
     if out is None:
         out = _out(q, side)
     if final_state is None and want_state:
         final_state = _new(ss, torch.float32, q.device, side)
     if workspace is None and nbytes:
         workspace = _scratch(nbytes, q.device, side)
-    _check(load().prism_linattn_forward(
-        dims, _strided("q", q), _strided("k", k), _strided("v", v),
-        _whole("log_decay", log_decay, qs[2:3], torch.float32),
-        _whole("initial_state", initial_state, ss, torch.float32), _whole("out", out, qs, dt),
-        _whole("final_state", final_state, ss, torch.float32), _whole("seq_lens", seq_lens, qs[:1], torch.int32),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        raw))
+    _call(
+        dev, load().prism_linattn_forward, dims, _strided("q", q, dev), _strided("k", k, dev),
+        _strided("v", v, dev), _whole("log_decay", log_decay, qs[2:3], torch.float32, dev),
+        _whole("initial_state", initial_state, ss, torch.float32, dev), _whole("out", out, qs, dt, dev),
+        _whole("final_state", final_state, ss, torch.float32, dev), _whole("seq_lens", seq_lens, qs[:1], torch.int32, dev),
+        *_room(workspace, dev), raw)
     return out, final_state
 
 
@@ -299,10 +322,11 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
     _like("v", v, qs, dt)
     _like("d_out", d_out, qs, dt)
     keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), d_out.stride())
-    raw, side = _stream(q, stream)
+    dev, raw, side = _stream(q, stream)
     ss = _state_shape(qs)
     g = dict(grads) if grads else {}
-    _used(side, q, k, v, log_decay, d_out, initial_state, d_final_state, seq_lens, workspace, *g.values())
+    if side is not None:
+        _used(side, q, k, v, log_decay, d_out, initial_state, d_final_state, seq_lens, workspace, *g.values())
     for n, t in (("q", q), ("k", k), ("v", v)):
         if g.get(n) is None:
             g[n] = _out(t, side)
@@ -310,16 +334,15 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
         g["initial_state"] = None if initial_state is None else _new(ss, torch.float32, q.device, side)
     if workspace is None and nbytes:
         workspace = _scratch(nbytes, q.device, side)
-    _check(load().prism_linattn_backward(
-        dims, _strided("q", q), _strided("k", k), _strided("v", v),
-        _whole("log_decay", log_decay, qs[2:3], torch.float32),
-        _whole("initial_state", initial_state, ss, torch.float32), _strided("d_out", d_out),
-        _whole("d_final_state", d_final_state, ss, torch.float32), _whole("grads['q']", g["q"], qs, dt),
-        _whole("grads['k']", g["k"], qs, dt), _whole("grads['v']", g["v"], qs, dt),
-        _whole("grads['initial_state']", g["initial_state"], ss, torch.float32),
-        _whole("seq_lens", seq_lens, qs[:1], torch.int32),
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        raw))
+    _call(
+        dev, load().prism_linattn_backward, dims, _strided("q", q, dev), _strided("k", k, dev),
+        _strided("v", v, dev), _whole("log_decay", log_decay, qs[2:3], torch.float32, dev),
+        _whole("initial_state", initial_state, ss, torch.float32, dev), _strided("d_out", d_out, dev),
+        _whole("d_final_state", d_final_state, ss, torch.float32, dev), _whole("grads['q']", g["q"], qs, dt, dev),
+        _whole("grads['k']", g["k"], qs, dt, dev), _whole("grads['v']", g["v"], qs, dt, dev),
+        _whole("grads['initial_state']", g["initial_state"], ss, torch.float32, dev),
+        _whole("seq_lens", seq_lens, qs[:1], torch.int32, dev),
+        *_room(workspace, dev), raw)
     return g
 
 
@@ -331,16 +354,17 @@ def prism_linattn_decode_step(q, k, v, log_decay, state, *, scale=1.0, slots=Non
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
     keep, dims = _decode_dims(qs, dt, scale, q.stride(), k.stride(), v.stride())
-    raw, side = _stream(q, stream)
+    dev, raw, side = _stream(q, stream)
     N = state.shape[0]
-    _used(side, q, k, v, log_decay, state, slots, out)
+    if side is not None:
+        _used(side, q, k, v, log_decay, state, slots, out)
     if out is None:
         out = _out(q, side)
-    _check(load().prism_linattn_decode_step(
-        dims, _strided("q", q), _strided("k", k), _strided("v", v),
-        _whole("log_decay", log_decay, qs[1:2], torch.float32),
-        _whole("state", state, (N, qs[1], qs[2], qs[2]), torch.float32), N,
-        _whole("slots", slots, qs[:1], torch.int32), _whole("out", out, qs, dt), raw))
+    _call(
+        dev, load().prism_linattn_decode_step, dims, _strided("q", q, dev), _strided("k", k, dev),
+        _strided("v", v, dev), _whole("log_decay", log_decay, qs[1:2], torch.float32, dev),
+        _whole("state", state, (N, qs[1], qs[2], qs[2]), torch.float32, dev), N,
+        _whole("slots", slots, qs[:1], torch.int32, dev), _whole("out", out, qs, dt, dev), raw)
     return out
 
 

@@ -10,7 +10,7 @@ import types
 import pytest
 import torch
 
-from linear_recurrent_sequence_causal_gb300 import linattn
+from linear_recurrent_sequence_causal_gb300 import linattn, prism
 
 
 class Stream:
@@ -145,3 +145,46 @@ def test_the_current_stream_by_name(world, call):
     x = operands()
     CALLS[call](x, stream=Stream(0))
     assert world.calls[0][1][-1] == 0 and all(t.noted == () and t.home == 0 for t in world.made)
+
+
+OPERANDS = {"rope": ("k", "table", "w", "pos", "lens"), "rope_backward": ("k", "table", "w", "pos", "lens", "do"),
+            "forward": ("k", "v", "ld", "s", "lens"), "backward": ("k", "v", "ld", "do", "s", "ds", "lens"),
+            "decode": ("ld", "s", "slots")}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_one_device(world, call):
+    """An operand on another device, or on none, is refused before anything is launched."""
+    for n in OPERANDS[call]:
+        for wrong in (lambda t: gpu(t, index=1), lambda t: t.as_subclass(torch.Tensor)):
+            x = operands()
+            setattr(x, n, wrong(getattr(x, n)))
+            for side in (None, Stream(0x51de)):
+                with pytest.raises(prism.PrismError):
+                    CALLS[call](x, stream=side)
+    with pytest.raises(prism.PrismError):
+        CALLS[call](operands(), stream=Stream(0x51de, device=1))
+    assert not world.calls
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_tensors_device_is_made_current(world, call):
+    """With all tensors on device 1 while device 0 is current, the library is called with 1 current."""
+    x = operands()
+    for n, t in vars(x).items():
+        t.index = 1
+    CALLS[call](x)
+    (_, _, device), = world.calls
+    assert device == 1 and not world.devices
+
+
+@pytest.mark.parametrize("call", ["rope_backward", "forward", "backward"])
+def test_workspaces(world, call):
+    """A workspace that is elsewhere, or smaller than its element count says, is refused; its size is in bytes."""
+    plain = torch.zeros(8192, dtype=torch.uint8)
+    for wrong in (plain, gpu(plain.clone(), index=1), gpu(plain.clone()[::2]), gpu(plain[:1].clone().expand(8192))):
+        with pytest.raises(prism.PrismError):
+            CALLS[call](operands(), workspace=wrong)
+    assert not world.calls
+    CALLS[call](operands(), workspace=gpu(torch.zeros(1024)))
+    assert 4096 in world.calls[0][1]
