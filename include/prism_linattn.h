@@ -92,8 +92,10 @@ typedef struct {
 /* Prompts, in chunks: out [B,T,H,d] in dtype; final_state [B,H,d_v,d_k] fp32 (NULL: not
  * written) after each sequence's last token; initial_state (NULL: zero) before its first.
  *   log_decay  [H] fp32, <= 0 (-inf: no memory at all)
- * A non-finite value makes the outputs of its own chunk of tokens non-finite, not only the
- * later ones.  Sums and states are fp32.  In PRISM_BF16 the products run on the tensor
+ * A non-finite value reaches what comes after it (outputs, in the gradients what comes after in their
+ * own direction, and states) as in the recurrence, and nothing before it.  What has decayed below
+ * 2^-126, fp32's smallest normal number, may count as nothing, a non-finite value's share
+ * as well.  Sums and states are fp32.  In PRISM_BF16 the products run on the tensor
  * cores: scores and the state that a chunk reads are rounded to bf16 once, the state's
  * own update keeps 16 bits of the decayed key (two bf16 terms). */
 PRISM_API size_t prism_linattn_workspace_bytes(const prism_linattn_dims* dims);

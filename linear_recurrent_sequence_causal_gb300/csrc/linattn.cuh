@@ -329,6 +329,20 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
       for (int e = 0; e < 2; ++e) {
         const int i = ti + e;
         if (i >= n) continue;
+        // A masked score is 0, and 0 times a NaN or an infinity is not: where a sum is not finite, it is
+        // taken again over the tokens that the output may see.
+        uint64_t nan2 = 0;                           // stays 0 where all are finite
+#pragma unroll
+        for (int f = 0; f < NP; ++f) nan2 = fma2(o[e][f], 0, nan2);
+        float nx, ny;
+        unpack2(nan2, nx, ny);
+        if (nx + ny != 0.f) {
+#pragma unroll
+          for (int f = 0; f < NP; ++f) o[e][f] = 0;
+#pragma unroll 1
+          for (int j = jb.rev ? i : 0; j < (jb.rev ? n : i + 1); ++j)
+            linattn_axpy<NC>(o[e], sp[i * LP + j], sz + j * LZ + tj * NC);
+        }
         const float g = jb.so * dc.pow(jb.rev ? n - 1 - i : i + 1);
         float v[2 * NP];
 #pragma unroll
