@@ -83,7 +83,7 @@ typedef struct {
     int B, T, H;
     int d;                 /* d_k = d_v: 16, 32, 64 or 128 */
     prism_dtype dtype;     /* type of q, k, v, out and their gradients */
-    unsigned flags;        /* 0 */
+    unsigned flags;        /* 0 or PRISM_FLAG_CHECK_WAIT_TIMEOUT */
     float scale;
     long long q_stride[2], k_stride[2], v_stride[2];
     long long do_stride[2];                 /* of d_out (backward) */
@@ -130,7 +130,13 @@ PRISM_API int prism_linattn_decode_step(const prism_linattn_dims* dims, const vo
  * bounded; one that gives up sets the library's word for the current device, which stays
  * set until it is cleared.  Synchronises the device and returns the word in *word (0: no
  * wait gave up), clearing it when `clear` is nonzero.  PRISM_ERR_INVALID_ARG for a NULL
- * word, PRISM_ERR_CUDA when the synchronisation or the copy fails. */
+ * word, PRISM_ERR_CUDA when the synchronisation or the copy fails.
+ *
+ * A wait's limit is about a second.  PRISM_FLAG_CHECK_WAIT_TIMEOUT in dims->flags is a diagnostic
+ * of this path: in prism_linattn_forward and _backward on the PRISM_BF16 path (it is ignored on
+ * PRISM_F32 and refused by prism_linattn_decode_step) the copies of every CTA with tokens first
+ * wait, for a millisecond, for what never comes, and give up.  The roles that wait for them
+ * follow after their second, the call returns, the word is set and its outputs are undefined. */
 PRISM_API int prism_linattn_status(int* word, int clear);
 
 #ifdef __cplusplus

@@ -52,6 +52,7 @@ struct LinattnArgs {
   int phase;                              // 0: full passes; 1: the runs' own states into seg
   float* seg;                             // [njobs][B][H][nseg - 1][D][D]
   int* status;                            // bounded waits (bf16 path)
+  int give_up;                            // check of the failure path: a wait that runs out
 };
 
 struct LinattnDecodeArgs {

@@ -86,10 +86,10 @@ int fill_rope(const prism_rope_dims* d, const void* q, const void* k, const floa
 
 // ---- linear attention ----
 
-int check_linattn(const prism_linattn_dims* d) {
+int check_linattn(const prism_linattn_dims* d, unsigned flags = PRISM_FLAG_CHECK_WAIT_TIMEOUT) {
   if (!d) return PRISM_ERR_INVALID_ARG;
   if (d->dtype != PRISM_F32 && d->dtype != PRISM_BF16) return PRISM_ERR_INVALID_ARG;
-  if (d->B <= 0 || d->T <= 0 || d->H <= 0 || d->d <= 0 || d->flags) return PRISM_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->T <= 0 || d->H <= 0 || d->d <= 0 || (d->flags & ~flags)) return PRISM_ERR_INVALID_ARG;
   if (!good_head_dim(d->d)) return PRISM_ERR_UNSUPPORTED;
   if ((long long)d->B * d->T > (1LL << 31) - 1 || (long long)d->B * d->H > (1LL << 22)) return PRISM_ERR_UNSUPPORTED;
   return PRISM_OK;
@@ -181,6 +181,7 @@ int run_linattn(const prism_linattn_dims* d, prism::LinattnArgs& a, const Operan
   a.log_decay = log_decay; a.seq_lens = seq_lens;
   a.seg = static_cast<float*>(workspace);
   a.status = nullptr;
+  a.give_up = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d->dtype == PRISM_F32) return prism::launch_linattn_fma(d->d, a, s) == cudaSuccess ? PRISM_OK : PRISM_ERR_LAUNCH;
   void* word = nullptr;
@@ -338,7 +339,7 @@ extern "C" PRISM_API int prism_linattn_backward(const prism_linattn_dims* dims, 
 extern "C" PRISM_API int prism_linattn_decode_step(const prism_linattn_dims* dims, const void* q, const void* k,
                                                    const void* v, const float* log_decay, float* state,
                                                    int n_states, const int32_t* slots, void* out, void* stream) {
-  int rc = check_linattn(dims);
+  int rc = check_linattn(dims, 0);
   if (rc != PRISM_OK) return rc;
   if (dims->T != 1 || n_states <= 0 || (!slots && n_states < dims->B)) return PRISM_ERR_INVALID_ARG;
   if (!log_decay) return PRISM_ERR_INVALID_ARG;

@@ -107,19 +107,26 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn_major, bool b
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
-// tc::bar_wait with the polls asleep for up to 20 us each (a second in all): a waiting warp takes
-// no issue slots from the working ones.
-__device__ __forceinline__ bool bar_wait_long(uint64_t* bar, uint32_t parity) {
-  for (uint32_t it = 0; it < 50000u; ++it) {
+// tc::bar_wait with `limit` polls that sleep for up to kPollNs each: a waiting warp takes no issue
+// slots from the working ones.
+constexpr uint32_t kPollNs = 20000u, kWaitPolls = 50000u;            // a second in all
+constexpr uint32_t kWaitCycles = 2000000000u;          // the same where polls do not sleep
+__device__ __forceinline__ bool bar_wait_long(uint64_t* bar, uint32_t parity, uint32_t limit = kWaitPolls) {
+  for (uint32_t it = 0; it < limit; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kPollNs)
         : "memory");
     if (ok) return true;
   }
   return false;
+}
+__device__ __forceinline__ uint32_t clock_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %clock;\n" : "=r"(t));
+  return t;
 }
 __device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -371,7 +378,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
   const uint32_t tmem = warp == WA + WB + 1 ? 0 : *tslot;
   const uint32_t base = tc::smem_addr(sm);
   bool ok = true;
-  // after a wait that gave up a role issues no more work and ends
+  // After a wait that gave up a role issues no more work and ends; the others' waits for it give up
+  // too.  What it still has in flight it waits for before the CTA ends.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = tc::bar_wait_long(bar, parity & 1);
     tc::fence_after();
@@ -382,7 +390,9 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     // ---- copies ----
     if (lane == 0) {
       int tile = 0;
-      for (; tile < nch * per; ++tile) {
+      // the failure path's check: a wait for what never comes, since nothing has been copied
+      if (p.give_up && nch > 0) ok = tc::bar_wait_long(bar_empty, 0, 50);
+      for (; tile < nch * per && ok; ++tile) {
         const int s = tile % SLOTS, which = full ? tile % 3 : tile % 2 + 1;
         const CUtensorMap* m = &args.map[which == 0 ? jb.xi : which == 1 ? jb.yi : jb.zi];
         if (tile >= SLOTS && !(ok = tc::bar_wait_long(bar_empty + s, (tile / SLOTS - 1) & 1))) break;
@@ -391,7 +401,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
           tc::tma_load_4d(sm + S::oRing + s * S::kTile + x * S::kBox, m, x * 64, h, first(tile / per), b, bar_full + s);
       }
       // a copy still in flight may not outlive the CTA
-      for (int i = max(tile - SLOTS, 0); i < tile; ++i) ok &= tc::bar_wait_long(bar_full + i % SLOTS, (i / SLOTS) & 1);
+      for (int i = max(tile - SLOTS, 0); i < tile; ++i)
+        ok &= tc::bar_wait_long(bar_full + i % SLOTS, (i / SLOTS) & 1);
     }
   } else if (warp == WA + WB) {
     // ---- MMAs: the whole warp runs, one lane issues ----
@@ -427,6 +438,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
         const bool z1 = it + 1 < steps && ragged(u0, count(u0)), z0 = !full && ragged(t0, n);
         bool need_pv = full && it >= 0, need_xs = need_pv, need_qk = full && it + 1 < steps, need_u = it >= 0;
         int r0 = 0;
+        uint32_t since = 0;
         for (uint32_t polls = 0; (need_pv || need_xs || need_qk || need_u) && ok; ++polls) {
           bool moved = false;
           if (need_pv && landed(tz) && done(bar_p, it) && (it == 0 || done(bar_out, it - 1))) {
@@ -506,7 +518,11 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
             moved = true;
           }
           if (moved) polls = 0;
-          if (polls > (1u << 22)) ok = false;                // seconds without an operand
+          if (polls >= 1024u) {                              // these polls do not sleep: the limit is in cycles
+            const uint32_t t = tc::clock_lo();
+            if (polls == 1024u) since = t;
+            ok = __all_sync(0xffffffffu, t - since <= tc::kWaitCycles);
+          }
         }
       }
       if (tc::elect()) tc::commit(bar_end);

@@ -191,10 +191,10 @@ def _rope_dims(qs, qst, ks, kst, dtype, table_shape, interleaved, eps, q_scale, 
 
 
 @functools.lru_cache(maxsize=256)
-def _linattn_dims(qs, dtype, scale, qst, kst, vst, dost):
+def _linattn_dims(qs, dtype, scale, qst, kst, vst, dost, flags=0):
     if len(qs) != 4:
         raise PrismError(1, f"q, k and v must be [B,T,H,D], got {tuple(qs)}")
-    d = LinattnDims(B=qs[0], T=qs[1], H=qs[2], d=qs[3], dtype=_dtype_code(dtype), flags=0, scale=scale,
+    d = LinattnDims(B=qs[0], T=qs[1], H=qs[2], d=qs[3], dtype=_dtype_code(dtype), flags=flags, scale=scale,
                     q_stride=_steps("q", qs, qst), k_stride=_steps("k", qs, kst), v_stride=_steps("v", qs, vst))
     if dost is not None:
         d.do_stride = _steps("d_out", qs, dost)
@@ -284,7 +284,7 @@ def _state_shape(qs):
 
 
 def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, out=None, final_state=None,
-                          seq_lens=None, workspace=None, stream=None, want_state=True):
+                          seq_lens=None, workspace=None, stream=None, want_state=True, flags=0):
     """Causal linear attention over q, k, v [B,T,H,D] with the decay exp(log_decay[h]) a token:
     S_t = exp(log_decay) S_(t-1) + v_t k_t^T, o_t = scale S_t q_t, S_0 = ``initial_state``
     [B,H,D,D] fp32 (None: zero).  Returns ``(out, final_state)``: out [B,T,H,D] in q's type,
@@ -292,7 +292,7 @@ def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, 
     qs, dt = q.shape, q.dtype
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
-    keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), None)
+    keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), None, flags)
     dev, raw, side = _stream(q, stream)
     ss = _state_shape(qs)
     if side is not None:
@@ -313,7 +313,7 @@ def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, 
 
 
 def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_state=None, d_final_state=None,
-                           seq_lens=None, grads=None, workspace=None, stream=None):
+                           seq_lens=None, grads=None, workspace=None, stream=None, flags=0):
     """Gradients through prism_linattn_forward given ``d_out`` [B,T,H,D] in q's type (and
     ``d_final_state`` [B,H,D,D] fp32).  Returns a dict: q, k, v in their type and initial_state
     fp32 (None where there was none).  ``grads`` may pass preallocated outputs."""
@@ -321,7 +321,7 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
     _like("d_out", d_out, qs, dt)
-    keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), d_out.stride())
+    keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), d_out.stride(), flags)
     dev, raw, side = _stream(q, stream)
     ss = _state_shape(qs)
     g = dict(grads) if grads else {}
