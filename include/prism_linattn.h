@@ -96,8 +96,9 @@ typedef struct {
  * own direction, and states) as in the recurrence, and nothing before it.  What has decayed below
  * 2^-126, fp32's smallest normal number, may count as nothing, a non-finite value's share
  * as well.  Sums and states are fp32.  In PRISM_BF16 the products run on the tensor
- * cores: scores and the state that a chunk reads are rounded to bf16 once, the state's
- * own update keeps 16 bits of the decayed key (two bf16 terms). */
+ * cores: scores and the state that a chunk reads are rounded to bf16 once; the state's own
+ * update keeps 16 bits of the decayed key (two bf16 terms), and 24 (three) in the tokens that
+ * final_state, or the backward pass's d_initial_state, remembers by more than a quarter. */
 PRISM_API size_t prism_linattn_workspace_bytes(const prism_linattn_dims* dims);
 PRISM_API int prism_linattn_forward(const prism_linattn_dims* dims, const void* q, const void* k,
                                     const void* v, const float* log_decay,
