@@ -476,13 +476,21 @@ __global__ void __launch_bounds__(128) linattn_decode_kernel(LinattnDecodeArgs p
   }
 #pragma unroll
   for (int i = 0; i < NR; ++i) vv[i] = Elem<E>::to_f(v[i * GR]);
-  const float la = expf(__ldg(p.log_decay + h));
+  // lambda in two terms, as in Decay::step: one rounding of it would be the same in every token
+  // (2e-4 of the state after 4096 tokens at lambda = 1 - 2^-12)
+  const float ld = __ldg(p.log_decay + h);
+  float la = expf(ld), lb = 0.f;
+  if (ld > -0.5f && ld < 0.5f) {
+    const float e = expm1f(ld);
+    la = 1.f + e;
+    lb = e - (la - 1.f);
+  }
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    s[i].x = fmaf(la, s[i].x, vv[i] * kv[0]);
-    s[i].y = fmaf(la, s[i].y, vv[i] * kv[1]);
-    s[i].z = fmaf(la, s[i].z, vv[i] * kv[2]);
-    s[i].w = fmaf(la, s[i].w, vv[i] * kv[3]);
+    s[i].x = fmaf(la, s[i].x, fmaf(lb, s[i].x, vv[i] * kv[0]));
+    s[i].y = fmaf(la, s[i].y, fmaf(lb, s[i].y, vv[i] * kv[1]));
+    s[i].z = fmaf(la, s[i].z, fmaf(lb, s[i].z, vv[i] * kv[2]));
+    s[i].w = fmaf(la, s[i].w, fmaf(lb, s[i].w, vv[i] * kv[3]));
     __stcs(reinterpret_cast<float4*>(st + (size_t)i * GR * D), s[i]);
     o[i] = fmaf(s[i].x, qv[0], fmaf(s[i].y, qv[1], fmaf(s[i].z, qv[2], s[i].w * qv[3])));
   }
