@@ -161,6 +161,35 @@ def _stream_ptr(stream):
     return s.cuda_stream
 
 
+def _beside(stream, device):
+    """``stream`` where it is not the current one of the device, else None."""
+    if stream is None or device.type != "cuda":
+        return None
+    return None if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream else stream
+
+
+def _empty(shape, dtype, device, side, returned=True):
+    """Memory that a call on the stream ``side`` (None: the current one) writes.  It comes from that
+    stream, so that no earlier work elsewhere still uses it, and what the caller gets is recorded
+    on the current stream."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(caller)
+    return t
+
+
+def _used(side, *tensors):
+    """The call's tensors, which may be dropped once it returns, are used on its stream."""
+    if side is not None:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(side)
+
+
 def workspace_layout(dims: Dims) -> dict:
     """Byte offsets of the workspace regions (None where absent)."""
     offs = (ctypes.c_size_t * len(WS_REGIONS))()
@@ -178,6 +207,14 @@ def alloc_workspace(dims: Dims, device) -> torch.Tensor:
     return torch.empty(max(workspace_bytes(dims), 1), dtype=torch.uint8, device=device)
 
 
+def _workspace(dims: Dims, device, side):
+    """alloc_workspace for one call, dropped when it returns."""
+    if side is None:
+        return alloc_workspace(dims, device)
+    with torch.cuda.stream(side):
+        return alloc_workspace(dims, device)
+
+
 def debug_bounds(clear: bool = True):
     """The debug build's word of out-of-bounds accesses (0: none; synchronises the
     device), or None when the loaded library is the normal build."""
@@ -193,7 +230,9 @@ def debug_activation(x: torch.Tensor, stream=None) -> torch.Tensor:
     """GELU of the fp32 device tensor ``x`` as the bf16 prepare kernel evaluates it."""
     if x.dtype != torch.float32:
         raise PrismError(1, "x must be fp32")
-    y = torch.empty_like(x)
+    side = _beside(stream, x.device)
+    _used(side, x)
+    y = torch.empty_like(x) if side is None else _empty(x.shape, x.dtype, x.device, side)
     _check(load().prism_debug_activation(_ptr(x), _ptr(y), x.numel(), _stream_ptr(stream)))
     return y
 
@@ -226,12 +265,14 @@ def prism_forward(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, chunk, *, 
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dims = _dims_for(q, v, conv_w, L, chunk, no_gelu, flags)
+    side = _beside(stream, q.device)
+    _used(side, q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, out, final_state, seq_lens, workspace)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float32, device=q.device)
+        out = _empty((B, T, H, dv), torch.float32, q.device, side)
     if final_state is None and want_state:
-        final_state = torch.empty((B, H, dv, dk), dtype=torch.float32, device=q.device)
+        final_state = _empty((B, H, dv, dk), torch.float32, q.device, side)
     if workspace is None:
-        workspace = alloc_workspace(dims, q.device)
+        workspace = _workspace(dims, q.device, side)
     rc = load().prism_forward(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                               _ptr(beta), _ptr(conv_w), _ptr(Wk), _ptr(Wp), _ptr(wbeta),
                               _ptr(out), _ptr(final_state), _ptr(seq_lens), _ptr(workspace),
@@ -251,12 +292,15 @@ def prism_forward_from(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, chunk
     dv = v.shape[-1]
     dims = _dims_for(q, v, conv_w, L, chunk, no_gelu,
                      (PRISM_FLAG_VHIST_TOKEN_MAJOR if v_hist_token_major else 0) | flags)
+    side = _beside(stream, q.device)
+    _used(side, q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, initial_state, v_hist, out,
+          final_state, seq_lens, workspace)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float32, device=q.device)
+        out = _empty((B, T, H, dv), torch.float32, q.device, side)
     if final_state is None and want_state:
-        final_state = torch.empty((B, H, dv, dk), dtype=torch.float32, device=q.device)
+        final_state = _empty((B, H, dv, dk), torch.float32, q.device, side)
     if workspace is None:
-        workspace = alloc_workspace(dims, q.device)
+        workspace = _workspace(dims, q.device, side)
     rc = load().prism_forward_from(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                                    _ptr(beta), _ptr(conv_w), _ptr(Wk), _ptr(Wp), _ptr(wbeta),
                                    _ptr(initial_state), _ptr(v_hist), _ptr(out), _ptr(final_state),
@@ -282,16 +326,18 @@ def prism_backward(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, d_out, *,
               "beta": (B, T, H), "conv_w": tuple(conv_w.shape)}
     if L > 0:
         shapes.update(Wk=(H, L, dk, dv), Wp=(H, L, dv, dv), wbeta=(H, L, dv))
+    side = _beside(stream, dev)
+    _used(side, q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, d_out, d_final_state, seq_lens, workspace, *g.values())
     for n, shp in shapes.items():
         if g.get(n) is None:
-            g[n] = torch.empty(shp, dtype=torch.float32, device=dev)
+            g[n] = _empty(shp, torch.float32, dev, side)
     for n in ("Wk", "Wp", "wbeta"):
         g.setdefault(n, None)
     if workspace is None:
         nbytes = load().prism_backward_workspace_bytes(ctypes.byref(dims))
         if nbytes == 0:
             raise PrismError(2, "prism_backward_workspace_bytes rejected the dims")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(nbytes, torch.uint8, dev, side, returned=False)
     rc = load().prism_backward(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                                _ptr(beta), _ptr(conv_w), _ptr(Wk), _ptr(Wp), _ptr(wbeta),
                                _ptr(d_out), _ptr(d_final_state), _ptr(g["q"]), _ptr(g["k"]),
@@ -310,8 +356,10 @@ def prism_decode_step(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, state,
     B, H, dk = q.shape
     dv = v.shape[-1]
     dims = make_dims(B, 1, H, dk, dv, conv_w.shape[1], L, 16, q.dtype, no_gelu)
+    side = _beside(stream, q.device)
+    _used(side, q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, state, v_hist, out)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=torch.float32, device=q.device)
+        out = _empty((B, H, dv), torch.float32, q.device, side)
     rc = load().prism_decode_step(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                                   _ptr(beta), _ptr(conv_w), _ptr(Wk), _ptr(Wp), _ptr(wbeta),
                                   _ptr(state), _ptr(v_hist), _ptr(out), _stream_ptr(stream))
@@ -342,10 +390,12 @@ def prism_forward_static(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, chu
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dims = _dims_for(q, v, conv_w, L, chunk, no_gelu, flags)
+    side = _beside(stream, q.device)
+    _used(side, q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, out, final_state, seq_lens)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float32, device=q.device)
+        out = _empty((B, T, H, dv), torch.float32, q.device, side)
     if final_state is None and want_state:
-        final_state = torch.empty((B, H, dv, dk), dtype=torch.float32, device=q.device)
+        final_state = _empty((B, H, dv, dk), torch.float32, q.device, side)
     rc = load().prism_forward_static(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v),
                                      _ptr(log_alpha), _ptr(beta), _ptr(conv_w), _ptr(Wk), _ptr(Wp),
                                      _ptr(wbeta), _ptr(out), _ptr(final_state), _ptr(seq_lens),
@@ -357,6 +407,7 @@ def prism_forward_static(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, chu
 def prism_prepare(q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, L, chunk, workspace, *,
                   seq_lens=None, stream=None, no_gelu=False, flags=0):
     """State-independent stage into ``workspace`` (see include/prism.h)."""
+    _used(_beside(stream, q.device), q, k, v, log_alpha, beta, conv_w, Wk, Wp, wbeta, workspace, seq_lens)
     dims = _dims_for(q, v, conv_w, L, chunk, no_gelu, flags)
     rc = load().prism_prepare(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                               _ptr(beta), _ptr(conv_w), _ptr(Wk), _ptr(Wp), _ptr(wbeta),
@@ -373,10 +424,12 @@ def prism_scan(q, k, v, log_alpha, beta, L, chunk, conv_width, workspace, *, out
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dims = make_dims(B, T, H, dk, dv, conv_width, L, chunk, q.dtype, no_gelu, flags)
+    side = _beside(stream, q.device)
+    _used(side, q, k, v, log_alpha, beta, out, final_state, seq_lens, workspace)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float32, device=q.device)
+        out = _empty((B, T, H, dv), torch.float32, q.device, side)
     if final_state is None and want_state:
-        final_state = torch.empty((B, H, dv, dk), dtype=torch.float32, device=q.device)
+        final_state = _empty((B, H, dv, dk), torch.float32, q.device, side)
     rc = load().prism_scan(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
                            _ptr(beta), _ptr(seq_lens), _ptr(workspace), workspace.numel(),
                            _ptr(out), _ptr(final_state), _stream_ptr(stream))
