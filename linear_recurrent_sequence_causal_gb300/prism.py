@@ -153,6 +153,8 @@ def _ptr(t):
         return None
     if not t.is_cuda or not t.is_contiguous():
         raise PrismError(1, "tensors must be contiguous CUDA tensors")
+    if t.get_device() != torch._C._cuda_getDevice():       # the library launches there
+        raise PrismError(1, "tensors must be on the current device")
     return t.data_ptr()
 
 

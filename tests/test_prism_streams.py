@@ -19,6 +19,7 @@ class World:
         names = ("float32", "bfloat16", "uint8", "dtype", "Tensor")
         fake = types.SimpleNamespace(**{n: getattr(torch, n) for n in names}, empty=self.empty,
                                      empty_like=lambda t: self.empty(t.shape, dtype=t.dtype, device=t.device))
+        fake._C = types.SimpleNamespace(_cuda_getDevice=lambda: 0)
         fake.cuda = types.SimpleNamespace(stream=self.on, current_stream=lambda d=None: self.now)
         monkeypatch.setattr(prism, "torch", fake)
         monkeypatch.setattr(prism, "load", lambda: self)
@@ -94,3 +95,19 @@ def test_the_current_stream(world, call, stream):
     CALLS[call](x, stream=stream)
     assert world.calls[0][1][-1] == 0
     assert all(t.noted == () and t.home == 0 for t in (*world.made, *vars(x).values()))
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_current_device(world, call):
+    """The library launches on the current device: a tensor of another one is refused before that."""
+    for n in ("q", "q1", "s", "cw", "lens", "ws"):
+        x = operands()
+        getattr(x, n).index = 1
+        before = len(world.calls)
+        try:
+            CALLS[call](x)
+        except prism.PrismError:
+            assert len(world.calls) == before
+        else:
+            known = {a for a in world.calls[-1][1] if isinstance(a, int) and a > 1 << 16}
+            assert getattr(x, n).data_ptr() not in known, "launched with another device's memory"
