@@ -13,8 +13,9 @@
  * inputs may be strided: heads of one token are contiguous ([H, d]), and `stride` gives
  * the elements from one sequence to the next (stride[0]) and from one token to the next
  * (stride[1]), so that q, k and v may lie in one fused projection.  stride[1] = 0 stands for
- * a contiguous [B,T,H,d] tensor.  Strides are multiples of 16 bytes, at least 0, and
- * stride[1] is at least H*d.  Outputs are contiguous and may not overlap inputs.
+ * a contiguous [B,T,H,d] tensor.  Strides are multiples of 16 bytes; stride[0] is greater than 0 (a
+ * sequence expanded over a batch is refused) and stride[1] is at least H*d.  Outputs are
+ * contiguous and may not overlap inputs.
  *
  *   seq_lens [B] int32 or NULL: tokens t >= seq_lens[b] are padding, as in prism.h: their
  *   outputs and gradients are 0 and their values, NaN included, reach nothing.  Lengths

@@ -154,7 +154,8 @@ __device__ __forceinline__ void linattn_start(float (&st)[R][N], const LinattnAr
 // Bound by the shared-memory reads of the products and the waits between them, hence 4 x 4
 // tiles of S, 2 x 4 tiles of the output, packed arithmetic, and one CTA for all columns
 // where that fits (32-row slices with 2 x 2 tiles and no tiles ahead took 1.5 times as long).
-// 4 x 1021 tokens, 4 heads of 64, 8 runs: states 11 us, passes 28 us, which overlap to 33 us.
+// 4 x 1021 tokens, 4 heads of 64, 8 runs: 34 us replayed from a graph, the states and after them the
+// passes (12 and 30 us each by itself on cold caches, as the profiler runs them).
 template <int D_>
 struct LinattnFma {
   static constexpr int D = D_, C = 32, BZ = D < 64 ? D : 64, NSL = D / BZ, NT = 256;
@@ -414,7 +415,8 @@ __global__ void __launch_bounds__(256) linattn_fma_kernel(LinattnArgs p) {
 // its time (2 D^2 4 bytes a head; k, q, v and o are a D-th of that).  D/4 lanes hold 4
 // columns each of one row; a lane keeps NR rows' pieces in flight.  The rows' dot products
 // are summed over the lanes together: each exchange halves the rows that a lane still sums.
-// 256 x 16 heads of 128: 76 us, 6.9 TB/s; 8 x 16 heads: 5.4 us, a launch and one trip to DRAM.
+// 256 x 16 heads of 128: 76 us, 7.1 TB/s; 8 x 16 heads: 3.3 us replayed from a graph, a launch and one
+// trip to L2 (6.2 us on cold caches).
 template <int D_>
 struct LinattnDecode {
   static constexpr int D = D_, LR = D / 4;           // lanes per row

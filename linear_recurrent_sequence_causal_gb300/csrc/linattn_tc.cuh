@@ -18,20 +18,27 @@
 // from chunk to chunk is U -> state -> O2; the scores and the split of the next chunk, its copies
 // and this chunk's outputs run beside it.
 //
-// What bounds it at d = 128: a chunk takes about 5300 cycles, alone on the GPU or not (16 or 128
-// heads of 4096 tokens: 107 and 108 us with two terms), so neither DRAM nor its latency.  It moves
-// 576 KB through shared memory (operands of the MMAs 288, copies in 96, the split of y 96, S 32,
-// outputs 64): 4600 cycles at 128 bytes a cycle.  The tensor core alone would need 2600, an SM's
-// share of DRAM 3900.  One term instead of two would save 96 KB a chunk and is not taken: two keep
-// the state's error below that of S's rounding.
+// What it spends its time on at d = 128, 8 x 4096 tokens of 16 heads, by clock stamps: the SMs run at
+// 1.95 GHz; a CTA takes 200 000 cycles (103 us), the slowest, three terms in every chunk, 223 000 (115
+// us).  13 700 of them pass before the first outputs (set-up 2300, then copies and a chunk's
+// whole chain), 5700 are a chunk (6500 with three terms), 6000 come after the last.  Against a
+// chunk's 5700 stand 2600 of the tensor core, 5000 of DRAM at the copy rate for 128 CTAs at once, and
+// 576 KB through shared memory (operands of the MMAs 288, copies in 96, the split of y 96, S 32, outputs
+// 64), 4600 at 128 bytes a cycle.  The load/store pipe counts 2300 shared wavefronts a chunk where the
+// split, S and the outputs make 1280: 490 are bank conflicts, the rest (score weights one by one, the
+// waits' polls) has not been taken apart, and neither has what keeps a chunk above 5000.  One term
+// instead of two would save 96 KB a chunk and is not taken: two keep the state's error below that of
+// S's rounding.
 // The element-wise work is latency and instruction fetch: hence eight warps in A, few registers
 // there, and short loops (unrolled and with four warps each in A and B a chunk took 18 000 cycles).
 // Slower or no faster: warps of their own for the split, sixteen warps in A or in B, the split
 // shared with B, outputs by A (8 x 4096 tokens 121 us instead of 114) or by both (118), A's operand
 // of U kept in the tensor core for the second term, polling instead of sleeping in A and B.
-// Measured, d = 128: 8 x 4096 tokens, 16 heads: 114 us, 4.8 TB/s; its gradient 284 us; 65536
-// tokens, 32 heads: the runs' states 133 us, the passes 389 us.  d = 32, 512 x 200 tokens, 2
-// heads: 28 us.
+// Measured, replayed from a graph, d = 128: 8 x 4096 tokens, 16 heads: 117 us, 4.7 TB/s; its gradient
+// 296 us; 65536 tokens, 32 heads: 526 us (the runs' states 135 and the passes 400 each by itself).  d =
+// 32, 512 x 200 tokens, 2 heads: 26 us.
+// Registers (-Xptxas -v): 96 a thread at d = 128, 72 at 64 and 71 below; 28 bytes are spilled at d = 128,
+// 128 at 64 and none below.
 //
 // Tiles lie in shared memory as TMA writes them with a swizzle as wide as a row (32, 64, 128
 // bytes; D = 128 is two boxes of 64 columns): K-major as X, Y and S are read, MN-major as Z
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
       auto landed = [&](int tile) { return done(bar_full + tile % SLOTS, tile / SLOTS); };
       // What a chunk needs issued, each as soon as its operands are there: PV (scores x Z), XS (X x
       // state), U's steps, and QK, the next chunk's scores.  (In a fixed order one late operand, the
-      // state after a long sum or a tile on its way, held back all that follow: 5700 cycles a
+      // state after a long sum or a tile on its way, held back all that follow: 8 % more a
       // chunk at d = 128.)  Products of one shape on one accumulator run in the order of their issue;
       // no other two do, so what overwrites PV's scores (QK, and U where it lies in P) waits for bar_pv.
       int step = 0;                                          // steps of Yd so far
@@ -652,8 +659,8 @@ __global__ void __launch_bounds__(LinattnTc<D>::NT, LinattnTc<D>::kCtas)
     constexpr int NS = S::NS;
     const int wb = warp - WA;
     const uint32_t lanes = tmem + ((uint32_t)((wb & 3) * 32) << 16);
-    // columns of the outputs of a warp, and at once (beside 64 registers of state 16 would spill: 129 us
-    // instead of 114 for 8 x 4096 tokens)
+    // columns of the outputs of a warp, and at once (beside 64 registers of state 8 spill 28 bytes, and
+    // 16 so many that 8 x 4096 tokens took 129 us instead of 114)
     constexpr int CO = D / (WB / 4), GO = D == 128 ? 8 : CO < 16 ? CO : 16;
     const int i = (wb & 3) * 32 + lane;                      // token of the chunk
     const int row = i % D;                                   // row of S (TMEM lane l holds row l % D)

@@ -11,8 +11,9 @@
 // So the rotation needs no exchange between lanes and the norm only log2(D/8) shuffles.  A
 // lane group takes up to kRopeRows heads of one token: their loads are in flight together, and
 // the token's angles and the weights are read once for all of them.  Padding is not read.
-// Forward, 8 x 4096 tokens, 16 + 16 heads of 128, bf16: 89 us, 0.90 of the copy rate (95 us with
-// scalar arithmetic, which filled the issue slots; 91 us with four CTAs an SM).
+// Forward, 8 x 4096 tokens, 16 + 16 heads of 128, bf16: 88 us, 0.92 of the copy rate (95 us with
+// scalar arithmetic, which filled the issue slots; 91 us with four CTAs an SM: five leave 48 registers a
+// thread, of which the bf16 kernels spill 8 to 24 bytes, and are still faster).
 #pragma once
 
 #include "prism_common.cuh"
@@ -200,7 +201,8 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(E) == 2 ? 5 : 3) rope_ker
 // Backward.  A fixed grid walks the blocks of the queries, then of the keys; each lane sums
 // its 8 columns of dw over the rows that it sees, and the CTA writes one partial row a side.
 // The next block's x and dy come in while one is worked on, and the arithmetic is packed: 97 us at
-// the lm shape (8 x 4096 tokens, 16 + 4 heads of 128, bf16; 0.77 of the copy rate), 110 us
+// the lm shape (8 x 4096 tokens, 16 + 4 heads of 128, bf16; 0.77 of the copy rate; its 128 registers
+// spill 32 to 56 bytes in bf16), 110 us
 // with scalar arithmetic, 114 us with two heads a lane group, 124 us with 32 warps an SM and
 // no block ahead.  The sums' second kernel takes 7 us, half of it under the first one's end.
 constexpr int kRopeBackCtas = 2;                                      // resident per SM
