@@ -173,7 +173,8 @@ def _used(side, *tensors):
 
 
 # The checked dims of a call by shapes, strides and settings: a layer calls with the same ones
-# over and over.  The structures are only read afterwards.
+# over and over.  The structures are only read afterwards.  Settings are plain numbers here (a
+# tensor would be known by its identity, whatever value it holds later).
 
 @functools.lru_cache(maxsize=256)
 def _rope_dims(qs, qst, ks, kst, dtype, table_shape, interleaved, eps, q_scale, k_scale, dqst, dkst):
@@ -226,8 +227,8 @@ def prism_qk_norm_rope(q, k, table, *, q_weight=None, k_weight=None, q_scale=1.0
     qs, ks, dt = q.shape, k.shape, q.dtype
     if k.dtype != dt:
         raise PrismError(1, f"q and k must have one type, got {dt} and {k.dtype}")
-    keep, dims, _ = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape, interleaved,
-                            eps, q_scale, k_scale, None, None)
+    keep, dims, _ = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape,
+                               bool(interleaved), float(eps), float(q_scale), float(k_scale), None, None)
     dev, raw, side = _stream(q, stream)
     if side is not None:
         _used(side, q, k, table, q_weight, k_weight, positions, seq_lens, q_out, k_out)
@@ -257,7 +258,8 @@ def prism_qk_norm_rope_backward(q, k, table, dq_out, dk_out, *, q_weight=None, k
     _like("dq_out", dq_out, qs, dt)
     _like("dk_out", dk_out, ks, dt)
     keep, dims, nbytes = _rope_dims(qs, q.stride(), ks, k.stride(), dt, None if table is None else table.shape,
-                                 interleaved, eps, q_scale, k_scale, dq_out.stride(), dk_out.stride())
+                                    bool(interleaved), float(eps), float(q_scale), float(k_scale), dq_out.stride(),
+                                    dk_out.stride())
     dev, raw, side = _stream(q, stream)
     D = qs[3:]
     g = dict(grads) if grads else {}
@@ -292,7 +294,7 @@ def prism_linattn_forward(q, k, v, log_decay, *, scale=1.0, initial_state=None, 
     qs, dt = q.shape, q.dtype
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
-    keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), None, flags)
+    keep, dims, nbytes = _linattn_dims(qs, dt, float(scale), q.stride(), k.stride(), v.stride(), None, int(flags))
     dev, raw, side = _stream(q, stream)
     ss = _state_shape(qs)
     if side is not None:
@@ -321,7 +323,7 @@ def prism_linattn_backward(q, k, v, log_decay, d_out, *, scale=1.0, initial_stat
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
     _like("d_out", d_out, qs, dt)
-    keep, dims, nbytes = _linattn_dims(qs, dt, scale, q.stride(), k.stride(), v.stride(), d_out.stride(), flags)
+    keep, dims, nbytes = _linattn_dims(qs, dt, float(scale), q.stride(), k.stride(), v.stride(), d_out.stride(), int(flags))
     dev, raw, side = _stream(q, stream)
     ss = _state_shape(qs)
     g = dict(grads) if grads else {}
@@ -353,7 +355,7 @@ def prism_linattn_decode_step(q, k, v, log_decay, state, *, scale=1.0, slots=Non
     qs, dt = q.shape, q.dtype
     _like("k", k, qs, dt)
     _like("v", v, qs, dt)
-    keep, dims = _decode_dims(qs, dt, scale, q.stride(), k.stride(), v.stride())
+    keep, dims = _decode_dims(qs, dt, float(scale), q.stride(), k.stride(), v.stride())
     dev, raw, side = _stream(q, stream)
     N = state.shape[0]
     if side is not None:
