@@ -29,6 +29,11 @@ int check_pointers(const void* const (&required)[N], const void* const* optional
   return PRISM_OK;
 }
 
+// Arrays that are read by the word: log_decay, positions, seq_lens, slots.
+int check_words(const void* a, const void* b) {
+  return aligned(a, 4) && aligned(b, 4) ? PRISM_OK : PRISM_ERR_MISALIGNED;
+}
+
 int elem_bytes(prism_dtype t) { return t == PRISM_F32 ? 4 : 2; }
 bool good_head_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
@@ -231,6 +236,7 @@ extern "C" PRISM_API int prism_qk_norm_rope(const prism_rope_dims* dims, const v
   const void* req[] = {q, k, q_out, k_out};
   const void* opt[] = {q_weight, k_weight, table};
   if ((rc = check_pointers(req, opt, 3)) != PRISM_OK) return rc;
+  if ((rc = check_words(positions, seq_lens)) != PRISM_OK) return rc;
   prism::RopeArgs a;
   if ((rc = fill_rope(dims, q, k, q_weight, k_weight, table, positions, seq_lens, a)) != PRISM_OK) return rc;
   a.side[0].out = q_out;
@@ -258,6 +264,7 @@ extern "C" PRISM_API int prism_qk_norm_rope_backward(const prism_rope_dims* dims
   const void* req[] = {q, k, dq_out, dk_out, dq, dk};
   const void* opt[] = {q_weight, k_weight, table, dq_weight, dk_weight};
   if ((rc = check_pointers(req, opt, 5)) != PRISM_OK) return rc;
+  if ((rc = check_words(positions, seq_lens)) != PRISM_OK) return rc;
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
   if (!workspace || workspace_bytes < prism_qk_norm_rope_workspace_bytes(dims)) return PRISM_ERR_WORKSPACE;
   prism::RopeArgs a;
@@ -298,6 +305,7 @@ extern "C" PRISM_API int prism_linattn_forward(const prism_linattn_dims* dims, c
   const void* opt[] = {initial_state, final_state};
   if (!log_decay) return PRISM_ERR_INVALID_ARG;
   if ((rc = check_pointers(req, opt, 2)) != PRISM_OK) return rc;
+  if ((rc = check_words(log_decay, seq_lens)) != PRISM_OK) return rc;
   Operand in[3] = {{q, {0, 0}}, {k, {0, 0}}, {v, {0, 0}}};
   const long long* st[3] = {dims->q_stride, dims->k_stride, dims->v_stride};
   for (int i = 0; i < 3; ++i)
@@ -321,6 +329,7 @@ extern "C" PRISM_API int prism_linattn_backward(const prism_linattn_dims* dims, 
   const void* opt[] = {initial_state, d_final_state, d_initial_state};
   if (!log_decay) return PRISM_ERR_INVALID_ARG;
   if ((rc = check_pointers(req, opt, 3)) != PRISM_OK) return rc;
+  if ((rc = check_words(log_decay, seq_lens)) != PRISM_OK) return rc;
   Operand in[4] = {{q, {0, 0}}, {k, {0, 0}}, {v, {0, 0}}, {d_out, {0, 0}}};
   const long long* st[4] = {dims->q_stride, dims->k_stride, dims->v_stride, dims->do_stride};
   for (int i = 0; i < 4; ++i)
@@ -345,6 +354,7 @@ extern "C" PRISM_API int prism_linattn_decode_step(const prism_linattn_dims* dim
   if (!log_decay) return PRISM_ERR_INVALID_ARG;
   const void* req[] = {q, k, v, state, out};
   if ((rc = check_pointers(req, nullptr, 0)) != PRISM_OK) return rc;
+  if ((rc = check_words(log_decay, slots)) != PRISM_OK) return rc;
   prism::LinattnDecodeArgs a;
   const long long* st[3] = {dims->q_stride, dims->k_stride, dims->v_stride};
   long long s[3][2];
