@@ -15,8 +15,9 @@
  * (stride[1]), so that q, k and v may lie in one fused projection.  stride[1] = 0 stands for
  * a contiguous [B,T,H,d] tensor.  Strides are multiples of 16 bytes; stride[0] is greater than 0 (a
  * sequence expanded over a batch is refused) and stride[1] is at least H*d.  Outputs are
- * contiguous and may not overlap inputs.  Pointers are 16-byte aligned; those of log_decay,
- * positions, seq_lens and slots 4-byte aligned.
+ * contiguous and may not overlap inputs (a state in the place of one that the call still reads is
+ * refused).  Pointers are 16-byte aligned; those of log_decay, positions, seq_lens and slots
+ * 4-byte aligned.
  *
  *   seq_lens [B] int32 or NULL: tokens t >= seq_lens[b] are padding, as in prism.h: their
  *   outputs and gradients are 0 and their values, NaN included, reach nothing.  Lengths

@@ -313,6 +313,8 @@ extern "C" PRISM_API int prism_linattn_forward(const prism_linattn_dims* dims, c
       return rc;
   prism::LinattnArgs a;
   plan_runs(dims, 1, a);
+  // runs read initial_state while the last one writes final_state
+  if (a.nseg > 1 && final_state && final_state == initial_state) return PRISM_ERR_INVALID_ARG;
   const float c = dims->scale;
   a.job[0] = make_job(in, 0, 1, 2, out, initial_state, 0, final_state, c, 1.f, c, 0);
   return run_linattn(dims, a, in, 3, log_decay, seq_lens, workspace, workspace_bytes, stream);
@@ -337,6 +339,8 @@ extern "C" PRISM_API int prism_linattn_backward(const prism_linattn_dims* dims, 
       return rc;
   prism::LinattnArgs a;
   plan_runs(dims, 3, a);
+  // three passes run beside each other: two read what d_initial_state would overwrite
+  if (d_initial_state && (d_initial_state == d_final_state || d_initial_state == initial_state)) return PRISM_ERR_INVALID_ARG;
   const float c = dims->scale;
   // the state of dq's pass is S^T [d_k][d_v], that of dv's H [d_v][d_k], that of dk's H^T
   a.job[0] = make_job(in, 3, 2, 1, dq, initial_state, 1, nullptr, c, 1.f, c, 0);
