@@ -5,7 +5,10 @@
 //   O2 = X S^T                      M 128             N D               K D
 //   U  = Z^T Yd                     M D (rows of S)   N D               K 128, once a term of Yd
 // out_i = O1_i + so lambda^e(i) O2_i in fp32 and S <- lambda^n S + U in fp32 registers; S enters
-// O2 rounded to bf16 once.  Yd_j = su lambda^f(j) y_j is split into bf16 terms, each rounding what
+// O2, and the scores enter O1, rounded to bf16 once: operands of these products have 16 bits, a second
+// term of either would add a product as large as the first and (S) 32 KB that shared memory does
+// not have at d = 128, and the outputs are bf16 themselves.  So outputs are off by 2.3e-3 of their norm,
+// where rounding them alone leaves 1.7e-3.  Yd_j = su lambda^f(j) y_j is split into bf16 terms, each rounding what
 // the ones before left: two (16 bits) where the state only feeds outputs, which the
 // roundings of S and of the scores bound anyway; three (24 bits) where the caller gets the
 // state and it still remembers the chunk (by more than a quarter, lambda^rest >= 1/4).
