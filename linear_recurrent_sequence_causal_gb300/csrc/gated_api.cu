@@ -1,0 +1,226 @@
+// C ABI of the gated recurrent layer's operators: argument checks, workspace layout and
+// dispatch.  See include/prism_gated.h for the contract of each entry point.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/prism_gated.h"
+#include "api_checks.h"
+#include "gated_scan.cuh"
+#include "layer_norm.cuh"
+
+__device__ int g_gated_status;   // a bounded wait gave up (prism_gated_status)
+
+namespace {
+
+using prism::aligned;
+using prism::check_pointers;
+using prism::check_words;
+using prism::resolve;
+
+static_assert(PRISM_GATED_CHUNK == prism::kGatedChunk, "a row of states for each tile");
+constexpr long long kMost = (1LL << 31) - 1;
+
+int check_tokens(int B, int T, int D, prism_dtype t) {
+  if (t != PRISM_F32 && t != PRISM_BF16) return PRISM_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0 || D <= 0) return PRISM_ERR_INVALID_ARG;
+  if (D % 8 || (long long)B * T > kMost) return PRISM_ERR_UNSUPPORTED;
+  return PRISM_OK;
+}
+
+// ---- layer norm ----
+
+int check_norm(const prism_layer_norm_dims* d) {
+  if (!d) return PRISM_ERR_INVALID_ARG;
+  if (d->flags || !(d->eps >= 0.f)) return PRISM_ERR_INVALID_ARG;
+  const int rc = check_tokens(d->B, d->T, d->D, d->dtype);
+  if (rc != PRISM_OK) return rc;
+  return d->D > prism::kLayerNormMaxD ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
+}
+
+int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight, const int32_t* seq_lens, void* out,
+              prism::LayerNormArgs& a) {
+  a = prism::LayerNormArgs();
+  a.x = x; a.w = weight; a.out = out;
+  a.lens = seq_lens;
+  a.B = d->B; a.T = d->T; a.D = d->D;
+  a.eps = d->eps;
+  return resolve(d->x_stride, d->B, d->T, d->D, d->dtype, a.xs);
+}
+
+// ---- gated recurrence ----
+
+int strips_of(const prism_gated_dims* d) { return (d->D + prism::kGatedCols - 1) / prism::kGatedCols; }
+int chunks_of(const prism_gated_dims* d) { return (d->T + prism::kGatedChunk - 1) / prism::kGatedChunk; }
+long long tiles_of(const prism_gated_dims* d) { return (long long)d->B * strips_of(d) * chunks_of(d); }
+
+int check_gated(const prism_gated_dims* d, unsigned flags) {
+  if (!d) return PRISM_ERR_INVALID_ARG;
+  if (d->flags & ~flags) return PRISM_ERR_INVALID_ARG;
+  const int rc = check_tokens(d->B, d->T, d->D, d->dtype);
+  if (rc != PRISM_OK) return rc;
+  if ((long long)d->B * strips_of(d) > kMost || tiles_of(d) > kMost) return PRISM_ERR_UNSUPPORTED;
+  return PRISM_OK;
+}
+
+// The counter, then 16 bytes of (P, L) and 8 of h a lane and tile.
+constexpr size_t kCounter = 256;
+size_t gated_bytes(const prism_gated_dims* d) {
+  return chunks_of(d) == 1 ? 0 : kCounter + (size_t)tiles_of(d) * 32 * 24;
+}
+
+int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, void* workspace, size_t workspace_bytes,
+              void* stream) {
+  const size_t need = gated_bytes(d);
+  if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
+  if (need && (!workspace || workspace_bytes < need)) return PRISM_ERR_WORKSPACE;
+  a.B = d->B; a.T = d->T; a.D = d->D;
+  a.NC = chunks_of(d);
+  a.strips = strips_of(d);
+  a.check = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (need) {
+    char* w = static_cast<char*>(workspace);
+    a.ticket = reinterpret_cast<unsigned*>(w);
+    a.agg = reinterpret_cast<ulonglong2*>(w + kCounter);
+    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d) * 32 * 16);
+    void* word = nullptr;
+    if (cudaGetSymbolAddress(&word, g_gated_status) != cudaSuccess) return PRISM_ERR_CUDA;
+    a.status = static_cast<int*>(word);
+    if (cudaMemsetAsync(workspace, 0xff, need, s) != cudaSuccess) return PRISM_ERR_CUDA;
+  }
+  return prism::launch_gated_scan(d->dtype == PRISM_F32 ? 0 : 1, backward, a, s) == cudaSuccess ? PRISM_OK
+                                                                                               : PRISM_ERR_LAUNCH;
+}
+
+int fill_inputs(const prism_gated_dims* d, const void* x, const void* forget, const void* input_gate, prism::GatedArgs& a) {
+  a = prism::GatedArgs();
+  a.x = x; a.f = forget; a.i = input_gate;
+  int rc = resolve(d->x_stride, d->B, d->T, d->D, d->dtype, a.xs);
+  if (rc == PRISM_OK) rc = resolve(d->f_stride, d->B, d->T, d->D, d->dtype, a.fs);
+  if (rc == PRISM_OK && input_gate) rc = resolve(d->i_stride, d->B, d->T, d->D, d->dtype, a.is);
+  return rc;
+}
+
+}  // namespace
+
+extern "C" PRISM_API int prism_layer_norm(const prism_layer_norm_dims* dims, const void* x, const float* weight,
+                                          const float* bias, const int32_t* seq_lens, void* out, void* stream) {
+  int rc = check_norm(dims);
+  if (rc != PRISM_OK) return rc;
+  const void* req[] = {x, out};
+  const void* opt[] = {weight, bias};
+  if ((rc = check_pointers(req, opt, 2)) != PRISM_OK) return rc;
+  if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
+  prism::LayerNormArgs a;
+  if ((rc = fill_norm(dims, x, weight, seq_lens, out, a)) != PRISM_OK) return rc;
+  a.b = bias;
+  return prism::launch_layer_norm(dims->dtype == PRISM_F32 ? 0 : 1, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PRISM_OK
+             : PRISM_ERR_LAUNCH;
+}
+
+extern "C" PRISM_API size_t prism_layer_norm_workspace_bytes(const prism_layer_norm_dims* dims) {
+  if (check_norm(dims) != PRISM_OK) return 0;
+  return prism::layer_norm_partial_rows(dims->D) * 2 * dims->D * 4;
+}
+
+extern "C" PRISM_API int prism_layer_norm_backward(const prism_layer_norm_dims* dims, const void* x,
+                                                   const float* weight, const int32_t* seq_lens, const void* d_out,
+                                                   void* dx, float* d_weight, float* d_bias, void* workspace,
+                                                   size_t workspace_bytes, void* stream) {
+  int rc = check_norm(dims);
+  if (rc != PRISM_OK) return rc;
+  const void* req[] = {x, d_out, dx};
+  const void* opt[] = {weight, d_weight, d_bias};
+  if ((rc = check_pointers(req, opt, 3)) != PRISM_OK) return rc;
+  if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
+  if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
+  if ((d_weight || d_bias) && (!workspace || workspace_bytes < prism_layer_norm_workspace_bytes(dims)))
+    return PRISM_ERR_WORKSPACE;
+  prism::LayerNormArgs a;
+  if ((rc = fill_norm(dims, x, weight, seq_lens, dx, a)) != PRISM_OK) return rc;
+  if ((rc = resolve(dims->do_stride, dims->B, dims->T, dims->D, dims->dtype, a.ds)) != PRISM_OK) return rc;
+  a.dy = d_out;
+  a.dw = d_weight; a.db = d_bias;
+  a.partial = static_cast<float*>(workspace);
+  return prism::launch_layer_norm_backward(dims->dtype == PRISM_F32 ? 0 : 1, a, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PRISM_OK
+             : PRISM_ERR_LAUNCH;
+}
+
+extern "C" PRISM_API size_t prism_gated_scan_workspace_bytes(const prism_gated_dims* dims) {
+  return check_gated(dims, PRISM_FLAG_CHECK_WAIT_TIMEOUT) == PRISM_OK ? gated_bytes(dims) : 0;
+}
+
+extern "C" PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, const void* x, const void* forget,
+                                                  const void* input_gate, const float* initial_state, void* out,
+                                                  float* final_state, float* states, const int32_t* seq_lens,
+                                                  void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_gated(dims, PRISM_FLAG_CHECK_WAIT_TIMEOUT);
+  if (rc != PRISM_OK) return rc;
+  const void* req[] = {x, forget, out};
+  const void* opt[] = {input_gate, initial_state, final_state, states};
+  if ((rc = check_pointers(req, opt, 4)) != PRISM_OK) return rc;
+  if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
+  prism::GatedArgs a;
+  if ((rc = fill_inputs(dims, x, forget, input_gate, a)) != PRISM_OK) return rc;
+  a.s_in = initial_state; a.s_out = final_state; a.states = states;
+  a.out = out; a.lens = seq_lens;
+  return run_gated(dims, false, a, workspace, workspace_bytes, stream);
+}
+
+extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims, const void* x, const void* forget,
+                                                   const void* input_gate, const float* states, const void* d_out,
+                                                   const float* d_final_state, void* dx, void* d_forget,
+                                                   void* d_input_gate, float* d_initial_state,
+                                                   const int32_t* seq_lens, void* workspace, size_t workspace_bytes,
+                                                   void* stream) {
+  int rc = check_gated(dims, PRISM_FLAG_CHECK_WAIT_TIMEOUT);
+  if (rc != PRISM_OK) return rc;
+  if (!input_gate != !d_input_gate) return PRISM_ERR_INVALID_ARG;
+  const void* req[] = {x, forget, states, d_out, dx, d_forget};
+  const void* opt[] = {input_gate, d_final_state, d_input_gate, d_initial_state};
+  if ((rc = check_pointers(req, opt, 4)) != PRISM_OK) return rc;
+  if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
+  prism::GatedArgs a;
+  if ((rc = fill_inputs(dims, x, forget, input_gate, a)) != PRISM_OK) return rc;
+  if ((rc = resolve(dims->do_stride, dims->B, dims->T, dims->D, dims->dtype, a.ds)) != PRISM_OK) return rc;
+  a.dy = d_out;
+  a.s_in = d_final_state; a.s_out = d_initial_state;
+  a.states = const_cast<float*>(states);
+  a.out = dx; a.df = d_forget; a.di = d_input_gate;
+  a.lens = seq_lens;
+  return run_gated(dims, true, a, workspace, workspace_bytes, stream);
+}
+
+extern "C" PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const void* x, const void* forget,
+                                                      const void* input_gate, float* state, int n_states,
+                                                      const int32_t* slots, void* out, void* stream) {
+  int rc = check_gated(dims, 0);
+  if (rc != PRISM_OK) return rc;
+  if (dims->T != 1 || n_states <= 0 || (!slots && n_states < dims->B)) return PRISM_ERR_INVALID_ARG;
+  const void* req[] = {x, forget, state, out};
+  const void* opt[] = {input_gate};
+  if ((rc = check_pointers(req, opt, 1)) != PRISM_OK) return rc;
+  if ((rc = check_words(slots, nullptr)) != PRISM_OK) return rc;
+  prism::GatedArgs g;
+  if ((rc = fill_inputs(dims, x, forget, input_gate, g)) != PRISM_OK) return rc;
+  prism::GatedDecodeArgs a;
+  a.x = x; a.f = forget; a.i = input_gate;
+  a.xs = g.xs[0]; a.fs = g.fs[0]; a.is = g.is[0];
+  a.state = state; a.slots = slots; a.out = out;
+  a.B = dims->B; a.D = dims->D; a.n_states = n_states;
+  return prism::launch_gated_decode(dims->dtype == PRISM_F32 ? 0 : 1, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PRISM_OK
+             : PRISM_ERR_LAUNCH;
+}
+
+extern "C" PRISM_API int prism_gated_status(int* word, int clear) {
+  if (!word) return PRISM_ERR_INVALID_ARG;
+  if (cudaDeviceSynchronize() != cudaSuccess) return PRISM_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(word, g_gated_status, sizeof(int)) != cudaSuccess) return PRISM_ERR_CUDA;
+  const int zero = 0;
+  if (clear && cudaMemcpyToSymbol(g_gated_status, &zero, sizeof(int)) != cudaSuccess) return PRISM_ERR_CUDA;
+  return PRISM_OK;
+}

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/prism_linattn.h"
+#include "api_checks.h"
 #include "linattn_tc.cuh"
 #include "linattn.h"
 #include "rope.cuh"
@@ -16,36 +17,12 @@ __device__ int g_linattn_status;   // a bounded wait gave up (prism_linattn_stat
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using prism::aligned;
+using prism::check_pointers;
+using prism::check_words;
+using prism::resolve;
 
-template <int N>
-int check_pointers(const void* const (&required)[N], const void* const* optional, int n) {
-  for (const void* p : required)
-    if (!p) return PRISM_ERR_INVALID_ARG;
-  for (const void* p : required)
-    if (!aligned(p, 16)) return PRISM_ERR_MISALIGNED;
-  for (int i = 0; i < n; ++i)
-    if (optional[i] && !aligned(optional[i], 16)) return PRISM_ERR_MISALIGNED;
-  return PRISM_OK;
-}
-
-// Arrays that are read by the word: log_decay, positions, seq_lens, slots.
-int check_words(const void* a, const void* b) {
-  return aligned(a, 4) && aligned(b, 4) ? PRISM_OK : PRISM_ERR_MISALIGNED;
-}
-
-int elem_bytes(prism_dtype t) { return t == PRISM_F32 ? 4 : 2; }
 bool good_head_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-// Strides of a [B,T,H,d] input as sequence and token steps; contiguous where given as 0.
-// A step that is never taken (one sequence, one token) is replaced by the contiguous one.
-int resolve(const long long given[2], int B, int T, long long row, prism_dtype t, long long (&out)[2]) {
-  const long long unit = 16 / elem_bytes(t);
-  out[1] = given[1] == 0 || T == 1 ? row : given[1];
-  out[0] = given[1] == 0 || B == 1 ? T * out[1] : given[0];
-  if (out[1] < row || out[0] <= 0 || out[1] % unit || out[0] % unit) return PRISM_ERR_INVALID_ARG;
-  return PRISM_OK;
-}
 
 // ---- head norm with rotation ----
 
