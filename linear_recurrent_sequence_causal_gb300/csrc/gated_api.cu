@@ -7,6 +7,7 @@
 #include "api_checks.h"
 #include "gated_scan.cuh"
 #include "layer_norm.cuh"
+#include "tensor_map.h"
 
 __device__ int g_gated_status;   // a bounded wait gave up (prism_gated_status)
 
@@ -68,8 +69,31 @@ size_t gated_bytes(const prism_gated_dims* d) {
   return chunks_of(d) == 1 ? 0 : kCounter + (size_t)tiles_of(d) * 32 * 24;
 }
 
-int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, void* workspace, size_t workspace_bytes,
-              void* stream) {
+struct GatedInput {
+  const void* p;
+  const long long* given;                // its strides as they came
+};
+
+// TMA map of a [B][T][D] tensor as (D, T, B), in boxes of a tile.
+bool make_map(CUtensorMap* m, const void* p, const long long (&step)[2], const prism_gated_dims* d) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = prism::encode_fn();
+  if (!fn) return false;
+  const int size = prism::elem_bytes(d->dtype);
+  const cuuint64_t dim[3] = {(cuuint64_t)d->D, (cuuint64_t)d->T, (cuuint64_t)d->B};
+  const cuuint64_t stride[2] = {(cuuint64_t)step[1] * size, (cuuint64_t)step[0] * size};
+  const cuuint32_t box[3] = {prism::kGatedCols, prism::kGatedChunk, 1}, one[3] = {1, 1, 1};
+  return fn(m, d->dtype == PRISM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, const GatedInput* in, int nin,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  long long step[4][2];
+  for (int i = 0; i < nin; ++i) {
+    const int rc = resolve(in[i].given, d->B, d->T, d->D, d->dtype, step[i]);
+    if (rc != PRISM_OK) return rc;
+  }
   const size_t need = gated_bytes(d);
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
   if (need && (!workspace || workspace_bytes < need)) return PRISM_ERR_WORKSPACE;
@@ -77,28 +101,21 @@ int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, voi
   a.NC = chunks_of(d);
   a.strips = strips_of(d);
   a.check = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
+  for (int i = 0; i < nin; ++i)
+    if (!make_map(&a.map[i], in[i].p, step[i], d)) return PRISM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_gated_status) != cudaSuccess) return PRISM_ERR_CUDA;
+  a.status = static_cast<int*>(word);
   if (need) {
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<unsigned*>(w);
     a.agg = reinterpret_cast<ulonglong2*>(w + kCounter);
     a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d) * 32 * 16);
-    void* word = nullptr;
-    if (cudaGetSymbolAddress(&word, g_gated_status) != cudaSuccess) return PRISM_ERR_CUDA;
-    a.status = static_cast<int*>(word);
     if (cudaMemsetAsync(workspace, 0xff, need, s) != cudaSuccess) return PRISM_ERR_CUDA;
   }
   return prism::launch_gated_scan(d->dtype == PRISM_F32 ? 0 : 1, backward, a, s) == cudaSuccess ? PRISM_OK
                                                                                                : PRISM_ERR_LAUNCH;
-}
-
-int fill_inputs(const prism_gated_dims* d, const void* x, const void* forget, const void* input_gate, prism::GatedArgs& a) {
-  a = prism::GatedArgs();
-  a.x = x; a.f = forget; a.i = input_gate;
-  int rc = resolve(d->x_stride, d->B, d->T, d->D, d->dtype, a.xs);
-  if (rc == PRISM_OK) rc = resolve(d->f_stride, d->B, d->T, d->D, d->dtype, a.fs);
-  if (rc == PRISM_OK && input_gate) rc = resolve(d->i_stride, d->B, d->T, d->D, d->dtype, a.is);
-  return rc;
 }
 
 }  // namespace
@@ -163,11 +180,12 @@ extern "C" PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, 
   const void* opt[] = {input_gate, initial_state, final_state, states};
   if ((rc = check_pointers(req, opt, 4)) != PRISM_OK) return rc;
   if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
-  prism::GatedArgs a;
-  if ((rc = fill_inputs(dims, x, forget, input_gate, a)) != PRISM_OK) return rc;
+  prism::GatedArgs a = prism::GatedArgs();
   a.s_in = initial_state; a.s_out = final_state; a.states = states;
   a.out = out; a.lens = seq_lens;
-  return run_gated(dims, false, a, workspace, workspace_bytes, stream);
+  a.gated = input_gate != nullptr;
+  const GatedInput in[3] = {{x, dims->x_stride}, {forget, dims->f_stride}, {input_gate, dims->i_stride}};
+  return run_gated(dims, false, a, in, a.gated ? 3 : 2, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims, const void* x, const void* forget,
@@ -183,15 +201,15 @@ extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims,
   const void* opt[] = {input_gate, d_final_state, d_input_gate, d_initial_state};
   if ((rc = check_pointers(req, opt, 4)) != PRISM_OK) return rc;
   if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
-  prism::GatedArgs a;
-  if ((rc = fill_inputs(dims, x, forget, input_gate, a)) != PRISM_OK) return rc;
-  if ((rc = resolve(dims->do_stride, dims->B, dims->T, dims->D, dims->dtype, a.ds)) != PRISM_OK) return rc;
-  a.dy = d_out;
+  prism::GatedArgs a = prism::GatedArgs();
   a.s_in = d_final_state; a.s_out = d_initial_state;
   a.states = const_cast<float*>(states);
   a.out = dx; a.df = d_forget; a.di = d_input_gate;
   a.lens = seq_lens;
-  return run_gated(dims, true, a, workspace, workspace_bytes, stream);
+  a.gated = input_gate != nullptr;
+  const GatedInput in[4] = {{x, dims->x_stride}, {forget, dims->f_stride}, {d_out, dims->do_stride},
+                            {input_gate, dims->i_stride}};
+  return run_gated(dims, true, a, in, a.gated ? 4 : 3, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const void* x, const void* forget,
@@ -204,11 +222,13 @@ extern "C" PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* di
   const void* opt[] = {input_gate};
   if ((rc = check_pointers(req, opt, 1)) != PRISM_OK) return rc;
   if ((rc = check_words(slots, nullptr)) != PRISM_OK) return rc;
-  prism::GatedArgs g;
-  if ((rc = fill_inputs(dims, x, forget, input_gate, g)) != PRISM_OK) return rc;
+  const long long* given[3] = {dims->x_stride, dims->f_stride, dims->i_stride};
+  long long step[3][2] = {};
+  for (int i = 0; i < (input_gate ? 3 : 2); ++i)
+    if ((rc = resolve(given[i], dims->B, 1, dims->D, dims->dtype, step[i])) != PRISM_OK) return rc;
   prism::GatedDecodeArgs a;
   a.x = x; a.f = forget; a.i = input_gate;
-  a.xs = g.xs[0]; a.fs = g.fs[0]; a.is = g.is[0];
+  a.xs = step[0][0]; a.fs = step[1][0]; a.is = step[2][0];
   a.state = state; a.slots = slots; a.out = out;
   a.B = dims->B; a.D = dims->D; a.n_states = n_states;
   return prism::launch_gated_decode(dims->dtype == PRISM_F32 ? 0 : 1, a, static_cast<cudaStream_t>(stream)) == cudaSuccess

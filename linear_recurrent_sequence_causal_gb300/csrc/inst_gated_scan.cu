@@ -2,23 +2,38 @@
 #include <cuda_runtime.h>
 
 #include "gated_scan.cuh"
+#include "linattn.h"
 
 namespace prism {
 
-constexpr int kGatedRows = 8;            // tokens a lane
+constexpr int kSMs = 152;
 
-template <class E, bool GATED>
-cudaError_t launch_scan_t(bool backward, const GatedArgs& a, cudaStream_t s) {
-  constexpr int NT = 32 * kGatedChunk / kGatedRows;
-  const unsigned grid = (unsigned)((long long)a.B * a.strips * a.NC);
-  if (backward) gated_scan_backward_kernel<E, GATED, kGatedRows><<<grid, NT, 0, s>>>(a);
-  else gated_scan_kernel<E, GATED, kGatedRows><<<grid, NT, 0, s>>>(a);
+template <class Shared, int R, int C, class F>
+cudaError_t launch_tiles(F* fn, const GatedArgs& a, std::atomic<unsigned long long>& done, cudaStream_t s) {
+  static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
+  const cudaError_t e = allow_smem(fn, sizeof(Shared), done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)a.B * a.strips * a.NC, most = kSMs * C;
+  fn<<<(unsigned)(tiles < most ? tiles : most), 32 * kGatedChunk / R, sizeof(Shared), s>>>(a);
   return cudaGetLastError();
 }
 
+template <class E, bool GATED>
+cudaError_t launch_scan_t(bool backward, const GatedArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> done[2];
+  constexpr bool half = sizeof(E) == 2;
+  if (backward) {
+    constexpr int R = 8, S = half ? 2 : 1, C = 2;
+    return launch_tiles<GatedShared<E, GATED ? 4 : 3, S, R, true>, R, C>(gated_scan_backward_kernel<E, GATED, R, S, C>, a,
+                                                                         done[1], s);
+  }
+  constexpr int R = 8, S = half ? 2 : 1, C = 3;
+  return launch_tiles<GatedShared<E, GATED ? 3 : 2, S, R, false>, R, C>(gated_scan_kernel<E, GATED, R, S, C>, a, done[0], s);
+}
+
 cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cudaStream_t s) {
-  if (dtype == 0) return a.i ? launch_scan_t<float, true>(backward, a, s) : launch_scan_t<float, false>(backward, a, s);
-  return a.i ? launch_scan_t<__nv_bfloat16, true>(backward, a, s) : launch_scan_t<__nv_bfloat16, false>(backward, a, s);
+  if (dtype == 0) return a.gated ? launch_scan_t<float, true>(backward, a, s) : launch_scan_t<float, false>(backward, a, s);
+  return a.gated ? launch_scan_t<__nv_bfloat16, true>(backward, a, s) : launch_scan_t<__nv_bfloat16, false>(backward, a, s);
 }
 
 template <class E, bool GATED>

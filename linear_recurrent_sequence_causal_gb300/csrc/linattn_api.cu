@@ -1,17 +1,14 @@
 // C ABI of the linear attention layer's operators: argument checks, segment plan and
 // dispatch.  See include/prism_linattn.h for the contract of each entry point.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <mutex>
 
 #include "../../include/prism_linattn.h"
 #include "api_checks.h"
 #include "linattn_tc.cuh"
 #include "linattn.h"
 #include "rope.cuh"
+#include "tensor_map.h"
 
 __device__ int g_linattn_status;   // a bounded wait gave up (prism_linattn_status)
 
@@ -20,6 +17,7 @@ namespace {
 using prism::aligned;
 using prism::check_pointers;
 using prism::check_words;
+using prism::encode_fn;
 using prism::resolve;
 
 bool good_head_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
@@ -120,21 +118,6 @@ struct Operand {
   const void* p;
   long long s[2];
 };
-
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the driver library).
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
 
 // TMA map of a bf16 [B][T][H][d] tensor as (d, H, T, B), in boxes of 128 tokens of one head and up
 // to 64 dims, swizzled as wide as their rows.

@@ -117,22 +117,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn_major, bool b
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
-// tc::bar_wait with `limit` polls that sleep for up to kPollNs each: a waiting warp takes no issue
-// slots from the working ones.
-constexpr uint32_t kPollNs = 20000u, kWaitPolls = 50000u;            // a second in all
-constexpr uint32_t kWaitCycles = 2000000000u;          // the same where polls do not sleep
-__device__ __forceinline__ bool bar_wait_long(uint64_t* bar, uint32_t parity, uint32_t limit = kWaitPolls) {
-  for (uint32_t it = 0; it < limit; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(kPollNs)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
-}
+constexpr uint32_t kWaitCycles = 2000000000u;          // kWaitPolls' time where polls do not sleep
 __device__ __forceinline__ uint32_t clock_lo() {
   uint32_t t;
   asm volatile("mov.u32 %0, %clock;\n" : "=r"(t));

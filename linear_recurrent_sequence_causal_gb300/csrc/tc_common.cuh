@@ -141,6 +141,22 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_
   return false;
 }
 
+// bar_wait with `limit` polls that sleep for up to kPollNs each: a waiting warp takes no issue
+// slots from the working ones.
+constexpr uint32_t kPollNs = 20000u, kWaitPolls = 50000u;            // a second in all
+__device__ __forceinline__ bool bar_wait_long(uint64_t* bar, uint32_t parity, uint32_t limit = kWaitPolls) {
+  for (uint32_t it = 0; it < limit; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kPollNs)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
 // Global loads that stay where they are written (a volatile asm is not moved
 // past other volatile asm), so a value can be fetched well before its first use.
 __device__ __forceinline__ float ldg_early(const float* p) {
