@@ -82,8 +82,8 @@ typedef struct {
  *               sequence's end are left as they are.
  * Gates and states are fp32; out is rounded once.  A gate below 2^-126 counts as 0.  Tiles of a
  * sequence wait for the state of the tiles before them; the result does not depend on their
- * timing (two calls agree bit for bit).  The workspace (prism_gated_scan_workspace_bytes, 0 up to 64
- * tokens) serves both directions. */
+ * timing (two calls agree bit for bit).  The workspace has prism_gated_scan_workspace_bytes (0 for short
+ * sequences, where no tile waits: it may then be NULL). */
 PRISM_API size_t prism_gated_scan_workspace_bytes(const prism_gated_dims* dims);
 PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, const void* x, const void* forget,
                                        const void* input_gate, const float* initial_state, void* out,
@@ -94,6 +94,7 @@ PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, const void*
  * [B,T,D] in dtype and d_final_state [B,D] fp32 (NULL: zero): dx, d_forget and d_input_gate (NULL
  * without an input gate, and only then) in dtype; d_initial_state [B,D] fp32 (NULL: not wanted), which
  * may be d_final_state.  Deterministic. */
+PRISM_API size_t prism_gated_scan_backward_workspace_bytes(const prism_gated_dims* dims);
 PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims, const void* x, const void* forget,
                                         const void* input_gate, const float* states, const void* d_out,
                                         const float* d_final_state, void* dx, void* d_forget,

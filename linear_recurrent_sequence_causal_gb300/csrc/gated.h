@@ -11,8 +11,11 @@ struct GatedArgs;
 struct GatedDecodeArgs;
 struct LayerNormArgs;
 
-constexpr int kGatedChunk = 64;          // tokens of a tile, and between two rows of states
+constexpr int kGatedChunk = 64;          // tokens from one row of states to the next
 constexpr int kGatedCols = 64;           // channels of a tile: two a lane
+// Tokens of a tile, whole chunks.  Tiles twice as long halve the states that tiles hand on; an SM's
+// shared memory bounds them.
+constexpr int gated_tile(int dtype, bool backward) { return dtype && !backward ? 128 : 64; }
 constexpr int kLayerNormMaxD = 16384;
 
 cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cudaStream_t s);

@@ -18,7 +18,7 @@ using prism::check_pointers;
 using prism::check_words;
 using prism::resolve;
 
-static_assert(PRISM_GATED_CHUNK == prism::kGatedChunk, "a row of states for each tile");
+static_assert(PRISM_GATED_CHUNK == prism::kGatedChunk, "rows of states");
 constexpr long long kMost = (1LL << 31) - 1;
 
 int check_tokens(int B, int T, int D, prism_dtype t) {
@@ -52,21 +52,25 @@ int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight
 
 int strips_of(const prism_gated_dims* d) { return (d->D + prism::kGatedCols - 1) / prism::kGatedCols; }
 int chunks_of(const prism_gated_dims* d) { return (d->T + prism::kGatedChunk - 1) / prism::kGatedChunk; }
-long long tiles_of(const prism_gated_dims* d) { return (long long)d->B * strips_of(d) * chunks_of(d); }
+int tile_of(const prism_gated_dims* d, bool backward) { return prism::gated_tile(d->dtype == PRISM_F32 ? 0 : 1, backward); }
+long long tiles_of(const prism_gated_dims* d, bool backward) {
+  const int t = tile_of(d, backward);
+  return (long long)d->B * strips_of(d) * (((long long)d->T + t - 1) / t);
+}
 
 int check_gated(const prism_gated_dims* d, unsigned flags) {
   if (!d) return PRISM_ERR_INVALID_ARG;
   if (d->flags & ~flags) return PRISM_ERR_INVALID_ARG;
   const int rc = check_tokens(d->B, d->T, d->D, d->dtype);
   if (rc != PRISM_OK) return rc;
-  if ((long long)d->B * strips_of(d) > kMost || tiles_of(d) > kMost) return PRISM_ERR_UNSUPPORTED;
+  if ((long long)d->B * strips_of(d) > kMost || tiles_of(d, true) > kMost / 2) return PRISM_ERR_UNSUPPORTED;
   return PRISM_OK;
 }
 
-// The counter, then 16 bytes of (P, L) and 8 of h a lane and tile.
+// The counter, then 16 bytes of (P, L) and 8 of h a lane and tile; nothing where no tile waits.
 constexpr size_t kCounter = 256;
-size_t gated_bytes(const prism_gated_dims* d) {
-  return chunks_of(d) == 1 ? 0 : kCounter + (size_t)tiles_of(d) * 32 * 24;
+size_t gated_bytes(const prism_gated_dims* d, bool backward) {
+  return d->T <= tile_of(d, backward) ? 0 : kCounter + (size_t)tiles_of(d, backward) * 32 * 24;
 }
 
 struct GatedInput {
@@ -75,26 +79,26 @@ struct GatedInput {
 };
 
 // TMA map of a [B][T][D] tensor as (D, T, B), in boxes of a tile.
-bool make_map(CUtensorMap* m, const void* p, const long long (&step)[2], const prism_gated_dims* d) {
+bool make_map(CUtensorMap* m, const void* p, const long long (&step)[2], const prism_gated_dims* d, int tile) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = prism::encode_fn();
   if (!fn) return false;
   const int size = prism::elem_bytes(d->dtype);
   const cuuint64_t dim[3] = {(cuuint64_t)d->D, (cuuint64_t)d->T, (cuuint64_t)d->B};
   const cuuint64_t stride[2] = {(cuuint64_t)step[1] * size, (cuuint64_t)step[0] * size};
-  const cuuint32_t box[3] = {prism::kGatedCols, prism::kGatedChunk, 1}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {prism::kGatedCols, (cuuint32_t)tile, 1}, one[3] = {1, 1, 1};
   return fn(m, d->dtype == PRISM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
             const_cast<void*>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, const GatedInput* in, int nin,
-              void* workspace, size_t workspace_bytes, void* stream) {
+              void* const* out, int nout, void* workspace, size_t workspace_bytes, void* stream) {
   long long step[4][2];
   for (int i = 0; i < nin; ++i) {
     const int rc = resolve(in[i].given, d->B, d->T, d->D, d->dtype, step[i]);
     if (rc != PRISM_OK) return rc;
   }
-  const size_t need = gated_bytes(d);
+  const size_t need = gated_bytes(d, backward);
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
   if (need && (!workspace || workspace_bytes < need)) return PRISM_ERR_WORKSPACE;
   a.B = d->B; a.T = d->T; a.D = d->D;
@@ -102,7 +106,10 @@ int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, con
   a.strips = strips_of(d);
   a.check = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
   for (int i = 0; i < nin; ++i)
-    if (!make_map(&a.map[i], in[i].p, step[i], d)) return PRISM_ERR_CUDA;
+    if (!make_map(&a.map[i], in[i].p, step[i], d, tile_of(d, backward))) return PRISM_ERR_CUDA;
+  const long long whole[2] = {(long long)d->T * d->D, d->D};
+  for (int i = 0; i < nout; ++i)
+    if (!make_map(&a.to[i], out[i], whole, d, tile_of(d, backward))) return PRISM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* word = nullptr;
   if (cudaGetSymbolAddress(&word, g_gated_status) != cudaSuccess) return PRISM_ERR_CUDA;
@@ -111,7 +118,7 @@ int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, con
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<unsigned*>(w);
     a.agg = reinterpret_cast<ulonglong2*>(w + kCounter);
-    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d) * 32 * 16);
+    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d, backward) * 32 * 16);
     if (cudaMemsetAsync(workspace, 0xff, need, s) != cudaSuccess) return PRISM_ERR_CUDA;
   }
   return prism::launch_gated_scan(d->dtype == PRISM_F32 ? 0 : 1, backward, a, s) == cudaSuccess ? PRISM_OK
@@ -167,7 +174,11 @@ extern "C" PRISM_API int prism_layer_norm_backward(const prism_layer_norm_dims* 
 }
 
 extern "C" PRISM_API size_t prism_gated_scan_workspace_bytes(const prism_gated_dims* dims) {
-  return check_gated(dims, PRISM_FLAG_CHECK_WAIT_TIMEOUT) == PRISM_OK ? gated_bytes(dims) : 0;
+  return check_gated(dims, PRISM_FLAG_CHECK_WAIT_TIMEOUT) == PRISM_OK ? gated_bytes(dims, false) : 0;
+}
+
+extern "C" PRISM_API size_t prism_gated_scan_backward_workspace_bytes(const prism_gated_dims* dims) {
+  return check_gated(dims, PRISM_FLAG_CHECK_WAIT_TIMEOUT) == PRISM_OK ? gated_bytes(dims, true) : 0;
 }
 
 extern "C" PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, const void* x, const void* forget,
@@ -182,10 +193,10 @@ extern "C" PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, 
   if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
   prism::GatedArgs a = prism::GatedArgs();
   a.s_in = initial_state; a.s_out = final_state; a.states = states;
-  a.out = out; a.lens = seq_lens;
+  a.lens = seq_lens;
   a.gated = input_gate != nullptr;
   const GatedInput in[3] = {{x, dims->x_stride}, {forget, dims->f_stride}, {input_gate, dims->i_stride}};
-  return run_gated(dims, false, a, in, a.gated ? 3 : 2, workspace, workspace_bytes, stream);
+  return run_gated(dims, false, a, in, a.gated ? 3 : 2, &out, 1, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims, const void* x, const void* forget,
@@ -204,12 +215,12 @@ extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims,
   prism::GatedArgs a = prism::GatedArgs();
   a.s_in = d_final_state; a.s_out = d_initial_state;
   a.states = const_cast<float*>(states);
-  a.out = dx; a.df = d_forget; a.di = d_input_gate;
   a.lens = seq_lens;
   a.gated = input_gate != nullptr;
   const GatedInput in[4] = {{x, dims->x_stride}, {forget, dims->f_stride}, {d_out, dims->do_stride},
                             {input_gate, dims->i_stride}};
-  return run_gated(dims, true, a, in, a.gated ? 4 : 3, workspace, workspace_bytes, stream);
+  void* const out[3] = {dx, d_forget, d_input_gate};
+  return run_gated(dims, true, a, in, a.gated ? 4 : 3, out, a.gated ? 3 : 2, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const void* x, const void* forget,

@@ -33,15 +33,16 @@ namespace prism {
 
 struct GatedArgs {
   CUtensorMap map[4];                              // x, f(, dout)(, i): the inputs of the direction
+  CUtensorMap to[3];                               // out; dx, df(, di)
   const float* s_in;                               // [B][D] or null: initial state; dL/d(final state)
   float* s_out;                                    // [B][D] or null: final state; dL/d(initial state)
   float* states;                                   // [B][NC][D]: written forwards (or null), read backwards
-  void *out, *df, *di;                             // out; dx, df, di
   const int* lens;
-  int B, T, D, NC, strips, gated;                  // gated: there is an input gate
+  int B, T, D, NC, strips, gated;                  // NC: rows of states a sequence; gated: there is an input gate
+  int tiles;                                       // of a sequence and strip
   unsigned* ticket;                                // workspace: counter, then agg and incl
-  ulonglong2* agg;                                 // [B][NC][strips][32]: (P, L) of two channels
-  uint2* incl;                                     // [B][NC][strips][32]: h of two channels
+  ulonglong2* agg;                                 // [B][tiles][strips][32]: (P, L) of two channels
+  uint2* incl;                                     // [B][tiles][strips][32]: h of two channels
   int* status;
   int check;                                       // diagnostic: waits run out once
 };
@@ -57,7 +58,7 @@ struct GatedDecodeArgs {
 
 constexpr unsigned kAbsent = 0xffffffffu;          // not published yet
 constexpr unsigned long long kWaitNs = 1000000000ull, kCheckNs = 1000000ull;
-constexpr int kLookBack = 16;                      // (P, L) that a tile holds on its way back
+constexpr int kLookBack = 8;                      // (P, L) that a tile holds on its way back
 
 __device__ __forceinline__ unsigned canonical(float x) {
   const unsigned u = __float_as_uint(x);
@@ -91,6 +92,12 @@ __device__ __forceinline__ void publish(uint2* p, uint64_t h) {
   float x, y;
   unpack2(h, x, y);
   asm volatile("st.relaxed.gpu.global.v2.u32 [%0], {%1, %2};\n" ::"l"(p), "r"(canonical(x)), "r"(canonical(y)) : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_addr(src))
+               : "memory");
 }
 // One box of a [B][T][D] tensor: coordinates in channels, tokens and sequences; outside it zeros.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
@@ -171,10 +178,11 @@ __device__ __forceinline__ uint64_t sigmoid_of(uint64_t z) {
   return pack2(rcp_approx(dx), rcp_approx(dy));
 }
 
-// The tile of a CTA.  `rank` is its place in the chain of its sequence (forwards the chunk itself,
-// backwards counted from the last chunk with tokens); ranks past the chain are tiles of padding.
+// A tile of TT tokens.  `rank` is its place in the chain of its sequence (forwards in time, backwards
+// from the last tile with tokens); ranks past the chain are tiles of padding.
+template <int TT>
 struct GatedTile {
-  int b, strip, chunk, rank, live, len;            // live: tokens of the tile that are there
+  int b, strip, rank, first, live, len;            // first token; live: tokens of the tile that are there
   bool last;                                       // the chain ends here
   __device__ __forceinline__ GatedTile(const GatedArgs& p, unsigned n, bool backward) {
     const unsigned lanes = (unsigned)(p.B * p.strips);
@@ -183,9 +191,9 @@ struct GatedTile {
     b = (int)(n / (unsigned)p.strips);
     strip = (int)(n - (unsigned)b * (unsigned)p.strips);
     len = p.lens ? min(max(__ldg(p.lens + b), 0), p.T) : p.T;
-    const int chain = (len + kGatedChunk - 1) / kGatedChunk;
-    chunk = backward && rank < chain ? chain - 1 - rank : rank;
-    live = min(max(len - chunk * kGatedChunk, 0), kGatedChunk);
+    const int chain = (len + TT - 1) / TT;
+    first = (backward && rank < chain ? chain - 1 - rank : rank) * TT;
+    live = min(max(len - first, 0), TT);
     last = rank == chain - 1;
   }
 };
@@ -245,249 +253,287 @@ __device__ __forceinline__ uint64_t look_back(const GatedArgs& p, long long at, 
   return h;
 }
 
-// Shared memory of a CTA: S stages of `N` input tiles, then what warps exchange.  A CTA takes tile after
-// tile; the copies (TMA, one box of 64 channels by 64 tokens an input) of the next ones are in flight while
-// it works, and a tile's stage is free again once its values are in registers.
-template <class E, int N, int S, int R, bool BACK>
+// What a CTA needs to know about its tile: computed by one thread, read by all.
+struct GatedJob {
+  int first, live, rank, last;
+  int b, strip, more, pad;                         // more: 0 where there is no tile left
+};
+
+// Shared memory of a CTA: S stages of NI input tiles, NO output tiles, then what warps exchange.  A CTA takes tile
+// after tile.  Copies are TMA's, a box of 64 channels by TT tokens each: the next tiles' come in while
+// it works (a stage is free again once its values are in registers), and a tile's outputs
+// leave while it works on the next one.
+template <class E, int NI, int NO, int TT, int R, int S>
 struct GatedShared {
-  static constexpr int NW = kGatedChunk / R;
-  alignas(128) E tile[S][N][kGatedChunk][kGatedCols];
-  ulonglong2 part[2][NW][32];                      // (P, L) of a warp's tokens: two channels each of P, then of L
+  static constexpr int NW = TT / R;
+  static constexpr bool BACK = NI > 2 && NO > 1;
+  alignas(128) E tile[S][NI][TT][kGatedCols];
+  alignas(128) E out[NO][TT][kGatedCols];
+  ulonglong2 part[2][NW][32];                      // (P, L) of a warp's tokens, then of those before them: both channels of P, of L
   ulonglong2 held[kLookBack][32];
-  uint64_t start[NW][32];                          // the state before a warp's tokens
-  uint64_t back[2][BACK ? NW : 1][32], ahead[BACK ? NW : 1][32];     // the gradient's, from behind
+  uint64_t carry[32];                              // what reaches the tile
+  // gradient: r that a warp's tokens send backwards, (P, r) of what is behind them, the state before them
+  uint64_t back[2][BACK ? NW : 1][32], start[BACK ? NW : 1][32];
+  ulonglong2 behind[BACK ? NW : 1][32];
+  GatedJob job[2 * S];
   uint64_t full[S];
-  unsigned ticket[2 * S];
 };
 
 // Tickets and copies of a CTA, which one thread makes.
-template <class E, int N, int S, int R, bool BACK>
+template <class E, int NI, int NO, int TT, int R, int S>
 struct GatedFeed {
-  GatedShared<E, N, S, R, BACK>& sm;
+  GatedShared<E, NI, NO, TT, R, S>& sm;
   const GatedArgs& p;
-  unsigned total, next;
+  unsigned next;
   __device__ __forceinline__ void init() {
-    total = (unsigned)((long long)p.B * p.strips * p.NC);
 #pragma unroll
     for (int s = 0; s < S; ++s) tc::bar_init(&sm.full[s], 1);
     tc::bar_fence_init();
     draw(0);
-    for (int it = 0; it < S; ++it) feed(it);
+    for (int it = 0; it < S; ++it) load(it);
   }
   // the tile that follows; without chains nobody waits and tiles are dealt out in turn
   __device__ __forceinline__ void draw(int it) {
-    next = p.NC == 1 ? blockIdx.x + (unsigned)it * gridDim.x : atomicAdd(p.ticket, 1u) + 1u;
+    next = p.tiles == 1 ? blockIdx.x + (unsigned)it * gridDim.x : atomicAdd(p.ticket, 1u) + 1u;
   }
-  __device__ __forceinline__ void feed(int it) {
-    const unsigned n = next;
-    sm.ticket[it % (2 * S)] = n;
-    if (n >= total) return;                        // the others see it and stop
-    const GatedTile tl(p, n, BACK);
+  __device__ __forceinline__ void load(int it) {
+    const unsigned n = next, total = (unsigned)((long long)p.B * p.strips * p.tiles);
+    GatedJob& j = sm.job[it % (2 * S)];
+    if (n >= total) {                              // the others see it and stop
+      j.more = 0;
+      return;
+    }
+    const GatedTile<TT> tl(p, n, NO > 1);
+    j = GatedJob{tl.first, tl.live, tl.rank, tl.last, tl.b, tl.strip, 1, 0};
     if (tl.live > 0) {
       const int s = it % S;
       tc::bar_expect_tx(&sm.full[s], sizeof(sm.tile[s]));
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        tma_load_3d(sm.tile[s][k], &p.map[k], tl.strip * kGatedCols, tl.chunk * kGatedChunk, tl.b, &sm.full[s]);
+      for (int k = 0; k < NI; ++k)
+        tma_load_3d(sm.tile[s][k], &p.map[k], tl.strip * kGatedCols, tl.first, tl.b, &sm.full[s]);
     }
     draw(it + 1);                                  // ready when it is needed
   }
-  // the way out of a wait that gave up: no copy in flight may outlive the CTA
-  __device__ __forceinline__ void drain(unsigned phase) {
-    if (threadIdx.x == 0) {
-      atomicOr(p.status, 1);
-      for (int s = 0; s < S; ++s) tc::bar_wait_long(&sm.full[s], phase >> s & 1);
-    }
-    __syncthreads();
+  __device__ __forceinline__ void store(const GatedJob& j) {
+#pragma unroll
+    for (int k = 0; k < NO; ++k) tma_store_3d(&p.to[k], sm.out[k], j.strip * kGatedCols, j.first, j.b);
+    tc::bulk_commit();
   }
 };
 
-// Forward.  R tokens a lane, 64/R warps, S stages, C CTAs an SM.
-template <class E, bool GATED, int R, int S, int C>
-__global__ void __launch_bounds__(32 * kGatedChunk / R, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
-  constexpr int NW = kGatedChunk / R, N = GATED ? 3 : 2;
-  using Shared = GatedShared<E, N, S, R, false>;
+// The way out of a wait that gave up: no copy in flight may outlive the CTA.
+template <int S>
+__device__ __forceinline__ void gated_drain(const GatedArgs& p, uint64_t* full, unsigned phase) {
+  if (threadIdx.x == 0) {
+    atomicOr(p.status, 1);
+    for (int s = 0; s < S; ++s) tc::bar_wait_long(full + s, phase >> s & 1);
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ uint64_t load_pair(const float* p) {
+  Two<float> v;
+  v.load(p);
+  return v.get();
+}
+
+// Forward.  Tiles of TT tokens, R a lane, TT/R warps, S stages, C CTAs an SM.
+template <class E, bool GATED, int TT, int R, int S, int C>
+__global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
+  static_assert(kGatedChunk % R == 0, "a row of states starts at a warp's tokens");
+  constexpr int NW = TT / R, NI = GATED ? 3 : 2;
+  using Shared = GatedShared<E, NI, 1, TT, R, S>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, N, S, R, false> feed{sm, p};
+  GatedFeed<E, NI, 1, TT, R, S> feed{sm, p, 0};
   if (feeder) feed.init();
   __syncthreads();
-  const unsigned total = (unsigned)((long long)p.B * p.strips * p.NC);
   unsigned phase = 0;                              // a bit a stage
-  for (int it = 0;; ++it) {
-    const unsigned n = sm.ticket[it % (2 * S)];
-    if (n >= total) break;
-    const GatedTile tl(p, n, false);
-    const int s = it % S, ch = tl.strip * kGatedCols + 2 * lane, t0 = tl.chunk * kGatedChunk + warp * R;
-    const bool on = ch < p.D;
-    E* out = static_cast<E*>(p.out) + ((long long)tl.b * p.T + t0) * p.D + ch;
-    const long long row = (long long)tl.b * p.D + ch;
-    if (tl.live == 0) {                            // padding alone, or a sequence without tokens
-#pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (on && t0 + j < p.T) Two<E>::store(out + (long long)j * p.D, both(0.f));
-      if (tl.rank == 0 && warp == 0 && on && p.s_out) {
-        Two<float> h;
-        h.r = make_float2(0.f, 0.f);
-        if (p.s_in) h.load(p.s_in + row);
-        Two<float>::store(p.s_out + row, h.get());
-      }
-      if (feeder) feed.feed(it + S);
-      __syncthreads();                             // the ticket is there
-      continue;
+  int it = 0;
+  for (;; ++it) {
+    const GatedJob job = sm.job[it % (2 * S)];
+    if (!job.more) break;
+    const int s = it % S, mine = warp * R;         // the warp's first token in the tile
+    bool ok = true;
+    if (job.live > 0) {
+      ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
+      phase ^= 1u << s;
     }
-    const bool ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
-    phase ^= 1u << s;
     uint64_t a[R], u[R], P = both(1.f), L = both(0.f);
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (t0 + j < tl.len) {
-        Two<E> x, f, i;
-        x.load(&sm.tile[s][0][warp * R + j][2 * lane]);
-        f.load(&sm.tile[s][1][warp * R + j][2 * lane]);
+    auto token = [&](int j) {
+      Two<E> x, f, i;
+      x.load(&sm.tile[s][0][mine + j][2 * lane]);
+      f.load(&sm.tile[s][1][mine + j][2 * lane]);
+      if constexpr (GATED) {
+        i.load(&sm.tile[s][2][mine + j][2 * lane]);
+        a[j] = gate_of<E>(f.get()).s;
+        u[j] = mul2(sigmoid_of<E>(i.get()), x.get());
+      } else {
         const Gate g = gate_of<E>(f.get());
         a[j] = g.s;
-        if constexpr (GATED) {
-          i.load(&sm.tile[s][2][warp * R + j][2 * lane]);
-          u[j] = mul2(sigmoid_of<E>(i.get()), x.get());
-        } else {
-          u[j] = mul2(g.c, x.get());
-        }
-      } else {
+        u[j] = mul2(g.c, x.get());
+      }
+    };
+    if (mine + R <= job.live) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) token(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
         a[j] = both(1.f);
         u[j] = both(0.f);
+        if (mine + j < job.live) token(j);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
       L = fma2(a[j], L, u[j]);
       P = mul2(a[j], P);
     }
     ulonglong2(*part)[32] = sm.part[it & 1];
     part[warp][lane] = make_ulonglong2(P, L);
+    tc::fence_smem_to_async();                     // the last tile's outputs
     if (__syncthreads_or(!ok)) {                   // a copy that never came
-      feed.drain(phase);
+      gated_drain<S>(p, sm.full, phase);
       break;
     }
-    if (feeder) feed.feed(it + S);
+    if (feeder) {
+      if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
+      feed.load(it + S);
+    }
+    const int ch = job.strip * kGatedCols + 2 * lane;
+    const bool on = ch < p.D;
     if (warp == 0) {
-      P = both(1.f);
-      L = both(0.f);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const ulonglong2 g = part[w][lane];
-        L = fma2(g.x, L, g.y);
-        P = mul2(g.x, P);
-      }
-      const int step = p.strips * 32;
-      const long long at = ((long long)tl.b * p.NC * p.strips + tl.strip) * 32 + lane, mine = at + (long long)tl.rank * step;
+      const long long row = (long long)job.b * p.D + ch;
       uint64_t h = both(0.f);
-      if (tl.rank == 0) {
-        if (p.s_in && on) {
-          Two<float> g;
-          g.load(p.s_in + row);
-          h = g.get();
+      if (job.live > 0) {
+        P = both(1.f);
+        L = both(0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const ulonglong2 g = part[w][lane];
+          part[w][lane] = make_ulonglong2(P, L);
+          L = fma2(g.x, L, g.y);
+          P = mul2(g.x, P);
         }
-      } else {
-        if (!tl.last) publish(p.agg + mine, P, L);
-        h = look_back(p, at, step, tl.rank, sm.held);
+        const int step = p.strips * 32;
+        const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
+        const long long here = at + (long long)job.rank * step;
+        if (job.rank > 0) {
+          if (!job.last) publish(p.agg + here, P, L);
+          h = look_back(p, at, step, job.rank, sm.held);
+        } else if (p.s_in && on) {
+          h = load_pair(p.s_in + row);
+        }
+        const uint64_t end = fma2(P, h, L);
+        if (!job.last) publish(p.incl + here, end);
+        else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+      } else if (job.rank == 0 && p.s_out && on) { // a sequence without tokens
+        Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : both(0.f));
       }
-      const uint64_t end = fma2(P, h, L);
-      if (!tl.last) publish(p.incl + mine, end);
-      else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
-      if (p.states && on) Two<float>::store(p.states + ((long long)tl.b * p.NC + tl.chunk) * p.D + ch, h);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        sm.start[w][lane] = h;
-        const ulonglong2 g = part[w][lane];
-        h = fma2(g.x, h, g.y);
-      }
+      sm.carry[lane] = h;
     }
+    if (feeder && it > 0) tc::bulk_wait_read();    // the output tile may be written again
     __syncthreads();
-    uint64_t h = sm.start[warp][lane];
+    const ulonglong2 g = part[warp][lane];
+    uint64_t h = fma2(g.x, sm.carry[lane], g.y);
+    if (p.states && on && mine % kGatedChunk == 0 && mine < job.live)
+      Two<float>::store(p.states + ((long long)job.b * p.NC + (job.first + mine) / kGatedChunk) * p.D + ch, h);
+    if (mine + R <= job.live) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      h = fma2(a[j], h, u[j]);
-      if (on && t0 + j < p.T) Two<E>::store(out + (long long)j * p.D, t0 + j < tl.len ? h : both(0.f));
+      for (int j = 0; j < R; ++j) {
+        h = fma2(a[j], h, u[j]);
+        Two<E>::store(&sm.out[0][mine + j][2 * lane], h);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        h = fma2(a[j], h, u[j]);
+        Two<E>::store(&sm.out[0][mine + j][2 * lane], mine + j < job.live ? h : both(0.f));
+      }
     }
+  }
+  if (it == 0) return;
+  tc::fence_smem_to_async();
+  __syncthreads();
+  if (feeder) {
+    feed.store(sm.job[(it - 1) % (2 * S)]);
+    tc::bulk_wait_all();
   }
 }
 
 // Gradient.  The tile's states come from the row of `states` before it, what reaches it from
 // behind from the tiles after it.
-template <class E, bool GATED, int R, int S, int C>
-__global__ void __launch_bounds__(32 * kGatedChunk / R, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
-  constexpr int NW = kGatedChunk / R, N = GATED ? 4 : 3;
-  using Shared = GatedShared<E, N, S, R, true>;
+template <class E, bool GATED, int TT, int R, int S, int C>
+__global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
+  static_assert(TT % kGatedChunk == 0, "a tile starts at a row of states");
+  constexpr int NW = TT / R, NI = GATED ? 4 : 3, NO = GATED ? 3 : 2;
+  using Shared = GatedShared<E, NI, NO, TT, R, S>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, N, S, R, true> feed{sm, p};
+  GatedFeed<E, NI, NO, TT, R, S> feed{sm, p, 0};
   if (feeder) feed.init();
   __syncthreads();
-  const unsigned total = (unsigned)((long long)p.B * p.strips * p.NC);
   const uint64_t none = both(0.f), one = both(1.f), minus = both(-1.f);
   unsigned phase = 0;
-  for (int it = 0;; ++it) {
-    const unsigned n = sm.ticket[it % (2 * S)];
-    if (n >= total) break;
-    const GatedTile tl(p, n, true);
-    const int s = it % S, ch = tl.strip * kGatedCols + 2 * lane, t0 = tl.chunk * kGatedChunk + warp * R;
+  int it = 0;
+  for (;; ++it) {
+    const GatedJob job = sm.job[it % (2 * S)];
+    if (!job.more) break;
+    const int s = it % S, mine = warp * R, ch = job.strip * kGatedCols + 2 * lane;
     const bool on = ch < p.D;
-    const long long o = ((long long)tl.b * p.T + t0) * p.D + ch, row = (long long)tl.b * p.D + ch;
-    E *dx = static_cast<E*>(p.out) + o, *df = static_cast<E*>(p.df) + o, *di = GATED ? static_cast<E*>(p.di) + o : nullptr;
-    if (tl.live == 0) {
-#pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (on && t0 + j < p.T) {
-          Two<E>::store(dx + (long long)j * p.D, none);
-          Two<E>::store(df + (long long)j * p.D, none);
-          if (GATED) Two<E>::store(di + (long long)j * p.D, none);
-        }
-      if (tl.rank == 0 && warp == 0 && on && p.s_out) {
-        Two<float> g;
-        g.r = make_float2(0.f, 0.f);
-        if (p.s_in) g.load(p.s_in + row);
-        Two<float>::store(p.s_out + row, g.get());
-      }
-      if (feeder) feed.feed(it + S);
-      __syncthreads();
-      continue;
+    uint64_t h0 = none;                            // the tile's first state: warp 1 hands it on
+    if (warp == 1 && on && job.live > 0)
+      h0 = load_pair(p.states + ((long long)job.b * p.NC + job.first / kGatedChunk) * p.D + ch);
+    bool ok = true;
+    if (job.live > 0) {
+      ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
+      phase ^= 1u << s;
     }
-    Two<float> h0;                                 // the tile's first state: warp 1 hands it on
-    h0.r = make_float2(0.f, 0.f);
-    if (warp == 1 && on) h0.load(p.states + ((long long)tl.b * p.NC + tl.chunk) * p.D + ch);
-    const bool ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
-    phase ^= 1u << s;
     Two<E> x[R], d[R];
+    // a, 1 - a, w and 1 - w of every token (without an input gate w is 1 - a)
     uint64_t a[R], c[R], w[GATED ? R : 1], v[GATED ? R : 1], P = one, L = none, r = none;
+    auto token = [&](int j) {
+      Two<E> f, i;
+      x[j].load(&sm.tile[s][0][mine + j][2 * lane]);
+      f.load(&sm.tile[s][1][mine + j][2 * lane]);
+      d[j].load(&sm.tile[s][2][mine + j][2 * lane]);
+      const Gate g = gate_of<E>(f.get());
+      a[j] = g.s;
+      c[j] = g.c;
+      if constexpr (GATED) {
+        i.load(&sm.tile[s][3][mine + j][2 * lane]);
+        const Gate k = gate_of<E>(i.get());
+        w[j] = k.s;
+        v[j] = k.c;
+      }
+    };
+    if (mine + R <= job.live) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (t0 + j < tl.len) {
-        Two<E> f, i;
-        x[j].load(&sm.tile[s][0][warp * R + j][2 * lane]);
-        f.load(&sm.tile[s][1][warp * R + j][2 * lane]);
-        d[j].load(&sm.tile[s][2][warp * R + j][2 * lane]);
-        const Gate g = gate_of<E>(f.get());
-        a[j] = g.s;
-        c[j] = g.c;
-        if constexpr (GATED) {
-          i.load(&sm.tile[s][3][warp * R + j][2 * lane]);
-          const Gate k = gate_of<E>(i.get());
-          w[j] = k.s;
-          v[j] = k.c;
-          L = fma2(a[j], L, mul2(w[j], x[j].get()));
-        } else {
-          L = fma2(a[j], L, mul2(c[j], x[j].get()));
-        }
-        P = mul2(a[j], P);
-      } else {
+      for (int j = 0; j < R; ++j) token(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
         a[j] = one;
         c[j] = none;
         if constexpr (GATED) w[j] = v[j] = none;
         x[j] = Two<E>();
         d[j] = Two<E>();
+        if (mine + j < job.live) token(j);
       }
+    }
+    auto write = [&](int j) {
+      if constexpr (GATED) return mul2(w[j], x[j].get());
+      else return mul2(c[j], x[j].get());
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      L = fma2(a[j], L, write(j));
+      P = mul2(a[j], P);
     }
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) r = mul2(a[j], add2(d[j].get(), r));
@@ -495,44 +541,47 @@ __global__ void __launch_bounds__(32 * kGatedChunk / R, C) gated_scan_backward_k
     uint64_t(*back)[32] = sm.back[it & 1];
     part[warp][lane] = make_ulonglong2(P, L);
     back[warp][lane] = r;
+    tc::fence_smem_to_async();
     if (__syncthreads_or(!ok)) {
-      feed.drain(phase);
+      gated_drain<S>(p, sm.full, phase);
       break;
     }
-    if (feeder) feed.feed(it + S);
+    if (feeder) {
+      if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
+      feed.load(it + S);
+    }
     if (warp == 0) {
-      P = one;
-      L = none;
-#pragma unroll
-      for (int k = NW - 1; k >= 0; --k) {
-        const uint64_t q = part[k][lane].x;
-        L = fma2(q, L, back[k][lane]);
-        P = mul2(q, P);
-      }
-      const int step = p.strips * 32;
-      const long long at = ((long long)tl.b * p.NC * p.strips + tl.strip) * 32 + lane, mine = at + (long long)tl.rank * step;
+      const long long row = (long long)job.b * p.D + ch;
       uint64_t g = none;
-      if (tl.rank == 0) {
-        if (p.s_in && on) {
-          Two<float> q;
-          q.load(p.s_in + row);
-          g = q.get();
-        }
-      } else {
-        if (!tl.last) publish(p.agg + mine, P, L);
-        g = look_back(p, at, step, tl.rank, sm.held);
-      }
-      const uint64_t end = fma2(P, g, L);
-      if (!tl.last) publish(p.incl + mine, end);
-      else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+      if (job.live > 0) {
+        P = one;
+        L = none;
 #pragma unroll
-      for (int k = NW - 1; k >= 0; --k) {
-        sm.ahead[k][lane] = g;
-        g = fma2(part[k][lane].x, g, back[k][lane]);
+        for (int k = NW - 1; k >= 0; --k) {
+          const uint64_t q = part[k][lane].x;
+          sm.behind[k][lane] = make_ulonglong2(P, L);
+          L = fma2(q, L, back[k][lane]);
+          P = mul2(q, P);
+        }
+        const int step = p.strips * 32;
+        const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
+        const long long here = at + (long long)job.rank * step;
+        if (job.rank > 0) {
+          if (!job.last) publish(p.agg + here, P, L);
+          g = look_back(p, at, step, job.rank, sm.held);
+        } else if (p.s_in && on) {
+          g = load_pair(p.s_in + row);
+        }
+        const uint64_t end = fma2(P, g, L);
+        if (!job.last) publish(p.incl + here, end);
+        else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+      } else if (job.rank == 0 && p.s_out && on) {
+        Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : none);
       }
+      sm.carry[lane] = g;
     }
     if (warp == 1) {
-      uint64_t h = h0.get();
+      uint64_t h = h0;
 #pragma unroll
       for (int k = 0; k < NW; ++k) {
         sm.start[k][lane] = h;
@@ -540,31 +589,38 @@ __global__ void __launch_bounds__(32 * kGatedChunk / R, C) gated_scan_backward_k
         h = fma2(g.x, h, g.y);
       }
     }
+    if (feeder && it > 0) tc::bulk_wait_read();
     __syncthreads();
     uint64_t h = sm.start[warp][lane], hp[R];      // hp: h_{t-1}
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       hp[j] = h;
-      h = fma2(a[j], h, mul2(GATED ? w[GATED ? j : 0] : c[j], x[j].get()));
+      h = fma2(a[j], h, write(j));
     }
-    r = sm.ahead[warp][lane];
+    const ulonglong2 q = sm.behind[warp][lane];
+    r = fma2(q.x, sm.carry[lane], q.y);
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
       const uint64_t xj = x[j].get(), G = add2(d[j].get(), r);
       r = mul2(a[j], G);                           // also a part of df; padding has a = 1, dout = 0
-      const bool there = t0 + j < tl.len;
-      if (on && t0 + j < p.T) {
-        if constexpr (GATED) {
-          const uint64_t gx = mul2(G, w[j]);
-          Two<E>::store(dx + (long long)j * p.D, there ? gx : none);
-          Two<E>::store(df + (long long)j * p.D, there ? mul2(mul2(r, c[j]), hp[j]) : none);
-          Two<E>::store(di + (long long)j * p.D, there ? mul2(mul2(gx, v[j]), xj) : none);
-        } else {
-          Two<E>::store(dx + (long long)j * p.D, there ? mul2(G, c[j]) : none);
-          Two<E>::store(df + (long long)j * p.D, there ? mul2(mul2(r, c[j]), fma2(xj, minus, hp[j])) : none);
-        }
+      const bool there = mine + j < job.live;
+      if constexpr (GATED) {
+        const uint64_t gx = mul2(G, w[j]);
+        Two<E>::store(&sm.out[0][mine + j][2 * lane], there ? gx : none);
+        Two<E>::store(&sm.out[1][mine + j][2 * lane], there ? mul2(mul2(r, c[j]), hp[j]) : none);
+        Two<E>::store(&sm.out[NO - 1][mine + j][2 * lane], there ? mul2(mul2(gx, v[j]), xj) : none);
+      } else {
+        Two<E>::store(&sm.out[0][mine + j][2 * lane], there ? mul2(G, c[j]) : none);
+        Two<E>::store(&sm.out[1][mine + j][2 * lane], there ? mul2(mul2(r, c[j]), fma2(xj, minus, hp[j])) : none);
       }
     }
+  }
+  if (it == 0) return;
+  tc::fence_smem_to_async();
+  __syncthreads();
+  if (feeder) {
+    feed.store(sm.job[(it - 1) % (2 * S)]);
+    tc::bulk_wait_all();
   }
 }
 

@@ -8,27 +8,40 @@ namespace prism {
 
 constexpr int kSMs = 152;
 
-template <class Shared, int R, int C, class F>
-cudaError_t launch_tiles(F* fn, const GatedArgs& a, std::atomic<unsigned long long>& done, cudaStream_t s) {
+template <class Shared, int TT, int R, int C, class F>
+cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& done, cudaStream_t s) {
   static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
   const cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)a.B * a.strips * a.NC, most = kSMs * C;
-  fn<<<(unsigned)(tiles < most ? tiles : most), 32 * kGatedChunk / R, sizeof(Shared), s>>>(a);
+  a.tiles = (a.T + TT - 1) / TT;
+  const long long tiles = (long long)a.B * a.strips * a.tiles, most = kSMs * C;
+  fn<<<(unsigned)(tiles < most ? tiles : most), 32 * TT / R, sizeof(Shared), s>>>(a);
   return cudaGetLastError();
 }
 
+template <class E, bool GATED, int TT, int R, int S, int C>
+cudaError_t launch_forward(const GatedArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, TT, R, S>, TT, R, C>(gated_scan_kernel<E, GATED, TT, R, S, C>, a,
+                                                                               done, s);
+}
+template <class E, bool GATED, int TT, int R, int S, int C>
+cudaError_t launch_backward(const GatedArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, TT, R, S>, TT, R, C>(
+      gated_scan_backward_kernel<E, GATED, TT, R, S, C>, a, done, s);
+}
+
+#ifndef GATED_BENCH
+// Stages and CTAs an SM are what its shared memory holds.
 template <class E, bool GATED>
 cudaError_t launch_scan_t(bool backward, const GatedArgs& a, cudaStream_t s) {
-  static std::atomic<unsigned long long> done[2];
-  constexpr bool half = sizeof(E) == 2;
-  if (backward) {
-    constexpr int R = 8, S = half ? 2 : 1, C = 2;
-    return launch_tiles<GatedShared<E, GATED ? 4 : 3, S, R, true>, R, C>(gated_scan_backward_kernel<E, GATED, R, S, C>, a,
-                                                                         done[1], s);
-  }
-  constexpr int R = 8, S = half ? 2 : 1, C = 3;
-  return launch_tiles<GatedShared<E, GATED ? 3 : 2, S, R, false>, R, C>(gated_scan_kernel<E, GATED, R, S, C>, a, done[0], s);
+  if constexpr (sizeof(E) == 2)
+    return backward ? launch_backward<E, GATED, gated_tile(1, true), 16, 2, 2>(a, s)
+                    : launch_forward<E, GATED, gated_tile(1, false), 16, GATED ? 1 : 2, 2>(a, s);
+  else
+    return backward ? launch_backward<E, GATED, gated_tile(0, true), 8, 1, GATED ? 1 : 2>(a, s)
+                    : launch_forward<E, GATED, gated_tile(0, false), 16, 1, 3>(a, s);
 }
 
 cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cudaStream_t s) {
@@ -47,5 +60,7 @@ cudaError_t launch_gated_decode(int dtype, const GatedDecodeArgs& a, cudaStream_
   if (dtype == 0) return a.i ? launch_gated_decode_t<float, true>(a, s) : launch_gated_decode_t<float, false>(a, s);
   return a.i ? launch_gated_decode_t<__nv_bfloat16, true>(a, s) : launch_gated_decode_t<__nv_bfloat16, false>(a, s);
 }
+
+#endif
 
 }  // namespace prism

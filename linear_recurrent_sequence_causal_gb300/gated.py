@@ -24,8 +24,8 @@ from .prism import PrismError
 
 PRISM_GATED_CHUNK = 64
 EXPORTS = ("prism_layer_norm", "prism_layer_norm_workspace_bytes", "prism_layer_norm_backward",
-           "prism_gated_scan_workspace_bytes", "prism_gated_scan_forward", "prism_gated_scan_backward",
-           "prism_gated_scan_decode_step", "prism_gated_status")
+           "prism_gated_scan_workspace_bytes", "prism_gated_scan_forward", "prism_gated_scan_backward_workspace_bytes",
+           "prism_gated_scan_backward", "prism_gated_scan_decode_step", "prism_gated_status")
 
 _vp, _int, _size = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
@@ -50,6 +50,7 @@ def load():
             ("prism_layer_norm_backward", [_vp] * 9 + [_size, _vp], _int),
             ("prism_gated_scan_workspace_bytes", [_vp], _size),
             ("prism_gated_scan_forward", [_vp] * 10 + [_size, _vp], _int),
+            ("prism_gated_scan_backward_workspace_bytes", [_vp], _size),
             ("prism_gated_scan_backward", [_vp] * 13 + [_size, _vp], _int),
             ("prism_gated_scan_decode_step", [_vp] * 5 + [_int, _vp, _vp, _vp], _int),
             ("prism_gated_status", [ctypes.POINTER(_int), _int], _int)):
@@ -99,7 +100,8 @@ def _gated_dims(xs, dtype, xst, fst, ist, dost, flags):
     if dost is not None:
         d.do_stride = _steps("d_out", xs, dost)
     rows = torch.Size((xs[0], -(-xs[1] // PRISM_GATED_CHUNK), xs[2]))
-    return d, ctypes.addressof(d), int(load().prism_gated_scan_workspace_bytes(ctypes.addressof(d))), rows
+    size = load().prism_gated_scan_workspace_bytes if dost is None else load().prism_gated_scan_backward_workspace_bytes
+    return d, ctypes.addressof(d), int(size(ctypes.addressof(d))), rows
 
 
 @functools.lru_cache(maxsize=256)

@@ -258,7 +258,7 @@ def test_single_tokens(B, D, gate, dtype):
     assert torch.equal(out2, a[:, 0]) and torch.equal(own, b)
 
 
-@pytest.mark.parametrize("T", [65, 3000])
+@pytest.mark.parametrize("T", [129, 3000])
 def test_waits_that_run_out(T):
     """The failure path's check sets the word and leaves the outputs as they are; short sequences wait for nothing."""
     z = make(2, T, 72, "bf16")
@@ -272,6 +272,6 @@ def test_waits_that_run_out(T):
     g2 = gated.prism_gated_scan_backward(c["x"], c["f"], states, c["do"], d_final_state=c["ds"], want_initial_state=True,
                                          **how)
     assert gated.gated_status() != 0 and all(torch.equal(g[n], g2[n]) for n in g)
-    x, f, i = (c[n][:, :64].contiguous() for n in ("x", "f", "i"))
+    x, f, i = (c[n][:, :32].contiguous() for n in ("x", "f", "i"))
     gated.prism_gated_scan_forward(x, f, input_gate=i, flags=prism.PRISM_FLAG_CHECK_WAIT_TIMEOUT)
     assert gated.gated_status() == 0
