@@ -110,8 +110,8 @@ PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const v
                                            const void* input_gate, float* state, int n_states,
                                            const int32_t* slots, void* out, void* stream);
 
-/* Failure detection: a tile's wait for the state before it is bounded (about a second); one that gives
- * up sets the library's word for the current device, which stays set until it is cleared, and the
+/* Failure detection: every wait, a tile's for the state before it and a kernel's for its own copies, is
+ * bounded (about a second); one that gives up sets the library's word for the current device, which stays set until it is cleared, and the
  * call's outputs are then undefined.  Synchronises the device and returns the word in *word (0: no
  * wait gave up), clearing it when `clear` is nonzero.  PRISM_ERR_INVALID_ARG for a NULL word,
  * PRISM_ERR_CUDA when the synchronisation or the copy fails.

@@ -22,6 +22,6 @@ cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cuda
 cudaError_t launch_gated_decode(int dtype, const GatedDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm(int dtype, const LayerNormArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(int dtype, const LayerNormArgs& a, cudaStream_t s);
-size_t layer_norm_partial_rows(int D);   // rows [2][D] that the gradient's workspace holds
+size_t layer_norm_partial_rows(int dtype, int D);      // rows [2][D] that the gradient's workspace holds
 
 }  // namespace prism

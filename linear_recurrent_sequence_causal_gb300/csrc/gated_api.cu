@@ -38,6 +38,10 @@ int check_norm(const prism_layer_norm_dims* d) {
   return d->D > prism::kLayerNormMaxD ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
 }
 
+bool one_behind_the_other(const long long (&step)[2], const prism_layer_norm_dims* d) {
+  return step[1] == d->D && (d->B == 1 || step[0] == (long long)d->T * d->D);
+}
+
 int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight, const int32_t* seq_lens, void* out,
               prism::LayerNormArgs& a) {
   a = prism::LayerNormArgs();
@@ -45,7 +49,9 @@ int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight
   a.lens = seq_lens;
   a.B = d->B; a.T = d->T; a.D = d->D;
   a.eps = d->eps;
-  return resolve(d->x_stride, d->B, d->T, d->D, d->dtype, a.xs);
+  const int rc = resolve(d->x_stride, d->B, d->T, d->D, d->dtype, a.xs);
+  a.whole = one_behind_the_other(a.xs, d);
+  return rc;
 }
 
 // ---- gated recurrence ----
@@ -71,6 +77,14 @@ int check_gated(const prism_gated_dims* d, unsigned flags) {
 constexpr size_t kCounter = 256;
 size_t gated_bytes(const prism_gated_dims* d, bool backward) {
   return d->T <= tile_of(d, backward) ? 0 : kCounter + (size_t)tiles_of(d, backward) * 32 * 24;
+}
+
+// The device's word of waits that gave up.
+int find_status(int** to) {
+  void* word = nullptr;
+  if (cudaGetSymbolAddress(&word, g_gated_status) != cudaSuccess) return PRISM_ERR_CUDA;
+  *to = static_cast<int*>(word);
+  return PRISM_OK;
 }
 
 struct GatedInput {
@@ -111,9 +125,8 @@ int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, con
   for (int i = 0; i < nout; ++i)
     if (!make_map(&a.to[i], out[i], whole, d, tile_of(d, backward))) return PRISM_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void* word = nullptr;
-  if (cudaGetSymbolAddress(&word, g_gated_status) != cudaSuccess) return PRISM_ERR_CUDA;
-  a.status = static_cast<int*>(word);
+  const int rc = find_status(&a.status);
+  if (rc != PRISM_OK) return rc;
   if (need) {
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<unsigned*>(w);
@@ -138,6 +151,7 @@ extern "C" PRISM_API int prism_layer_norm(const prism_layer_norm_dims* dims, con
   prism::LayerNormArgs a;
   if ((rc = fill_norm(dims, x, weight, seq_lens, out, a)) != PRISM_OK) return rc;
   a.b = bias;
+  if ((rc = find_status(&a.status)) != PRISM_OK) return rc;
   return prism::launch_layer_norm(dims->dtype == PRISM_F32 ? 0 : 1, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PRISM_OK
              : PRISM_ERR_LAUNCH;
@@ -145,7 +159,7 @@ extern "C" PRISM_API int prism_layer_norm(const prism_layer_norm_dims* dims, con
 
 extern "C" PRISM_API size_t prism_layer_norm_workspace_bytes(const prism_layer_norm_dims* dims) {
   if (check_norm(dims) != PRISM_OK) return 0;
-  return prism::layer_norm_partial_rows(dims->D) * 2 * dims->D * 4;
+  return prism::layer_norm_partial_rows(dims->dtype == PRISM_F32 ? 0 : 1, dims->D) * 2 * dims->D * 4;
 }
 
 extern "C" PRISM_API int prism_layer_norm_backward(const prism_layer_norm_dims* dims, const void* x,
@@ -164,9 +178,11 @@ extern "C" PRISM_API int prism_layer_norm_backward(const prism_layer_norm_dims* 
   prism::LayerNormArgs a;
   if ((rc = fill_norm(dims, x, weight, seq_lens, dx, a)) != PRISM_OK) return rc;
   if ((rc = resolve(dims->do_stride, dims->B, dims->T, dims->D, dims->dtype, a.ds)) != PRISM_OK) return rc;
+  a.whole = a.whole && one_behind_the_other(a.ds, dims);
   a.dy = d_out;
   a.dw = d_weight; a.db = d_bias;
   a.partial = static_cast<float*>(workspace);
+  if ((rc = find_status(&a.status)) != PRISM_OK) return rc;
   return prism::launch_layer_norm_backward(dims->dtype == PRISM_F32 ? 0 : 1, a, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? PRISM_OK

@@ -131,13 +131,6 @@ template <> struct Two<__nv_bfloat16> {
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
   }
 };
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t both(float x) { return pack2(x, x); }
-
 // sigmoid(z) and 1 - sigmoid(z), both to their own precision: with e = exp(-|z|) <= 1 the smaller
 // one is e / (1 + e) and the other its difference from 1, rounded once.  A gate near 1 is what a long
 // memory multiplies with for thousands of tokens, so it may not have a bias.
