@@ -58,7 +58,7 @@ int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight
 
 int strips_of(const prism_gated_dims* d) { return (d->D + prism::kGatedCols - 1) / prism::kGatedCols; }
 int chunks_of(const prism_gated_dims* d) { return (d->T + prism::kGatedChunk - 1) / prism::kGatedChunk; }
-int tile_of(const prism_gated_dims* d, bool backward) { return prism::gated_tile(d->dtype == PRISM_F32 ? 0 : 1, backward); }
+int tile_of(const prism_gated_dims* d, bool backward) { return prism::gated_tile(d->dtype == PRISM_F32 ? 0 : 1, backward, d->T); }
 long long tiles_of(const prism_gated_dims* d, bool backward) {
   const int t = tile_of(d, backward);
   return (long long)d->B * strips_of(d) * (((long long)d->T + t - 1) / t);
@@ -87,9 +87,15 @@ int find_status(int** to) {
   return PRISM_OK;
 }
 
-struct GatedInput {
-  const void* p;
-  const long long* given;                // its strides as they came
+// A call's tensors; the inputs in the order of GatedArgs::map.
+struct GatedCall {
+  const void* in[4];
+  const long long* given[4];             // strides of the inputs as they came
+  void* out[3];
+  int inputs, outputs;
+  const float* s_in;
+  float *s_out, *states;
+  const int32_t* lens;
 };
 
 // TMA map of a [B][T][D] tensor as (D, T, B), in boxes of a tile.
@@ -105,26 +111,50 @@ bool make_map(CUtensorMap* m, const void* p, const long long (&step)[2], const p
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int run_gated(const prism_gated_dims* d, bool backward, prism::GatedArgs& a, const GatedInput* in, int nin,
-              void* const* out, int nout, void* workspace, size_t workspace_bytes, void* stream) {
-  long long step[4][2];
-  for (int i = 0; i < nin; ++i) {
-    const int rc = resolve(in[i].given, d->B, d->T, d->D, d->dtype, step[i]);
+int run_short(const prism_gated_dims* d, bool backward, const GatedCall& c, const long long (&step)[4][2], cudaStream_t s) {
+  prism::GatedShortArgs a = prism::GatedShortArgs();
+  a.x = c.in[0]; a.f = c.in[1];
+  a.dy = backward ? c.in[2] : nullptr;
+  a.i = c.in[backward ? 3 : 2];
+  for (int k = 0; k < 2; ++k) {
+    a.xs[k] = step[0][k];
+    a.fs[k] = step[1][k];
+    a.ds[k] = step[2][k];
+    a.is[k] = step[backward ? 3 : 2][k];
+  }
+  a.s_in = c.s_in; a.s_out = c.s_out; a.states = c.states;
+  a.out = c.out[0]; a.df = c.out[1]; a.di = c.out[2];
+  a.lens = c.lens;
+  a.B = d->B; a.T = d->T; a.D = d->D;
+  return prism::launch_gated_short(d->dtype == PRISM_F32 ? 0 : 1, backward, a, s) == cudaSuccess ? PRISM_OK : PRISM_ERR_LAUNCH;
+}
+
+int run_gated(const prism_gated_dims* d, bool backward, const GatedCall& c, void* workspace, size_t workspace_bytes,
+              void* stream) {
+  long long step[4][2] = {};
+  for (int i = 0; i < c.inputs; ++i) {
+    const int rc = resolve(c.given[i], d->B, d->T, d->D, d->dtype, step[i]);
     if (rc != PRISM_OK) return rc;
   }
   const size_t need = gated_bytes(d, backward);
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
   if (need && (!workspace || workspace_bytes < need)) return PRISM_ERR_WORKSPACE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->T <= prism::kGatedShort) return run_short(d, backward, c, step, s);
+  prism::GatedArgs a = prism::GatedArgs();
+  a.s_in = c.s_in; a.s_out = c.s_out; a.states = c.states;
+  a.lens = c.lens;
   a.B = d->B; a.T = d->T; a.D = d->D;
   a.NC = chunks_of(d);
   a.strips = strips_of(d);
+  a.gated = c.in[backward ? 3 : 2] != nullptr;
   a.check = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
-  for (int i = 0; i < nin; ++i)
-    if (!make_map(&a.map[i], in[i].p, step[i], d, tile_of(d, backward))) return PRISM_ERR_CUDA;
+  const int tile = tile_of(d, backward);
+  for (int i = 0; i < c.inputs; ++i)
+    if (!make_map(&a.map[i], c.in[i], step[i], d, tile)) return PRISM_ERR_CUDA;
   const long long whole[2] = {(long long)d->T * d->D, d->D};
-  for (int i = 0; i < nout; ++i)
-    if (!make_map(&a.to[i], out[i], whole, d, tile_of(d, backward))) return PRISM_ERR_CUDA;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int i = 0; i < c.outputs; ++i)
+    if (!make_map(&a.to[i], c.out[i], whole, d, tile)) return PRISM_ERR_CUDA;
   const int rc = find_status(&a.status);
   if (rc != PRISM_OK) return rc;
   if (need) {
@@ -207,12 +237,9 @@ extern "C" PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, 
   const void* opt[] = {input_gate, initial_state, final_state, states};
   if ((rc = check_pointers(req, opt, 4)) != PRISM_OK) return rc;
   if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
-  prism::GatedArgs a = prism::GatedArgs();
-  a.s_in = initial_state; a.s_out = final_state; a.states = states;
-  a.lens = seq_lens;
-  a.gated = input_gate != nullptr;
-  const GatedInput in[3] = {{x, dims->x_stride}, {forget, dims->f_stride}, {input_gate, dims->i_stride}};
-  return run_gated(dims, false, a, in, a.gated ? 3 : 2, &out, 1, workspace, workspace_bytes, stream);
+  const GatedCall c = {{x, forget, input_gate}, {dims->x_stride, dims->f_stride, dims->i_stride}, {out},
+                       input_gate ? 3 : 2, 1, initial_state, final_state, states, seq_lens};
+  return run_gated(dims, false, c, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims, const void* x, const void* forget,
@@ -228,15 +255,10 @@ extern "C" PRISM_API int prism_gated_scan_backward(const prism_gated_dims* dims,
   const void* opt[] = {input_gate, d_final_state, d_input_gate, d_initial_state};
   if ((rc = check_pointers(req, opt, 4)) != PRISM_OK) return rc;
   if ((rc = check_words(seq_lens, nullptr)) != PRISM_OK) return rc;
-  prism::GatedArgs a = prism::GatedArgs();
-  a.s_in = d_final_state; a.s_out = d_initial_state;
-  a.states = const_cast<float*>(states);
-  a.lens = seq_lens;
-  a.gated = input_gate != nullptr;
-  const GatedInput in[4] = {{x, dims->x_stride}, {forget, dims->f_stride}, {d_out, dims->do_stride},
-                            {input_gate, dims->i_stride}};
-  void* const out[3] = {dx, d_forget, d_input_gate};
-  return run_gated(dims, true, a, in, a.gated ? 4 : 3, out, a.gated ? 3 : 2, workspace, workspace_bytes, stream);
+  const GatedCall c = {{x, forget, d_out, input_gate}, {dims->x_stride, dims->f_stride, dims->do_stride, dims->i_stride},
+                       {dx, d_forget, d_input_gate}, input_gate ? 4 : 3, input_gate ? 3 : 2, d_final_state, d_initial_state,
+                       const_cast<float*>(states), seq_lens};
+  return run_gated(dims, true, c, workspace, workspace_bytes, stream);
 }
 
 extern "C" PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const void* x, const void* forget,

@@ -58,7 +58,6 @@ struct GatedDecodeArgs {
 
 constexpr unsigned kAbsent = 0xffffffffu;          // not published yet
 constexpr unsigned long long kWaitNs = 1000000000ull, kCheckNs = 1000000ull;
-constexpr int kLookBack = 8;                      // (P, L) that a tile holds on its way back
 
 __device__ __forceinline__ unsigned canonical(float x) {
   const unsigned u = __float_as_uint(x);
@@ -191,59 +190,141 @@ struct GatedTile {
   }
 };
 
-// The state before the tile of rank `rank` >= 1 (one warp; lane: two channels).  `at` is the lane's
-// slot at rank 0 and `step` the slots from one rank to the next.  Several tiles are looked at together: a
-// look at one takes an L2 access' time.
+// The look back of a tile of rank >= 1.  `at` is the lane's slot at rank 0 and `step` the slots from one rank
+// to the next (a lane: two channels).  A look takes an L2 access' time, so kLooks tiles are looked at together.
 constexpr int kLooks = 4;
-__device__ __forceinline__ uint64_t look_back(const GatedArgs& p, long long at, int step, int rank, ulonglong2 (*held)[32]) {
+struct GatedLook {
+  uint2 u[kLooks];
+  ulonglong2 g[kLooks];
+  __device__ __forceinline__ GatedLook(const GatedArgs& p, long long at, int step, int rank) {
+#pragma unroll
+    for (int k = 0; k < kLooks; ++k) {
+      const long long s = at + (long long)max(rank - k, 0) * step;
+      u[k] = peek(p.incl + s);
+      g[k] = peek(p.agg + s);
+    }
+  }
+  // whole warp: the tile knows its state; its (P, L) is there
+  __device__ __forceinline__ bool knows(int k) const { return __all_sync(0xffffffffu, u[k].x != kAbsent && u[k].y != kAbsent); }
+  __device__ __forceinline__ bool has(int k) const {
+    return __all_sync(0xffffffffu, (unsigned)g[k].x != kAbsent && (unsigned)g[k].y != kAbsent);
+  }
+  __device__ __forceinline__ uint64_t state(int k) const { return pack2(__uint_as_float(u[k].x), __uint_as_float(u[k].y)); }
+};
+// h behind the tile that published g, from h before it
+__device__ __forceinline__ uint64_t step_over(ulonglong2 g, uint64_t h) {
+  return fma2(pack2(__uint_as_float((unsigned)g.x), __uint_as_float((unsigned)g.y)), h,
+              pack2(__uint_as_float((unsigned)(g.x >> 32)), __uint_as_float((unsigned)(g.y >> 32))));
+}
+
+// One warp walks back over the nearest kNear tiles until it comes to one that knows its state (true), or all
+// of them have only their own run (false: a long chain that every tile waits for; look_far takes longer steps).
+constexpr int kNear = 8;
+__device__ __forceinline__ bool look_near(const GatedArgs& p, long long at, int step, int rank, ulonglong2 (*held)[32],
+                                          uint64_t& h) {
   const int lane = threadIdx.x & 31;
   const unsigned all = 0xffffffffu;
   const unsigned long long begin = wall_ns();
   if (p.check) {                                   // a word that nobody writes yet: this tile's own state
     while (true) {
-      const uint2 h = peek(p.incl + at + (long long)rank * step);
-      if (__any_sync(all, h.x != kAbsent || wall_ns() - begin > kCheckNs)) break;
+      const uint2 u = peek(p.incl + at + (long long)rank * step);
+      if (__any_sync(all, u.x != kAbsent || wall_ns() - begin > kCheckNs)) break;
     }
     if (lane == 0) atomicOr(p.status, 1);
   }
-  int n = 0, j = rank - 1;
-  uint64_t h = both(0.f);
+  int n = 0;
+  h = both(0.f);
   for (bool found = false; !found;) {
-    uint2 u[kLooks];
-    ulonglong2 g[kLooks];
-#pragma unroll
-    for (int k = 0; k < kLooks; ++k) {
-      const long long s = at + (long long)max(j - k, 0) * step;
-      u[k] = peek(p.incl + s);
-      g[k] = peek(p.agg + s);
-    }
-    bool going = true, moved = false;
+    const int before = n;
+    const GatedLook look(p, at, step, rank - 1 - n);
+    bool going = true;
 #pragma unroll
     for (int k = 0; k < kLooks; ++k) {
       if (!going) continue;
-      if (__all_sync(all, u[k].x != kAbsent && u[k].y != kAbsent)) {
-        h = pack2(__uint_as_float(u[k].x), __uint_as_float(u[k].y));
+      if (look.knows(k)) {
+        h = look.state(k);
         found = true;
         going = false;
-      } else if (n < kLookBack && j > 0 && __all_sync(all, (unsigned)g[k].x != kAbsent && (unsigned)g[k].y != kAbsent)) {
-        held[n++][lane] = g[k];
-        --j;
-        moved = true;
+      } else if (n < kNear && rank - 1 - n > 0 && look.has(k)) {
+        held[n++][lane] = look.g[k];
       } else {
         going = false;
       }
     }
-    if (!found && !moved && __any_sync(all, wall_ns() - begin > kWaitNs)) {
+    if (found) break;
+    if (n == kNear) return false;
+    if (n == before && __any_sync(all, wall_ns() - begin > kWaitNs)) {
       if (lane == 0) atomicOr(p.status, 1);
       break;
     }
   }
-  while (n > 0) {
-    const ulonglong2 g = held[--n][lane];          // (P, L) of either channel
-    h = fma2(pack2(__uint_as_float((unsigned)g.x), __uint_as_float((unsigned)g.y)), h,
-             pack2(__uint_as_float((unsigned)(g.x >> 32)), __uint_as_float((unsigned)(g.y >> 32))));
+  while (n > 0) h = step_over(held[--n][lane], h);
+  return true;
+}
+
+// All NW warps look, kLooks tiles each, in turns with a barrier; warp 0 gets the state.
+template <int NW>
+struct GatedFar {
+  static_assert(NW == 4 || NW == 8, "a byte a warp, in one or two words");
+  ulonglong2 held[kLooks * NW][32];                // (P, L), or the state that ends the walk
+  unsigned has[2][NW / 4], knows[2][NW / 4];       // a byte a warp, a bit a tile
+  int late[2];
+};
+// four bits of each byte, side by side
+__device__ __forceinline__ unsigned close_up(unsigned x) {
+  x = (x | x >> 4) & 0x00ff00ffu;
+  return (x | x >> 8) & 0xffffu;
+}
+template <int NW>
+__device__ __forceinline__ uint64_t look_far(const GatedArgs& p, long long at, int step, int rank, GatedFar<NW>& far) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned long long begin = wall_ns();
+  for (int turn = 0;; turn ^= 1) {
+    const int first = warp * kLooks;
+    const GatedLook look(p, at, step, rank - 1 - first);
+    unsigned has = 0, knows = 0;
+#pragma unroll
+    for (int k = 0; k < kLooks; ++k) {
+      const int r = rank - 1 - first - k;
+      const bool a = look.knows(k), b = look.has(k);
+      if (r >= 0 && a) knows |= 1u << k;
+      if (r > 0 && b && !a) has |= 1u << k;
+      far.held[first + k][lane] = a ? make_ulonglong2(look.state(k), 0) : look.g[k];
+    }
+    if (lane == 0) {
+      reinterpret_cast<unsigned char*>(far.has[turn])[warp] = has;
+      reinterpret_cast<unsigned char*>(far.knows[turn])[warp] = knows;
+    }
+    if (threadIdx.x == 0) far.late[turn] = wall_ns() - begin > kWaitNs;
+    __syncthreads();
+    has = close_up(far.has[turn][0]);
+    knows = close_up(far.knows[turn][0]);
+    if constexpr (NW == 8) {
+      has |= close_up(far.has[turn][1]) << 16;
+      knows |= close_up(far.knows[turn][1]) << 16;
+    }
+    const int n = has == 0xffffffffu ? 32 : __ffs(~has) - 1;       // tiles to step over
+    if (n < 32 && (knows >> n & 1)) {
+      uint64_t h = both(0.f);
+      if (warp == 0) {
+        h = far.held[n][lane].x;
+#pragma unroll 1
+        for (int k = n; k > 0; k -= 8) {           // eight at a time: their loads do not wait for each other
+          ulonglong2 g[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = far.held[max(k - 1 - j, 0)][lane];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (k - 1 - j >= 0) h = step_over(g[j], h);
+        }
+      }
+      return h;
+    }
+    if (far.late[turn]) {
+      if (threadIdx.x == 0) atomicOr(p.status, 1);
+      return both(0.f);
+    }
   }
-  return h;
 }
 
 // What a CTA needs to know about its tile: computed by one thread, read by all.
@@ -263,7 +344,8 @@ struct GatedShared {
   alignas(128) E tile[S][NI][TT][kGatedCols];
   alignas(128) E out[NO][TT][kGatedCols];
   ulonglong2 part[2][NW][32];                      // (P, L) of a warp's tokens, then of those before them: both channels of P, of L
-  ulonglong2 held[kLookBack][32];
+  GatedFar<NW> far;
+  int found;                                       // the state came by look_near
   uint64_t carry[32];                              // what reaches the tile
   // gradient: r that a warp's tokens send backwards, (P, r) of what is behind them, the state before them
   uint64_t back[2][BACK ? NW : 1][32], start[BACK ? NW : 1][32];
@@ -396,11 +478,18 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
       feed.load(it + S);
     }
-    const int ch = job.strip * kGatedCols + 2 * lane;
+    const int ch = job.strip * kGatedCols + 2 * lane, step = p.strips * 32;
     const bool on = ch < p.D;
+    const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
+    const long long row = (long long)job.b * p.D + ch;
+    auto arrive = [&](uint64_t h) {                // the state before the tile is known
+      const uint64_t end = fma2(P, h, L);
+      if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
+      else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+      sm.carry[lane] = h;
+    };
     if (warp == 0) {
-      const long long row = (long long)job.b * p.D + ch;
-      uint64_t h = both(0.f);
+      bool found = true;
       if (job.live > 0) {
         P = both(1.f);
         L = both(0.f);
@@ -411,25 +500,28 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
           L = fma2(g.x, L, g.y);
           P = mul2(g.x, P);
         }
-        const int step = p.strips * 32;
-        const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
-        const long long here = at + (long long)job.rank * step;
+        uint64_t h = both(0.f);
         if (job.rank > 0) {
-          if (!job.last) publish(p.agg + here, P, L);
-          h = look_back(p, at, step, job.rank, sm.held);
+          if (!job.last) publish(p.agg + at + (long long)job.rank * step, P, L);
+          found = look_near(p, at, step, job.rank, sm.far.held, h);
         } else if (p.s_in && on) {
           h = load_pair(p.s_in + row);
         }
-        const uint64_t end = fma2(P, h, L);
-        if (!job.last) publish(p.incl + here, end);
-        else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
-      } else if (job.rank == 0 && p.s_out && on) { // a sequence without tokens
-        Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : both(0.f));
+        if (found) arrive(h);
+      } else {
+        if (job.rank == 0 && p.s_out && on)        // a sequence without tokens
+          Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : both(0.f));
+        sm.carry[lane] = both(0.f);
       }
-      sm.carry[lane] = h;
+      if (lane == 0) sm.found = found;
     }
     if (feeder && it > 0) tc::bulk_wait_read();    // the output tile may be written again
     __syncthreads();
+    if (!sm.found) {
+      const uint64_t h = look_far<NW>(p, at, step, job.rank, sm.far);
+      if (warp == 0) arrive(h);
+      __syncthreads();
+    }
     const ulonglong2 g = part[warp][lane];
     uint64_t h = fma2(g.x, sm.carry[lane], g.y);
     if (p.states && on && mine % kGatedChunk == 0 && mine < job.live)
@@ -543,9 +635,17 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
       feed.load(it + S);
     }
+    const int step = p.strips * 32;
+    const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
+    const long long row = (long long)job.b * p.D + ch;
+    auto arrive = [&](uint64_t g) {                // what comes from behind the tile is known
+      const uint64_t end = fma2(P, g, L);
+      if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
+      else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+      sm.carry[lane] = g;
+    };
     if (warp == 0) {
-      const long long row = (long long)job.b * p.D + ch;
-      uint64_t g = none;
+      bool found = true;
       if (job.live > 0) {
         P = one;
         L = none;
@@ -556,22 +656,20 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
           L = fma2(q, L, back[k][lane]);
           P = mul2(q, P);
         }
-        const int step = p.strips * 32;
-        const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
-        const long long here = at + (long long)job.rank * step;
+        uint64_t g = none;
         if (job.rank > 0) {
-          if (!job.last) publish(p.agg + here, P, L);
-          g = look_back(p, at, step, job.rank, sm.held);
+          if (!job.last) publish(p.agg + at + (long long)job.rank * step, P, L);
+          found = look_near(p, at, step, job.rank, sm.far.held, g);
         } else if (p.s_in && on) {
           g = load_pair(p.s_in + row);
         }
-        const uint64_t end = fma2(P, g, L);
-        if (!job.last) publish(p.incl + here, end);
-        else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
-      } else if (job.rank == 0 && p.s_out && on) {
-        Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : none);
+        if (found) arrive(g);
+      } else {
+        if (job.rank == 0 && p.s_out && on)
+          Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : none);
+        sm.carry[lane] = none;
       }
-      sm.carry[lane] = g;
+      if (lane == 0) sm.found = found;
     }
     if (warp == 1) {
       uint64_t h = h0;
@@ -584,6 +682,11 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     }
     if (feeder && it > 0) tc::bulk_wait_read();
     __syncthreads();
+    if (!sm.found) {
+      const uint64_t g = look_far<NW>(p, at, step, job.rank, sm.far);
+      if (warp == 0) arrive(g);
+      __syncthreads();
+    }
     uint64_t h = sm.start[warp][lane], hp[R];      // hp: h_{t-1}
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -615,6 +718,135 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     feed.store(sm.job[(it - 1) % (2 * S)]);
     tc::bulk_wait_all();
   }
+}
+
+// Short sequences, up to kGatedShort tokens: a thread takes two channels of one sequence from token to token,
+// and nothing waits for anything.  (A tile of 64 tokens would be mostly padding: 512 sequences of 4
+// tokens, 1512 channels, fp32, took 47 us in tiles.)
+struct GatedShortArgs {
+  const void *x, *f, *i, *dy;                      // i null: w = 1 - a
+  long long xs[2], fs[2], is[2], ds[2];            // strides: sequence, token (elements)
+  const float* s_in;                               // as GatedArgs
+  float *s_out, *states;
+  void *out, *df, *di;
+  const int* lens;
+  int B, T, D;
+};
+constexpr int kGatedShortThreads = 128, kGatedAhead = 8;   // tokens whose loads are in flight together
+
+struct GatedShortPlace {
+  int b, ch, len;
+  __device__ __forceinline__ GatedShortPlace(const GatedShortArgs& p, long long n) {
+    b = (int)(n / (p.D / 2));
+    ch = 2 * (int)(n - (long long)b * (p.D / 2));
+    len = b < p.B ? p.lens ? min(max(__ldg(p.lens + b), 0), p.T) : p.T : 0;
+  }
+};
+
+template <class E, bool GATED>
+__global__ void __launch_bounds__(kGatedShortThreads) gated_short_kernel(GatedShortArgs p) {
+  const GatedShortPlace at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
+  if (at.b >= p.B) return;
+  const E* x = static_cast<const E*>(p.x) + at.b * p.xs[0] + at.ch;
+  const E* f = static_cast<const E*>(p.f) + at.b * p.fs[0] + at.ch;
+  const E* i = GATED ? static_cast<const E*>(p.i) + at.b * p.is[0] + at.ch : nullptr;
+  E* out = static_cast<E*>(p.out) + (long long)at.b * p.T * p.D + at.ch;
+  const long long row = (long long)at.b * p.D + at.ch;
+  uint64_t h = p.s_in ? load_pair(p.s_in + row) : both(0.f);
+  if (p.states && at.len > 0) Two<float>::store(p.states + row, h);    // T <= 64: one row a sequence
+  for (int t0 = 0; t0 < p.T; t0 += kGatedAhead) {
+    Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead];
+#pragma unroll
+    for (int j = 0; j < kGatedAhead; ++j)
+      if (t0 + j < at.len) {
+        rx[j].load(x + (t0 + j) * p.xs[1]);
+        rf[j].load(f + (t0 + j) * p.fs[1]);
+        if (GATED) ri[j].load(i + (t0 + j) * p.is[1]);
+      }
+#pragma unroll
+    for (int j = 0; j < kGatedAhead; ++j)
+      if (t0 + j < p.T) {
+        if (t0 + j < at.len) {
+          const Gate g = gate_of<E>(rf[j].get());
+          h = fma2(g.s, h, mul2(GATED ? sigmoid_of<E>(ri[j].get()) : g.c, rx[j].get()));
+        }
+        Two<E>::store(out + (long long)(t0 + j) * p.D, t0 + j < at.len ? h : both(0.f));
+      }
+  }
+  if (p.s_out) Two<float>::store(p.s_out + row, h);
+}
+
+// Gradient: forwards for the states before every token, which stay in registers, then backwards.
+template <class E, bool GATED>
+__global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kernel(GatedShortArgs p) {
+  const GatedShortPlace at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
+  if (at.b >= p.B) return;
+  const E* x = static_cast<const E*>(p.x) + at.b * p.xs[0] + at.ch;
+  const E* f = static_cast<const E*>(p.f) + at.b * p.fs[0] + at.ch;
+  const E* i = GATED ? static_cast<const E*>(p.i) + at.b * p.is[0] + at.ch : nullptr;
+  const E* d = static_cast<const E*>(p.dy) + at.b * p.ds[0] + at.ch;
+  const long long o = (long long)at.b * p.T * p.D + at.ch, row = (long long)at.b * p.D + at.ch;
+  E *dx = static_cast<E*>(p.out) + o, *df = static_cast<E*>(p.df) + o, *di = GATED ? static_cast<E*>(p.di) + o : nullptr;
+  const uint64_t none = both(0.f), minus = both(-1.f);
+  uint64_t h = at.len > 0 ? load_pair(p.states + row) : none, before[kGatedShort];
+#pragma unroll
+  for (int t0 = 0; t0 < kGatedShort; t0 += kGatedAhead) {
+    if (t0 >= at.len) break;
+    Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead];
+#pragma unroll
+    for (int j = 0; j < kGatedAhead; ++j)
+      if (t0 + j < at.len) {
+        rx[j].load(x + (t0 + j) * p.xs[1]);
+        rf[j].load(f + (t0 + j) * p.fs[1]);
+        if (GATED) ri[j].load(i + (t0 + j) * p.is[1]);
+      }
+#pragma unroll
+    for (int j = 0; j < kGatedAhead; ++j) {
+      before[t0 + j] = h;
+      if (t0 + j < at.len) {
+        const Gate g = gate_of<E>(rf[j].get());
+        h = fma2(g.s, h, mul2(GATED ? sigmoid_of<E>(ri[j].get()) : g.c, rx[j].get()));
+      }
+    }
+  }
+  uint64_t r = p.s_in ? load_pair(p.s_in + row) : none;
+#pragma unroll
+  for (int t0 = kGatedShort - kGatedAhead; t0 >= 0; t0 -= kGatedAhead) {
+    if (t0 >= p.T) continue;
+    Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead], rd[kGatedAhead];
+#pragma unroll
+    for (int j = 0; j < kGatedAhead; ++j)
+      if (t0 + j < at.len) {
+        rx[j].load(x + (t0 + j) * p.xs[1]);
+        rf[j].load(f + (t0 + j) * p.fs[1]);
+        if (GATED) ri[j].load(i + (t0 + j) * p.is[1]);
+        rd[j].load(d + (t0 + j) * p.ds[1]);
+      }
+#pragma unroll
+    for (int j = kGatedAhead - 1; j >= 0; --j) {
+      if (t0 + j >= p.T) continue;
+      const long long to = (long long)(t0 + j) * p.D;
+      uint64_t gx = none, gf = none, gi = none;
+      if (t0 + j < at.len) {
+        const Gate g = gate_of<E>(rf[j].get());
+        const uint64_t xj = rx[j].get(), G = add2(rd[j].get(), r);
+        r = mul2(g.s, G);
+        if constexpr (GATED) {
+          const Gate w = gate_of<E>(ri[j].get());
+          gx = mul2(G, w.s);
+          gf = mul2(mul2(r, g.c), before[t0 + j]);
+          gi = mul2(mul2(gx, w.c), xj);
+        } else {
+          gx = mul2(G, g.c);
+          gf = mul2(mul2(r, g.c), fma2(xj, minus, before[t0 + j]));
+        }
+      }
+      Two<E>::store(dx + to, gx);
+      Two<E>::store(df + to, gf);
+      if (GATED) Two<E>::store(di + to, gi);
+    }
+  }
+  if (p.s_out) Two<float>::store(p.s_out + row, r);
 }
 
 // One token: a lane takes two channels of one sequence.

@@ -33,20 +33,35 @@ cudaError_t launch_backward(const GatedArgs& a, cudaStream_t s) {
 }
 
 #ifndef GATED_BENCH
-// Stages and CTAs an SM are what its shared memory holds.
+// Stages and CTAs an SM are what its shared memory and registers hold.
 template <class E, bool GATED>
 cudaError_t launch_scan_t(bool backward, const GatedArgs& a, cudaStream_t s) {
-  if constexpr (sizeof(E) == 2)
-    return backward ? launch_backward<E, GATED, gated_tile(1, true), 16, 2, 2>(a, s)
-                    : launch_forward<E, GATED, gated_tile(1, false), 16, GATED ? 1 : 2, 2>(a, s);
-  else
-    return backward ? launch_backward<E, GATED, gated_tile(0, true), 8, 1, GATED ? 1 : 2>(a, s)
-                    : launch_forward<E, GATED, gated_tile(0, false), 16, 1, 3>(a, s);
+  if constexpr (sizeof(E) == 2) {
+    if (backward) return launch_backward<E, GATED, 64, 16, 2, 2>(a, s);
+    return gated_tile(1, false, a.T) == 64 ? launch_forward<E, GATED, 64, 16, 1, 4>(a, s)
+                                           : launch_forward<E, GATED, 128, 16, GATED ? 1 : 2, 2>(a, s);
+  } else {
+    return backward ? launch_backward<E, GATED, 64, GATED ? 8 : 16, 1, GATED ? 1 : 2>(a, s)
+                    : launch_forward<E, GATED, 64, 16, 1, GATED ? 2 : 3>(a, s);
+  }
 }
 
 cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cudaStream_t s) {
   if (dtype == 0) return a.gated ? launch_scan_t<float, true>(backward, a, s) : launch_scan_t<float, false>(backward, a, s);
   return a.gated ? launch_scan_t<__nv_bfloat16, true>(backward, a, s) : launch_scan_t<__nv_bfloat16, false>(backward, a, s);
+}
+
+template <class E, bool GATED>
+cudaError_t launch_short_t(bool backward, const GatedShortArgs& a, cudaStream_t s) {
+  const unsigned grid = (unsigned)(((long long)a.B * (a.D / 2) + kGatedShortThreads - 1) / kGatedShortThreads);
+  if (backward) gated_short_backward_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
+  else gated_short_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gated_short(int dtype, bool backward, const GatedShortArgs& a, cudaStream_t s) {
+  if (dtype == 0) return a.i ? launch_short_t<float, true>(backward, a, s) : launch_short_t<float, false>(backward, a, s);
+  return a.i ? launch_short_t<__nv_bfloat16, true>(backward, a, s) : launch_short_t<__nv_bfloat16, false>(backward, a, s);
 }
 
 template <class E, bool GATED>
