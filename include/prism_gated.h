@@ -21,6 +21,7 @@
  * is scratch for one call: two calls that may run at the same time take one each.
  *
  *   D   channels of a token: a multiple of 8 (layer norm: up to 16384)
+ *   T   up to 2^30 tokens, B * T below 2^31
  *   seq_lens [B] int32 or NULL: tokens t >= seq_lens[b] are padding, as in prism.h: their
  *   outputs and gradients are 0 and their values, NaN included, reach nothing.  Lengths
  *   are clamped to 0..T.
@@ -83,7 +84,7 @@ typedef struct {
  * Gates and states are fp32; out is rounded once.  A gate below 2^-126 counts as 0.  Tiles of a
  * sequence wait for the state of the tiles before them; the result does not depend on their
  * timing (two calls agree bit for bit).  The workspace has prism_gated_scan_workspace_bytes (0 for short
- * sequences, where no tile waits: it may then be NULL). */
+ * sequences, where no tile looks back: it may then be NULL). */
 PRISM_API size_t prism_gated_scan_workspace_bytes(const prism_gated_dims* dims);
 PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, const void* x, const void* forget,
                                        const void* input_gate, const float* initial_state, void* out,

@@ -14,13 +14,42 @@ struct LayerNormArgs;
 
 constexpr int kGatedChunk = 64;          // tokens from one row of states to the next
 constexpr int kGatedCols = 64;           // channels of a tile: two a lane
-constexpr int kGatedShort = 32;          // sequences up to here go token by token
-// Tokens of a tile, whole chunks.  Tiles twice as long halve the states that tiles hand on; an SM's
-// shared memory bounds them, and a sequence's length where it is shorter.
-constexpr int gated_tile(int dtype, bool backward, int T) { return dtype && !backward && T > 64 ? 128 : 64; }
+// Short sequences go token by token, a thread two channels: up to 8 tokens always (2 x 2 x 240 bf16: 1.8 us,
+// 3.0 in tiles), up to 32 where there are threads enough (36 x 15 x 1256 bf16: 4.0 us, 8.4 in tiles; but
+// 2 x 23 x 48 fp32 gradient: 8.6 us, 4.4 in tiles).
+constexpr int kGatedShort = 32;
+constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGatedShort && (long long)B * D >= 1 << 15); }
+
+// How a call's chains of tiles go (times: GB300, bf16 unless said otherwise).
+//  tile     tokens of a tile, whole chunks.  An SM's shared memory and registers hold half as many tiles of twice the
+//           length, which halves what a chain hands on but leaves less beside each other.  With an input gate 64 where
+//           there are chains for all CTAs (64 x 512 x 2048: 94 us, in tiles of 128 101), 128 where few chains are
+//           long (1 x 65536 x 256: 51 us, of 64 80); without one 128 (8 x 4096 x 2048: 74 us, of 64 82), and 256
+//           where half of the SMs have no chain of their own (1 x 65536 x 4096: 293 us, of 128 318).
+//  cluster  the tiles of a chain are one cluster and need no workspace: chains of up to 8 tiles where all tiles
+//           run at once (4 x 1000 x 256: 8.7 us, 11.2 by looking back), or nearly so for two tiles a chain (512 x 200 x
+//           64: 16.9 us and 18.1).  Where clusters take chain after chain they wait for the slowest of their CTAs
+//           each time (64 x 512 x 2048: 217 us and 101).
+struct GatedPlan {
+  int tile;
+  bool cluster;
+};
+inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, int D) {
+  const long long chains = (long long)B * ((D + kGatedCols - 1) / kGatedCols);
+  const auto fits = [&](int tile, int ctas) {      // by cluster, `ctas` on an SM
+    const long long n = ((long long)T + tile - 1) / tile;
+    return n == 1 || (n <= 8 && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
+  };
+  if (backward) return {64, fits(64, dtype ? 2 : 1)};
+  if (dtype == 0) return {64, fits(64, 2)};
+  if (T <= 64) return {64, true};
+  if (fits(128, 2)) return {128, true};
+  if (gated) return {chains >= 256 ? 64 : 128, false};
+  return {chains <= 76 ? 256 : 128, false};
+}
 constexpr int kLayerNormMaxD = 16384;
 
-cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cudaStream_t s);
+cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, GatedPlan plan, cudaStream_t s);
 cudaError_t launch_gated_short(int dtype, bool backward, const GatedShortArgs& a, cudaStream_t s);
 cudaError_t launch_gated_decode(int dtype, const GatedDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm(int dtype, const LayerNormArgs& a, cudaStream_t s);

@@ -24,7 +24,7 @@ constexpr long long kMost = (1LL << 31) - 1;
 int check_tokens(int B, int T, int D, prism_dtype t) {
   if (t != PRISM_F32 && t != PRISM_BF16) return PRISM_ERR_INVALID_ARG;
   if (B <= 0 || T <= 0 || D <= 0) return PRISM_ERR_INVALID_ARG;
-  if (D % 8 || (long long)B * T > kMost) return PRISM_ERR_UNSUPPORTED;
+  if (D % 8 || T > 1 << 30 || (long long)B * T > kMost) return PRISM_ERR_UNSUPPORTED;     // token numbers are 32-bit
   return PRISM_OK;
 }
 
@@ -58,10 +58,11 @@ int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight
 
 int strips_of(const prism_gated_dims* d) { return (d->D + prism::kGatedCols - 1) / prism::kGatedCols; }
 int chunks_of(const prism_gated_dims* d) { return (d->T + prism::kGatedChunk - 1) / prism::kGatedChunk; }
-int tile_of(const prism_gated_dims* d, bool backward) { return prism::gated_tile(d->dtype == PRISM_F32 ? 0 : 1, backward, d->T); }
-long long tiles_of(const prism_gated_dims* d, bool backward) {
-  const int t = tile_of(d, backward);
-  return (long long)d->B * strips_of(d) * (((long long)d->T + t - 1) / t);
+prism::GatedPlan plan_of(const prism_gated_dims* d, bool backward, bool gated) {
+  return prism::gated_plan(d->dtype == PRISM_F32 ? 0 : 1, backward, gated, d->B, d->T, d->D);
+}
+long long tiles_of(const prism_gated_dims* d, int tile) {
+  return (long long)d->B * strips_of(d) * (((long long)d->T + tile - 1) / tile);
 }
 
 int check_gated(const prism_gated_dims* d, unsigned flags) {
@@ -69,14 +70,20 @@ int check_gated(const prism_gated_dims* d, unsigned flags) {
   if (d->flags & ~flags) return PRISM_ERR_INVALID_ARG;
   const int rc = check_tokens(d->B, d->T, d->D, d->dtype);
   if (rc != PRISM_OK) return rc;
-  if ((long long)d->B * strips_of(d) > kMost || tiles_of(d, true) > kMost / 2) return PRISM_ERR_UNSUPPORTED;
+  if ((long long)d->B * strips_of(d) > kMost || tiles_of(d, prism::kGatedChunk) > kMost) return PRISM_ERR_UNSUPPORTED;
   return PRISM_OK;
 }
 
-// The counter, then 16 bytes of (P, L) and 8 of h a lane and tile; nothing where no tile waits.
+// The counter, then 16 bytes of (P, L) and 8 of h a lane and tile; nothing where no tile looks back.
 constexpr size_t kCounter = 256;
+size_t gated_bytes(const prism_gated_dims* d, prism::GatedPlan plan) {
+  if (plan.cluster || prism::gated_is_short(d->B, d->T, d->D)) return 0;
+  return kCounter + (size_t)tiles_of(d, plan.tile) * 32 * 24;
+}
+// with or without an input gate
 size_t gated_bytes(const prism_gated_dims* d, bool backward) {
-  return d->T <= tile_of(d, backward) ? 0 : kCounter + (size_t)tiles_of(d, backward) * 32 * 24;
+  const size_t a = gated_bytes(d, plan_of(d, backward, true)), b = gated_bytes(d, plan_of(d, backward, false));
+  return a > b ? a : b;
 }
 
 // The device's word of waits that gave up.
@@ -136,36 +143,37 @@ int run_gated(const prism_gated_dims* d, bool backward, const GatedCall& c, void
     const int rc = resolve(c.given[i], d->B, d->T, d->D, d->dtype, step[i]);
     if (rc != PRISM_OK) return rc;
   }
-  const size_t need = gated_bytes(d, backward);
+  const bool gated = c.in[backward ? 3 : 2] != nullptr;
+  const prism::GatedPlan plan = plan_of(d, backward, gated);
+  const size_t need = gated_bytes(d, plan);
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
   if (need && (!workspace || workspace_bytes < need)) return PRISM_ERR_WORKSPACE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d->T <= prism::kGatedShort) return run_short(d, backward, c, step, s);
+  if (prism::gated_is_short(d->B, d->T, d->D)) return run_short(d, backward, c, step, s);
   prism::GatedArgs a = prism::GatedArgs();
   a.s_in = c.s_in; a.s_out = c.s_out; a.states = c.states;
   a.lens = c.lens;
   a.B = d->B; a.T = d->T; a.D = d->D;
   a.NC = chunks_of(d);
   a.strips = strips_of(d);
-  a.gated = c.in[backward ? 3 : 2] != nullptr;
+  a.gated = gated;
   a.check = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
-  const int tile = tile_of(d, backward);
   for (int i = 0; i < c.inputs; ++i)
-    if (!make_map(&a.map[i], c.in[i], step[i], d, tile)) return PRISM_ERR_CUDA;
+    if (!make_map(&a.map[i], c.in[i], step[i], d, plan.tile)) return PRISM_ERR_CUDA;
   const long long whole[2] = {(long long)d->T * d->D, d->D};
   for (int i = 0; i < c.outputs; ++i)
-    if (!make_map(&a.to[i], c.out[i], whole, d, tile)) return PRISM_ERR_CUDA;
+    if (!make_map(&a.to[i], c.out[i], whole, d, plan.tile)) return PRISM_ERR_CUDA;
   const int rc = find_status(&a.status);
   if (rc != PRISM_OK) return rc;
   if (need) {
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<unsigned*>(w);
     a.agg = reinterpret_cast<ulonglong2*>(w + kCounter);
-    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d, backward) * 32 * 16);
+    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d, plan.tile) * 32 * 16);
     if (cudaMemsetAsync(workspace, 0xff, need, s) != cudaSuccess) return PRISM_ERR_CUDA;
   }
-  return prism::launch_gated_scan(d->dtype == PRISM_F32 ? 0 : 1, backward, a, s) == cudaSuccess ? PRISM_OK
-                                                                                               : PRISM_ERR_LAUNCH;
+  return prism::launch_gated_scan(d->dtype == PRISM_F32 ? 0 : 1, backward, a, plan, s) == cudaSuccess ? PRISM_OK
+                                                                                                     : PRISM_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -39,7 +39,7 @@ struct GatedArgs {
   float* states;                                   // [B][NC][D]: written forwards (or null), read backwards
   const int* lens;
   int B, T, D, NC, strips, gated;                  // NC: rows of states a sequence; gated: there is an input gate
-  int tiles;                                       // of a sequence and strip
+  int tiles, deep;                                 // of a sequence and strip; deep: many of a chain run at once
   unsigned* ticket;                                // workspace: counter, then agg and incl
   ulonglong2* agg;                                 // [B][tiles][strips][32]: (P, L) of two channels
   uint2* incl;                                     // [B][tiles][strips][32]: h of two channels
@@ -176,10 +176,8 @@ template <int TT>
 struct GatedTile {
   int b, strip, rank, first, live, len;            // first token; live: tokens of the tile that are there
   bool last;                                       // the chain ends here
-  __device__ __forceinline__ GatedTile(const GatedArgs& p, unsigned n, bool backward) {
-    const unsigned lanes = (unsigned)(p.B * p.strips);
-    rank = (int)(n / lanes);
-    n -= (unsigned)rank * lanes;
+  // tile `rank_of` of the chain of sequence and strip n
+  __device__ __forceinline__ GatedTile(const GatedArgs& p, unsigned n, int rank_of, bool backward) : rank(rank_of) {
     b = (int)(n / (unsigned)p.strips);
     strip = (int)(n - (unsigned)b * (unsigned)p.strips);
     len = p.lens ? min(max(__ldg(p.lens + b), 0), p.T) : p.T;
@@ -191,14 +189,14 @@ struct GatedTile {
 };
 
 // The look back of a tile of rank >= 1.  `at` is the lane's slot at rank 0 and `step` the slots from one rank
-// to the next (a lane: two channels).  A look takes an L2 access' time, so kLooks tiles are looked at together.
-constexpr int kLooks = 4;
+// to the next (a lane: two channels).  A look takes an L2 access' time, so K tiles are looked at together.
+template <int K>
 struct GatedLook {
-  uint2 u[kLooks];
-  ulonglong2 g[kLooks];
+  uint2 u[K];
+  ulonglong2 g[K];
   __device__ __forceinline__ GatedLook(const GatedArgs& p, long long at, int step, int rank) {
 #pragma unroll
-    for (int k = 0; k < kLooks; ++k) {
+    for (int k = 0; k < K; ++k) {
       const long long s = at + (long long)max(rank - k, 0) * step;
       u[k] = peek(p.incl + s);
       g[k] = peek(p.agg + s);
@@ -217,29 +215,30 @@ __device__ __forceinline__ uint64_t step_over(ulonglong2 g, uint64_t h) {
               pack2(__uint_as_float((unsigned)(g.x >> 32)), __uint_as_float((unsigned)(g.y >> 32))));
 }
 
+// PRISM_FLAG_CHECK_WAIT_TIMEOUT (one warp): a wait for a word that nobody writes yet, this tile's own state.
+__device__ __forceinline__ void look_in_vain(const GatedArgs& p, const uint2* own) {
+  const unsigned long long begin = wall_ns();
+  while (!__any_sync(0xffffffffu, peek(own).x != kAbsent || wall_ns() - begin > kCheckNs)) {}
+  if ((threadIdx.x & 31) == 0) atomicOr(p.status, 1);
+}
+
 // One warp walks back over the nearest kNear tiles until it comes to one that knows its state (true), or all
 // of them have only their own run (false: a long chain that every tile waits for; look_far takes longer steps).
-constexpr int kNear = 8;
+// (Two a look: 8 x 4096 x 2048 bf16 98 us; one 100, four 100, eight 102, whose words L2 has to carry for every poll.)
+constexpr int kNear = 8, kLooksNear = 2;
 __device__ __forceinline__ bool look_near(const GatedArgs& p, long long at, int step, int rank, ulonglong2 (*held)[32],
                                           uint64_t& h) {
   const int lane = threadIdx.x & 31;
   const unsigned all = 0xffffffffu;
   const unsigned long long begin = wall_ns();
-  if (p.check) {                                   // a word that nobody writes yet: this tile's own state
-    while (true) {
-      const uint2 u = peek(p.incl + at + (long long)rank * step);
-      if (__any_sync(all, u.x != kAbsent || wall_ns() - begin > kCheckNs)) break;
-    }
-    if (lane == 0) atomicOr(p.status, 1);
-  }
   int n = 0;
   h = both(0.f);
   for (bool found = false; !found;) {
     const int before = n;
-    const GatedLook look(p, at, step, rank - 1 - n);
+    const GatedLook<kLooksNear> look(p, at, step, rank - 1 - n);
     bool going = true;
 #pragma unroll
-    for (int k = 0; k < kLooks; ++k) {
+    for (int k = 0; k < kLooksNear; ++k) {
       if (!going) continue;
       if (look.knows(k)) {
         h = look.state(k);
@@ -262,6 +261,7 @@ __device__ __forceinline__ bool look_near(const GatedArgs& p, long long at, int 
   return true;
 }
 
+constexpr int kLooks = 4;
 // All NW warps look, kLooks tiles each, in turns with a barrier; warp 0 gets the state.
 template <int NW>
 struct GatedFar {
@@ -280,20 +280,22 @@ __device__ __forceinline__ uint64_t look_far(const GatedArgs& p, long long at, i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned long long begin = wall_ns();
   for (int turn = 0;; turn ^= 1) {
-    const int first = warp * kLooks;
-    const GatedLook look(p, at, step, rank - 1 - first);
     unsigned has = 0, knows = 0;
+    if (warp < NW) {
+      const int first = warp * kLooks;
+      const GatedLook<kLooks> look(p, at, step, rank - 1 - first);
 #pragma unroll
-    for (int k = 0; k < kLooks; ++k) {
-      const int r = rank - 1 - first - k;
-      const bool a = look.knows(k), b = look.has(k);
-      if (r >= 0 && a) knows |= 1u << k;
-      if (r > 0 && b && !a) has |= 1u << k;
-      far.held[first + k][lane] = a ? make_ulonglong2(look.state(k), 0) : look.g[k];
-    }
-    if (lane == 0) {
-      reinterpret_cast<unsigned char*>(far.has[turn])[warp] = has;
-      reinterpret_cast<unsigned char*>(far.knows[turn])[warp] = knows;
+      for (int k = 0; k < kLooks; ++k) {
+        const int r = rank - 1 - first - k;
+        const bool a = look.knows(k), b = look.has(k);
+        if (r >= 0 && a) knows |= 1u << k;
+        if (r > 0 && b && !a) has |= 1u << k;
+        far.held[first + k][lane] = a ? make_ulonglong2(look.state(k), 0) : look.g[k];
+      }
+      if (lane == 0) {
+        reinterpret_cast<unsigned char*>(far.has[turn])[warp] = has;
+        reinterpret_cast<unsigned char*>(far.knows[turn])[warp] = knows;
+      }
     }
     if (threadIdx.x == 0) far.late[turn] = wall_ns() - begin > kWaitNs;
     __syncthreads();
@@ -337,14 +339,20 @@ struct GatedJob {
 // after tile.  Copies are TMA's, a box of 64 channels by TT tokens each: the next tiles' come in while
 // it works (a stage is free again once its values are in registers), and a tile's outputs
 // leave while it works on the next one.
-template <class E, int NI, int NO, int TT, int R, int S>
+// With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles): they hand each other (P, L)
+// through shared memory, with one barrier of the cluster, and need neither tickets nor workspace.
+constexpr int kGatedCluster = 8;
+template <class E, int NI, int NO, int TT, int R, int S, bool CL>
 struct GatedShared {
   static constexpr int NW = TT / R;
   static constexpr bool BACK = NI > 2 && NO > 1;
   alignas(128) E tile[S][NI][TT][kGatedCols];
   alignas(128) E out[NO][TT][kGatedCols];
   ulonglong2 part[2][NW][32];                      // (P, L) of a warp's tokens, then of those before them: both channels of P, of L
-  GatedFar<NW> far;
+  union {
+    GatedFar<(NW < 8 ? NW : 8)> far;
+    ulonglong2 ahead[CL ? 2 : 1][kGatedCluster][32];       // CL: (P, L) of the chain's tiles, by rank
+  };
   int found;                                       // the state came by look_near
   uint64_t carry[32];                              // what reaches the tile
   // gradient: r that a warp's tokens send backwards, (P, r) of what is behind them, the state before them
@@ -355,11 +363,12 @@ struct GatedShared {
 };
 
 // Tickets and copies of a CTA, which one thread makes.
-template <class E, int NI, int NO, int TT, int R, int S>
+template <class E, int NI, int NO, int TT, int R, int S, bool CL>
 struct GatedFeed {
-  GatedShared<E, NI, NO, TT, R, S>& sm;
+  GatedShared<E, NI, NO, TT, R, S, CL>& sm;
   const GatedArgs& p;
   unsigned next;
+  bool lost;                                       // a copy never came: no more of them
   __device__ __forceinline__ void init() {
 #pragma unroll
     for (int s = 0; s < S; ++s) tc::bar_init(&sm.full[s], 1);
@@ -367,20 +376,21 @@ struct GatedFeed {
     draw(0);
     for (int it = 0; it < S; ++it) load(it);
   }
-  // the tile that follows; without chains nobody waits and tiles are dealt out in turn
+  // the tile that follows
   __device__ __forceinline__ void draw(int it) {
-    next = p.tiles == 1 ? blockIdx.x + (unsigned)it * gridDim.x : atomicAdd(p.ticket, 1u) + 1u;
+    next = CL ? blockIdx.x / p.tiles + (unsigned)it * (gridDim.x / p.tiles) : atomicAdd(p.ticket, 1u) + 1u;
   }
   __device__ __forceinline__ void load(int it) {
-    const unsigned n = next, total = (unsigned)((long long)p.B * p.strips * p.tiles);
+    const unsigned chains = (unsigned)p.B * p.strips, total = CL ? chains : chains * p.tiles;
     GatedJob& j = sm.job[it % (2 * S)];
-    if (n >= total) {                              // the others see it and stop
+    if (next >= total) {                           // the others see it and stop
       j.more = 0;
       return;
     }
-    const GatedTile<TT> tl(p, n, NO > 1);
+    const unsigned rank = CL ? blockIdx.x % p.tiles : next / chains;
+    const GatedTile<TT> tl(p, CL ? next : next - rank * chains, rank, NO > 1);
     j = GatedJob{tl.first, tl.live, tl.rank, tl.last, tl.b, tl.strip, 1, 0};
-    if (tl.live > 0) {
+    if (tl.live > 0 && !lost) {
       const int s = it % S;
       tc::bar_expect_tx(&sm.full[s], sizeof(sm.tile[s]));
 #pragma unroll
@@ -395,6 +405,24 @@ struct GatedFeed {
     tc::bulk_commit();
   }
 };
+
+// All of the chain's CTAs; alone, the CTA's own.
+__device__ __forceinline__ void chain_barrier(const GatedArgs& p) {
+  if (p.tiles == 1) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  }
+}
+// v to the same place in the shared memory of the chain's tiles behind this one (a lane 16 bytes)
+__device__ __forceinline__ void hand_on(const GatedArgs& p, int rank, ulonglong2* at, ulonglong2 v) {
+  for (int r = rank + 1; r < p.tiles; ++r) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(there) : "r"(tc::smem_addr(at)), "r"(r));
+    asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};\n" ::"r"(there), "l"(v.x), "l"(v.y) : "memory");
+  }
+}
 
 // The way out of a wait that gave up: no copy in flight may outlive the CTA.
 template <int S>
@@ -413,26 +441,28 @@ __device__ __forceinline__ uint64_t load_pair(const float* p) {
 }
 
 // Forward.  Tiles of TT tokens, R a lane, TT/R warps, S stages, C CTAs an SM.
-template <class E, bool GATED, int TT, int R, int S, int C>
+template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
 __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(kGatedChunk % R == 0, "a row of states starts at a warp's tokens");
   constexpr int NW = TT / R, NI = GATED ? 3 : 2;
-  using Shared = GatedShared<E, NI, 1, TT, R, S>;
+  using Shared = GatedShared<E, NI, 1, TT, R, S, CL>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, NI, 1, TT, R, S> feed{sm, p, 0};
+  GatedFeed<E, NI, 1, TT, R, S, CL> feed{sm, p, 0, false};
   if (feeder) feed.init();
-  __syncthreads();
+  if (CL) chain_barrier(p);                        // its CTAs are there
+  else __syncthreads();
   unsigned phase = 0;                              // a bit a stage
+  bool lost = false;
   int it = 0;
   for (;; ++it) {
     const GatedJob job = sm.job[it % (2 * S)];
     if (!job.more) break;
     const int s = it % S, mine = warp * R;         // the warp's first token in the tile
     bool ok = true;
-    if (job.live > 0) {
+    if (job.live > 0 && !lost) {
       ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
       phase ^= 1u << s;
     }
@@ -472,7 +502,8 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
     tc::fence_smem_to_async();                     // the last tile's outputs
     if (__syncthreads_or(!ok)) {                   // a copy that never came
       gated_drain<S>(p, sm.full, phase);
-      break;
+      if (!CL) break;
+      feed.lost = lost = true;                     // the chain's others still meet at their barriers
     }
     if (feeder) {
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
@@ -482,15 +513,11 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
     const bool on = ch < p.D;
     const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
     const long long row = (long long)job.b * p.D + ch;
-    auto arrive = [&](uint64_t h) {                // the state before the tile is known
-      const uint64_t end = fma2(P, h, L);
-      if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
-      else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
-      sm.carry[lane] = h;
-    };
-    if (warp == 0) {
-      bool found = true;
-      if (job.live > 0) {
+    uint64_t entry;                                // the state before the tile
+    if constexpr (CL) {
+      uint64_t h = both(0.f);
+      if (p.s_in && on) h = load_pair(p.s_in + row);
+      if (warp == 0) {
         P = both(1.f);
         L = both(0.f);
 #pragma unroll
@@ -500,30 +527,65 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
           L = fma2(g.x, L, g.y);
           P = mul2(g.x, P);
         }
-        uint64_t h = both(0.f);
-        if (job.rank > 0) {
-          if (!job.last) publish(p.agg + at + (long long)job.rank * step, P, L);
-          found = look_near(p, at, step, job.rank, sm.far.held, h);
-        } else if (p.s_in && on) {
-          h = load_pair(p.s_in + row);
-        }
-        if (found) arrive(h);
-      } else {
-        if (job.rank == 0 && p.s_out && on)        // a sequence without tokens
-          Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : both(0.f));
-        sm.carry[lane] = both(0.f);
+        hand_on(p, job.rank, &sm.ahead[it & 1][job.rank][lane], make_ulonglong2(P, L));
       }
-      if (lane == 0) sm.found = found;
-    }
-    if (feeder && it > 0) tc::bulk_wait_read();    // the output tile may be written again
-    __syncthreads();
-    if (!sm.found) {
-      const uint64_t h = look_far<NW>(p, at, step, job.rank, sm.far);
-      if (warp == 0) arrive(h);
+      if (feeder && it > 0) tc::bulk_wait_read();  // the output tile may be written again
+      chain_barrier(p);
+      for (int r = 0; r < job.rank; ++r) {
+        const ulonglong2 g = sm.ahead[it & 1][r][lane];
+        h = fma2(g.x, h, g.y);
+      }
+      if (warp == 0 && p.s_out && on) {
+        if (job.last) Two<float>::store(p.s_out + row, fma2(P, h, L));
+        else if (job.rank == 0 && job.live == 0) Two<float>::store(p.s_out + row, h);      // a sequence without tokens
+      }
+      entry = h;
+    } else {
+      auto arrive = [&](uint64_t h) {                // the state before the tile is known
+        const uint64_t end = fma2(P, h, L);
+        if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
+        else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+        sm.carry[lane] = h;
+      };
+      if (warp == 0) {
+        bool found = true;
+        if (job.live > 0) {
+          P = both(1.f);
+          L = both(0.f);
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const ulonglong2 g = part[w][lane];
+            part[w][lane] = make_ulonglong2(P, L);
+            L = fma2(g.x, L, g.y);
+            P = mul2(g.x, P);
+          }
+          uint64_t h = both(0.f);
+          if (job.rank > 0) {
+            if (!job.last) publish(p.agg + at + (long long)job.rank * step, P, L);
+            if (p.check) look_in_vain(p, p.incl + at + (long long)job.rank * step);
+            found = !p.deep && look_near(p, at, step, job.rank, sm.far.held, h);
+          } else if (p.s_in && on) {
+            h = load_pair(p.s_in + row);
+          }
+          if (found) arrive(h);
+        } else {
+          if (job.rank == 0 && p.s_out && on)        // a sequence without tokens
+            Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : both(0.f));
+          sm.carry[lane] = both(0.f);
+        }
+        if (lane == 0) sm.found = found;
+      }
+      if (feeder && it > 0) tc::bulk_wait_read();    // the output tile may be written again
       __syncthreads();
+      if (!sm.found) {
+        const uint64_t h = look_far<(NW < 8 ? NW : 8)>(p, at, step, job.rank, sm.far);
+        if (warp == 0) arrive(h);
+        __syncthreads();
+      }
+      entry = sm.carry[lane];
     }
     const ulonglong2 g = part[warp][lane];
-    uint64_t h = fma2(g.x, sm.carry[lane], g.y);
+    uint64_t h = fma2(g.x, entry, g.y);
     if (p.states && on && mine % kGatedChunk == 0 && mine < job.live)
       Two<float>::store(p.states + ((long long)job.b * p.NC + (job.first + mine) / kGatedChunk) * p.D + ch, h);
     if (mine + R <= job.live) {
@@ -551,20 +613,22 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
 
 // Gradient.  The tile's states come from the row of `states` before it, what reaches it from
 // behind from the tiles after it.
-template <class E, bool GATED, int TT, int R, int S, int C>
+template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
 __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(TT % kGatedChunk == 0, "a tile starts at a row of states");
   constexpr int NW = TT / R, NI = GATED ? 4 : 3, NO = GATED ? 3 : 2;
-  using Shared = GatedShared<E, NI, NO, TT, R, S>;
+  using Shared = GatedShared<E, NI, NO, TT, R, S, CL>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, NI, NO, TT, R, S> feed{sm, p, 0};
+  GatedFeed<E, NI, NO, TT, R, S, CL> feed{sm, p, 0, false};
   if (feeder) feed.init();
-  __syncthreads();
+  if (CL) chain_barrier(p);                        // its CTAs are there
+  else __syncthreads();
   const uint64_t none = both(0.f), one = both(1.f), minus = both(-1.f);
   unsigned phase = 0;
+  bool lost = false;
   int it = 0;
   for (;; ++it) {
     const GatedJob job = sm.job[it % (2 * S)];
@@ -575,7 +639,7 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     if (warp == 1 && on && job.live > 0)
       h0 = load_pair(p.states + ((long long)job.b * p.NC + job.first / kGatedChunk) * p.D + ch);
     bool ok = true;
-    if (job.live > 0) {
+    if (job.live > 0 && !lost) {
       ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
       phase ^= 1u << s;
     }
@@ -629,7 +693,8 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     tc::fence_smem_to_async();
     if (__syncthreads_or(!ok)) {
       gated_drain<S>(p, sm.full, phase);
-      break;
+      if (!CL) break;
+      feed.lost = lost = true;
     }
     if (feeder) {
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
@@ -638,39 +703,6 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     const int step = p.strips * 32;
     const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
     const long long row = (long long)job.b * p.D + ch;
-    auto arrive = [&](uint64_t g) {                // what comes from behind the tile is known
-      const uint64_t end = fma2(P, g, L);
-      if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
-      else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
-      sm.carry[lane] = g;
-    };
-    if (warp == 0) {
-      bool found = true;
-      if (job.live > 0) {
-        P = one;
-        L = none;
-#pragma unroll
-        for (int k = NW - 1; k >= 0; --k) {
-          const uint64_t q = part[k][lane].x;
-          sm.behind[k][lane] = make_ulonglong2(P, L);
-          L = fma2(q, L, back[k][lane]);
-          P = mul2(q, P);
-        }
-        uint64_t g = none;
-        if (job.rank > 0) {
-          if (!job.last) publish(p.agg + at + (long long)job.rank * step, P, L);
-          found = look_near(p, at, step, job.rank, sm.far.held, g);
-        } else if (p.s_in && on) {
-          g = load_pair(p.s_in + row);
-        }
-        if (found) arrive(g);
-      } else {
-        if (job.rank == 0 && p.s_out && on)
-          Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : none);
-        sm.carry[lane] = none;
-      }
-      if (lane == 0) sm.found = found;
-    }
     if (warp == 1) {
       uint64_t h = h0;
 #pragma unroll
@@ -680,12 +712,76 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
         h = fma2(g.x, h, g.y);
       }
     }
-    if (feeder && it > 0) tc::bulk_wait_read();
-    __syncthreads();
-    if (!sm.found) {
-      const uint64_t g = look_far<NW>(p, at, step, job.rank, sm.far);
-      if (warp == 0) arrive(g);
+    uint64_t entry;                                // what comes from behind the tile
+    if constexpr (CL) {
+      uint64_t g = none;
+      if (p.s_in && on) g = load_pair(p.s_in + row);
+      if (warp == 0) {
+        P = one;
+        L = none;
+#pragma unroll
+        for (int k = NW - 1; k >= 0; --k) {
+          const uint64_t q = part[k][lane].x;
+          sm.behind[k][lane] = make_ulonglong2(P, L);
+          L = fma2(q, L, back[k][lane]);
+          P = mul2(q, P);
+        }
+        hand_on(p, job.rank, &sm.ahead[it & 1][job.rank][lane], make_ulonglong2(P, L));
+      }
+      if (feeder && it > 0) tc::bulk_wait_read();
+      chain_barrier(p);
+      for (int k = 0; k < job.rank; ++k) {
+        const ulonglong2 q = sm.ahead[it & 1][k][lane];
+        g = fma2(q.x, g, q.y);
+      }
+      if (warp == 0 && p.s_out && on) {
+        if (job.last) Two<float>::store(p.s_out + row, fma2(P, g, L));
+        else if (job.rank == 0 && job.live == 0) Two<float>::store(p.s_out + row, g);
+      }
+      entry = g;
+    } else {
+      auto arrive = [&](uint64_t g) {                // what comes from behind the tile is known
+        const uint64_t end = fma2(P, g, L);
+        if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
+        else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
+        sm.carry[lane] = g;
+      };
+      if (warp == 0) {
+        bool found = true;
+        if (job.live > 0) {
+          P = one;
+          L = none;
+#pragma unroll
+          for (int k = NW - 1; k >= 0; --k) {
+            const uint64_t q = part[k][lane].x;
+            sm.behind[k][lane] = make_ulonglong2(P, L);
+            L = fma2(q, L, back[k][lane]);
+            P = mul2(q, P);
+          }
+          uint64_t g = none;
+          if (job.rank > 0) {
+            if (!job.last) publish(p.agg + at + (long long)job.rank * step, P, L);
+            if (p.check) look_in_vain(p, p.incl + at + (long long)job.rank * step);
+            found = !p.deep && look_near(p, at, step, job.rank, sm.far.held, g);
+          } else if (p.s_in && on) {
+            g = load_pair(p.s_in + row);
+          }
+          if (found) arrive(g);
+        } else {
+          if (job.rank == 0 && p.s_out && on)
+            Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : none);
+          sm.carry[lane] = none;
+        }
+        if (lane == 0) sm.found = found;
+      }
+      if (feeder && it > 0) tc::bulk_wait_read();
       __syncthreads();
+      if (!sm.found) {
+        const uint64_t g = look_far<(NW < 8 ? NW : 8)>(p, at, step, job.rank, sm.far);
+        if (warp == 0) arrive(g);
+        __syncthreads();
+      }
+      entry = sm.carry[lane];
     }
     uint64_t h = sm.start[warp][lane], hp[R];      // hp: h_{t-1}
 #pragma unroll
@@ -694,7 +790,7 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
       h = fma2(a[j], h, write(j));
     }
     const ulonglong2 q = sm.behind[warp][lane];
-    r = fma2(q.x, sm.carry[lane], q.y);
+    r = fma2(q.x, entry, q.y);
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
       const uint64_t xj = x[j].get(), G = add2(d[j].get(), r);
@@ -776,8 +872,9 @@ __global__ void __launch_bounds__(kGatedShortThreads) gated_short_kernel(GatedSh
   if (p.s_out) Two<float>::store(p.s_out + row, h);
 }
 
-// Gradient: forwards for the states before every token, which stay in registers, then backwards.
-template <class E, bool GATED>
+// Gradient of up to N tokens: forwards for the states before every token, which stay in registers, then
+// backwards.  Where all tokens' loads are in flight together (N = kGatedAhead) nothing is read twice.
+template <class E, bool GATED, int N>
 __global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kernel(GatedShortArgs p) {
   const GatedShortPlace at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
   if (at.b >= p.B) return;
@@ -788,18 +885,22 @@ __global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kerne
   const long long o = (long long)at.b * p.T * p.D + at.ch, row = (long long)at.b * p.D + at.ch;
   E *dx = static_cast<E*>(p.out) + o, *df = static_cast<E*>(p.df) + o, *di = GATED ? static_cast<E*>(p.di) + o : nullptr;
   const uint64_t none = both(0.f), minus = both(-1.f);
-  uint64_t h = at.len > 0 ? load_pair(p.states + row) : none, before[kGatedShort];
-#pragma unroll
-  for (int t0 = 0; t0 < kGatedShort; t0 += kGatedAhead) {
-    if (t0 >= at.len) break;
-    Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead];
+  Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead], rd[kGatedAhead];
+  auto load = [&](int t0, bool with_d) {
 #pragma unroll
     for (int j = 0; j < kGatedAhead; ++j)
       if (t0 + j < at.len) {
         rx[j].load(x + (t0 + j) * p.xs[1]);
         rf[j].load(f + (t0 + j) * p.fs[1]);
         if (GATED) ri[j].load(i + (t0 + j) * p.is[1]);
+        if (with_d) rd[j].load(d + (t0 + j) * p.ds[1]);
       }
+  };
+  uint64_t h = at.len > 0 ? load_pair(p.states + row) : none, before[N];
+#pragma unroll
+  for (int t0 = 0; t0 < N; t0 += kGatedAhead) {
+    if (t0 >= at.len) break;
+    load(t0, N == kGatedAhead);
 #pragma unroll
     for (int j = 0; j < kGatedAhead; ++j) {
       before[t0 + j] = h;
@@ -811,17 +912,9 @@ __global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kerne
   }
   uint64_t r = p.s_in ? load_pair(p.s_in + row) : none;
 #pragma unroll
-  for (int t0 = kGatedShort - kGatedAhead; t0 >= 0; t0 -= kGatedAhead) {
+  for (int t0 = N - kGatedAhead; t0 >= 0; t0 -= kGatedAhead) {
     if (t0 >= p.T) continue;
-    Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead], rd[kGatedAhead];
-#pragma unroll
-    for (int j = 0; j < kGatedAhead; ++j)
-      if (t0 + j < at.len) {
-        rx[j].load(x + (t0 + j) * p.xs[1]);
-        rf[j].load(f + (t0 + j) * p.fs[1]);
-        if (GATED) ri[j].load(i + (t0 + j) * p.is[1]);
-        rd[j].load(d + (t0 + j) * p.ds[1]);
-      }
+    if (N > kGatedAhead) load(t0, true);
 #pragma unroll
     for (int j = kGatedAhead - 1; j >= 0; --j) {
       if (t0 + j >= p.T) continue;

@@ -8,53 +8,91 @@ namespace prism {
 
 constexpr int kSMs = 152;
 
-template <class Shared, int TT, int R, int C, class F>
+// Persistent CTAs.  Chains by cluster: a cluster takes chain after chain; else a CTA takes tile after tile.
+template <class Shared, int TT, int R, int C, bool CL, class F>
 cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& done, cudaStream_t s) {
   static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
   const cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
   a.tiles = (a.T + TT - 1) / TT;
-  const long long tiles = (long long)a.B * a.strips * a.tiles, most = kSMs * C;
-  fn<<<(unsigned)(tiles < most ? tiles : most), 32 * TT / R, sizeof(Shared), s>>>(a);
-  return cudaGetLastError();
+  if (CL && a.tiles > kGatedCluster) return cudaErrorInvalidValue;
+  const long long chains = (long long)a.B * a.strips, most = kSMs * C / a.tiles > 0 ? kSMs * C / a.tiles : 1;
+  const long long tiles = chains * a.tiles, grid = CL ? (chains < most ? chains : most) * a.tiles : tiles < kSMs * C ? tiles : kSMs * C;
+  // Where 16 tiles of a chain run at once, look_near finds only runs (gradient, 1 x 55647 x 328: 91 us, 103 with
+  // it; 1 x 10807 x 2368, 8 tiles: 74 and 69).
+  a.deep = grid >= 16 * chains;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(32 * TT / R);
+  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.tiles;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CL && a.tiles > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-template <class E, bool GATED, int TT, int R, int S, int C>
+template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
 cudaError_t launch_forward(const GatedArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, TT, R, S>, TT, R, C>(gated_scan_kernel<E, GATED, TT, R, S, C>, a,
-                                                                               done, s);
+  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, TT, R, S, CL>, TT, R, C, CL>(
+      gated_scan_kernel<E, GATED, TT, R, S, C, CL>, a, done, s);
 }
-template <class E, bool GATED, int TT, int R, int S, int C>
+template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
 cudaError_t launch_backward(const GatedArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, TT, R, S>, TT, R, C>(
-      gated_scan_backward_kernel<E, GATED, TT, R, S, C>, a, done, s);
+  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, TT, R, S, CL>, TT, R, C, CL>(
+      gated_scan_backward_kernel<E, GATED, TT, R, S, C, CL>, a, done, s);
 }
 
 #ifndef GATED_BENCH
 // Stages and CTAs an SM are what its shared memory and registers hold.
 template <class E, bool GATED>
-cudaError_t launch_scan_t(bool backward, const GatedArgs& a, cudaStream_t s) {
+cudaError_t launch_scan_t(bool backward, const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   if constexpr (sizeof(E) == 2) {
-    if (backward) return launch_backward<E, GATED, 64, 16, 2, 2>(a, s);
-    return gated_tile(1, false, a.T) == 64 ? launch_forward<E, GATED, 64, 16, 1, 4>(a, s)
-                                           : launch_forward<E, GATED, 128, 16, GATED ? 1 : 2, 2>(a, s);
+    const int t = plan.tile;
+    if (backward) {
+      if (plan.cluster) return launch_backward<E, GATED, 64, 16, 2, 2, true>(a, s);
+      return launch_backward<E, GATED, 64, 16, 2, 2, false>(a, s);
+    }
+    if (plan.cluster) {
+      if (t == 64) return launch_forward<E, GATED, 64, 16, 1, 4, true>(a, s);
+      return launch_forward<E, GATED, 128, 16, GATED ? 1 : 2, 2, true>(a, s);
+    }
+    if constexpr (GATED) {
+      if (t == 64) return launch_forward<E, true, 64, 16, 1, 4, false>(a, s);
+      return launch_forward<E, true, 128, 16, 1, 2, false>(a, s);
+    } else {
+      if (t == 256) return launch_forward<E, false, 256, 16, 2, 1, false>(a, s);
+      return launch_forward<E, false, 128, 16, 2, 2, false>(a, s);
+    }
   } else {
-    return backward ? launch_backward<E, GATED, 64, GATED ? 8 : 16, 1, GATED ? 1 : 2>(a, s)
-                    : launch_forward<E, GATED, 64, 16, 1, GATED ? 2 : 3>(a, s);
+    if (backward) {
+      constexpr int R = GATED ? 8 : 16, C = GATED ? 1 : 2;
+      if (plan.cluster) return launch_backward<E, GATED, 64, R, 1, C, true>(a, s);
+      return launch_backward<E, GATED, 64, R, 1, C, false>(a, s);
+    }
+    constexpr int C = GATED ? 2 : 3;
+    if (plan.cluster) return launch_forward<E, GATED, 64, 16, 1, C, true>(a, s);
+    return launch_forward<E, GATED, 64, 16, 1, C, false>(a, s);
   }
 }
 
-cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, cudaStream_t s) {
-  if (dtype == 0) return a.gated ? launch_scan_t<float, true>(backward, a, s) : launch_scan_t<float, false>(backward, a, s);
-  return a.gated ? launch_scan_t<__nv_bfloat16, true>(backward, a, s) : launch_scan_t<__nv_bfloat16, false>(backward, a, s);
+cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
+  if (dtype == 0)
+    return a.gated ? launch_scan_t<float, true>(backward, a, plan, s) : launch_scan_t<float, false>(backward, a, plan, s);
+  return a.gated ? launch_scan_t<__nv_bfloat16, true>(backward, a, plan, s)
+                 : launch_scan_t<__nv_bfloat16, false>(backward, a, plan, s);
 }
 
 template <class E, bool GATED>
 cudaError_t launch_short_t(bool backward, const GatedShortArgs& a, cudaStream_t s) {
   const unsigned grid = (unsigned)(((long long)a.B * (a.D / 2) + kGatedShortThreads - 1) / kGatedShortThreads);
-  if (backward) gated_short_backward_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
+  if (backward && a.T <= kGatedAhead) gated_short_backward_kernel<E, GATED, kGatedAhead><<<grid, kGatedShortThreads, 0, s>>>(a);
+  else if (backward) gated_short_backward_kernel<E, GATED, kGatedShort><<<grid, kGatedShortThreads, 0, s>>>(a);
   else gated_short_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
   return cudaGetLastError();
 }

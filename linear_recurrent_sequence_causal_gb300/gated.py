@@ -76,6 +76,26 @@ def _out(t, side):
     return _new(t.shape, t.dtype, t.device, side)
 
 
+# Outputs and workspaces that are passed in are checked; what the call makes itself is as it has to be.
+
+def _result(name, t, like, dev, side):
+    """A contiguous output of ``like``'s shape and type, and its address."""
+    if t is not None:
+        return t, _whole(name, t, like.shape, like.dtype, dev)
+    t = _out(like, side)
+    return t, t.data_ptr()
+
+
+def _workspace(t, nbytes, device, dev, side):
+    """A workspace, its address and its bytes."""
+    if t is not None:
+        return (t, *_room(t, dev))
+    if not nbytes:
+        return None, None, 0
+    t = _scratch(nbytes, device, side)
+    return t, t.data_ptr(), nbytes
+
+
 # The checked dims of a call by shapes, strides and settings, as in ``linattn``.
 
 @functools.lru_cache(maxsize=256)
@@ -124,18 +144,16 @@ def prism_layer_norm(x, *, weight=None, bias=None, eps=1e-5, seq_lens=None, out=
     """Layer norm of every token of x [B,T,D]: (x - mean) / sqrt(var + eps) * weight + bias, ``weight``
     and ``bias`` [D] fp32 (None: ones, zeros).  Returns out [B,T,D], contiguous, in x's type,
     0 at padding tokens."""
-    xs, dt = x.shape, x.dtype
-    keep, dims, _ = _norm_dims(xs, x.stride(), dt, float(eps), None)
+    xs = x.shape
+    keep, dims, _ = _norm_dims(xs, x.stride(), x.dtype, float(eps), None)
     dev, raw, side = _stream(x, stream)
     if side is not None:
         _used(side, x, weight, bias, seq_lens, out)
-    if out is None:
-        out = _out(x, side)
     D = xs[2:]
-    _call(
-        dev, load().prism_layer_norm, dims, x.data_ptr(), _whole("weight", weight, D, torch.float32, dev),
-        _whole("bias", bias, D, torch.float32, dev), _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev),
-        _whole("out", out, xs, dt, dev), raw)
+    w, b = _whole("weight", weight, D, torch.float32, dev), _whole("bias", bias, D, torch.float32, dev)
+    lens = _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev)
+    out, to = _result("out", out, x, dev, side)
+    _call(dev, load().prism_layer_norm, dims, x.data_ptr(), w, b, lens, to, raw)
     return out
 
 
@@ -144,25 +162,28 @@ def prism_layer_norm_backward(x, d_out, *, weight=None, bias=None, eps=1e-5, seq
     """Gradients through prism_layer_norm given ``d_out`` [B,T,D] in x's type.  Returns a dict: x in its
     type, weight and bias fp32 (None where the norm had none).  ``grads`` may pass preallocated
     outputs with the same keys."""
-    xs, dt = x.shape, x.dtype
-    _like("d_out", d_out, xs, dt)
-    keep, dims, nbytes = _norm_dims(xs, x.stride(), dt, float(eps), d_out.stride())
+    xs = x.shape
+    _like("d_out", d_out, xs, x.dtype)
+    keep, dims, nbytes = _norm_dims(xs, x.stride(), x.dtype, float(eps), d_out.stride())
     dev, raw, side = _stream(x, stream)
     D = xs[2:]
     g = dict(grads) if grads else {}
     if side is not None:
         _used(side, x, d_out, weight, bias, seq_lens, workspace, *g.values())
+    w = _whole("weight", weight, D, torch.float32, dev)
     _whole("bias", bias, D, torch.float32, dev)
-    for n, t in (("x", x), ("weight", weight), ("bias", bias)):
-        if g.get(n) is None:
-            g[n] = None if t is None else _out(t, side)
-    if workspace is None and (g["weight"] is not None or g["bias"] is not None):
-        workspace = _scratch(nbytes, x.device, side)
-    _call(
-        dev, load().prism_layer_norm_backward, dims, x.data_ptr(), _whole("weight", weight, D, torch.float32, dev),
-        _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev), _strided("d_out", d_out, dev),
-        _whole("grads['x']", g["x"], xs, dt, dev), _whole("grads['weight']", g["weight"], D, torch.float32, dev),
-        _whole("grads['bias']", g["bias"], D, torch.float32, dev), *_room(workspace, dev), raw)
+    lens, dy = _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev), _strided("d_out", d_out, dev)
+    g["x"], dx = _result("grads['x']", g.get("x"), x, dev, side)
+    to = {}
+    for n, t in (("weight", weight), ("bias", bias)):
+        mine = g.get(n)
+        if mine is None and t is not None:
+            g[n], to[n] = _result(n, None, t, dev, side)
+        else:
+            g[n], to[n] = mine, _whole(f"grads['{n}']", mine, D, torch.float32, dev)
+    wanted = to["weight"] is not None or to["bias"] is not None
+    keep2, room, size = _workspace(workspace, nbytes if wanted else 0, x.device, dev, side)
+    _call(dev, load().prism_layer_norm_backward, dims, x.data_ptr(), w, lens, dy, dx, to["weight"], to["bias"], room, size, raw)
     return g
 
 
@@ -194,18 +215,17 @@ def prism_gated_scan_forward(x, forget, *, input_gate=None, initial_state=None, 
     ss = rows[::2]
     if side is not None:
         _used(side, x, forget, input_gate, initial_state, out, final_state, states, seq_lens, workspace)
-    if out is None:
-        out = _out(x, side)
+    f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
+    s0, st = _whole("initial_state", initial_state, ss, torch.float32, dev), _whole("states", states, rows, torch.float32, dev)
+    lens = _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev)
+    out, to = _result("out", out, x, dev, side)
     if final_state is None and want_state:
         final_state = _new(ss, torch.float32, x.device, side)
-    if workspace is None and nbytes:
-        workspace = _scratch(nbytes, x.device, side)
-    _call(
-        dev, load().prism_gated_scan_forward, dims, x.data_ptr(), _strided("forget", forget, dev),
-        None if input_gate is None else _strided("input_gate", input_gate, dev),
-        _whole("initial_state", initial_state, ss, torch.float32, dev), _whole("out", out, xs, dt, dev),
-        _whole("final_state", final_state, ss, torch.float32, dev), _whole("states", states, rows, torch.float32, dev),
-        _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev), *_room(workspace, dev), raw)
+        s1 = final_state.data_ptr()
+    else:
+        s1 = _whole("final_state", final_state, ss, torch.float32, dev)
+    keep2, room, size = _workspace(workspace, nbytes, x.device, dev, side)
+    _call(dev, load().prism_gated_scan_forward, dims, x.data_ptr(), f, i, s0, to, s1, st, lens, room, size, raw)
     return out, final_state
 
 
@@ -223,22 +243,22 @@ def prism_gated_scan_backward(x, forget, states, d_out, *, input_gate=None, d_fi
     g = dict(grads) if grads else {}
     if side is not None:
         _used(side, x, forget, input_gate, states, d_out, d_final_state, seq_lens, workspace, *g.values())
-    for n, t in (("x", x), ("forget", forget), ("input_gate", input_gate)):
-        if g.get(n) is None:
-            g[n] = None if t is None else _out(t, side)
-    if g.get("initial_state") is None:
-        g["initial_state"] = _new(ss, torch.float32, x.device, side) if want_initial_state else None
-    if workspace is None and nbytes:
-        workspace = _scratch(nbytes, x.device, side)
-    _call(
-        dev, load().prism_gated_scan_backward, dims, x.data_ptr(), _strided("forget", forget, dev),
-        None if input_gate is None else _strided("input_gate", input_gate, dev),
-        _whole("states", states, rows, torch.float32, dev), _strided("d_out", d_out, dev),
-        _whole("d_final_state", d_final_state, ss, torch.float32, dev), _whole("grads['x']", g["x"], xs, dt, dev),
-        _whole("grads['forget']", g["forget"], xs, dt, dev),
-        _whole("grads['input_gate']", g["input_gate"], xs, dt, dev),
-        _whole("grads['initial_state']", g["initial_state"], ss, torch.float32, dev),
-        _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev), *_room(workspace, dev), raw)
+    f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
+    st, dy = _whole("states", states, rows, torch.float32, dev), _strided("d_out", d_out, dev)
+    s1, lens = _whole("d_final_state", d_final_state, ss, torch.float32, dev), _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev)
+    g["x"], dx = _result("grads['x']", g.get("x"), x, dev, side)
+    g["forget"], df = _result("grads['forget']", g.get("forget"), forget, dev, side)
+    if input_gate is not None:
+        g["input_gate"], di = _result("grads['input_gate']", g.get("input_gate"), input_gate, dev, side)
+    else:
+        di = _whole("grads['input_gate']", g.setdefault("input_gate", None), xs, dt, dev)
+    if g.get("initial_state") is None and want_initial_state:
+        g["initial_state"] = _new(ss, torch.float32, x.device, side)
+        d0 = g["initial_state"].data_ptr()
+    else:
+        d0 = _whole("grads['initial_state']", g.setdefault("initial_state", None), ss, torch.float32, dev)
+    keep2, room, size = _workspace(workspace, nbytes, x.device, dev, side)
+    _call(dev, load().prism_gated_scan_backward, dims, x.data_ptr(), f, i, st, dy, s1, dx, df, di, d0, lens, room, size, raw)
     return g
 
 
@@ -252,13 +272,10 @@ def prism_gated_scan_decode_step(x, forget, state, *, input_gate=None, slots=Non
     N = state.shape[0]
     if side is not None:
         _used(side, x, forget, input_gate, state, slots, out)
-    if out is None:
-        out = _out(x, side)
-    _call(
-        dev, load().prism_gated_scan_decode_step, dims, x.data_ptr(), _strided("forget", forget, dev),
-        None if input_gate is None else _strided("input_gate", input_gate, dev),
-        _whole("state", state, (N, xs[1]), torch.float32, dev), N, _whole("slots", slots, xs[:1], torch.int32, dev),
-        _whole("out", out, xs, dt, dev), raw)
+    f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
+    st, at = _whole("state", state, (N, xs[1]), torch.float32, dev), _whole("slots", slots, xs[:1], torch.int32, dev)
+    out, to = _result("out", out, x, dev, side)
+    _call(dev, load().prism_gated_scan_decode_step, dims, x.data_ptr(), f, i, st, N, at, to, raw)
     return out
 
 

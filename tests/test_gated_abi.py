@@ -32,7 +32,7 @@ def norm_dims(**kw):
 
 
 def scan_dims(**kw):
-    d = gated.GatedDims(B=2, T=300, D=64, dtype=prism.PRISM_BF16, flags=0)
+    d = gated.GatedDims(B=2, T=3000, D=64, dtype=prism.PRISM_BF16, flags=0)
     for n, v in kw.items():
         setattr(d, n, pair(v) if isinstance(v, tuple) else v)
     return d
@@ -90,8 +90,8 @@ def test_norm_bad_pointers(lib):
 
 @pytest.mark.parametrize("field,value,code", [
     ("B", 0, ARG), ("T", 0, ARG), ("D", -8, ARG), ("D", 20, UNSUPPORTED), ("dtype", 9, ARG), ("flags", 1, ARG),
-    ("flags", 16, ARG), ("x_stride", (300 * 64, 32), ARG), ("f_stride", (300 * 64, 68), ARG), ("f_stride", (0, 64), ARG),
-    ("i_stride", (-19200, 64), ARG), ("i_stride", (19204, 64), ARG), ("T", 1 << 30, UNSUPPORTED)])
+    ("flags", 16, ARG), ("x_stride", (3000 * 64, 32), ARG), ("f_stride", (3000 * 64, 68), ARG), ("f_stride", (0, 64), ARG),
+    ("i_stride", (-192000, 64), ARG), ("i_stride", (192004, 64), ARG), ("T", 1 << 30, UNSUPPORTED)])
 def test_scan_bad_dims(lib, field, value, code):
     d = scan_dims(**{field: value})
     assert lib.prism_gated_scan_forward(a(d), *[OK] * 7, None, WS, 1 << 62, None) == code
@@ -108,7 +108,7 @@ def test_scan_bad_pointers(lib):
     n, nb = lib.prism_gated_scan_workspace_bytes(a(d)), lib.prism_gated_scan_backward_workspace_bytes(a(d))
     assert n > 0 and nb > 0
     # x, forget, input_gate, initial_state, out, final_state, states, seq_lens
-    good = [OK, OK, None, None, OK, None, None, None]
+    good = [OK, OK, OK, None, OK, None, None, None]
 
     def fwd(p, ws=WS, size=n, dims=d):
         return lib.prism_gated_scan_forward(a(dims), *p, ws, size, None)
@@ -132,7 +132,7 @@ def test_scan_bad_pointers(lib):
         assert back([*good[:i], ODD, *good[i + 1:]]) == MISALIGNED
     assert back([*good[:10], 0x1003]) == MISALIGNED
     assert back(good, ws=None) == WORKSPACE and back(good, size=nb - 1) == WORKSPACE
-    assert back(good, dims=scan_dims(do_stride=(300 * 64, 8))) == ARG
+    assert back(good, dims=scan_dims(do_stride=(3000 * 64, 8))) == ARG
 
 
 def test_more_tiles_than_a_grid_has(lib):
@@ -141,12 +141,22 @@ def test_more_tiles_than_a_grid_has(lib):
     assert lib.prism_gated_scan_workspace_bytes(a(d)) == 0
 
 
+def test_token_numbers_stay_within_32_bits(lib):
+    for dims, f, args in ((norm_dims, lib.prism_layer_norm, [OK] * 3 + [None, OK, None]),
+                          (scan_dims, lib.prism_gated_scan_forward, [OK] * 7 + [None, WS, 1 << 62, None])):
+        assert f(a(dims(B=1, T=(1 << 30) + 1)), *args) == UNSUPPORTED
+
+
 def test_short_sequences_need_no_workspace(lib):
-    for dtype, T in ((prism.PRISM_BF16, 128), (prism.PRISM_F32, 64)):
-        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=T, dtype=dtype))) == 0
-        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=T + 1, dtype=dtype))) > 0
-        assert lib.prism_gated_scan_backward_workspace_bytes(a(scan_dims(T=64, dtype=dtype))) == 0
-        assert lib.prism_gated_scan_backward_workspace_bytes(a(scan_dims(T=65, dtype=dtype))) > 0
+    for dtype, T, back in ((prism.PRISM_BF16, 128, 64), (prism.PRISM_F32, 64, 64)):
+        many = dict(dtype=dtype, B=64, D=2048)
+        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=T, **many))) == 0
+        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=T + 1, **many))) > 0
+        assert lib.prism_gated_scan_backward_workspace_bytes(a(scan_dims(T=back, **many))) == 0
+        assert lib.prism_gated_scan_backward_workspace_bytes(a(scan_dims(T=back + 1, **many))) > 0
+        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=500, dtype=dtype))) == 0        # a cluster a chain
+        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=1025, dtype=dtype))) > 0
+        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=32, **many))) == 0
 
 
 @pytest.mark.parametrize("flags,fine", [(0, True), (8, True), (1, False), (2, False), (4, False), (9, False), (1 << 31, False)])

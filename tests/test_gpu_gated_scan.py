@@ -122,6 +122,17 @@ def test_many_tiles_and_sequences(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("B,T,D", [(2000, 4, 40), (1100, 20, 40), (1300, 130, 24), (300, 64, 136), (300, 65, 136), (40, 400, 520), (4, 1000, 256),
+                                   (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72)])
+def test_every_way(B, T, D, gate, dtype):
+    """Token by token, a cluster a chain, looking back in tiles of each length: the rules' borders."""
+    lens = torch.randint(0, T + 1, (B,), generator=torch.Generator().manual_seed(B))
+    z = make(B, T, D, dtype, gate)
+    check(z, dev(z), lens=lens)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_long_sequence(dtype):
     """A chain of 400 tiles, with channels that hardly forget."""
     z = make(1, 25600, 8, dtype, spread=12.0)
@@ -258,7 +269,7 @@ def test_single_tokens(B, D, gate, dtype):
     assert torch.equal(out2, a[:, 0]) and torch.equal(own, b)
 
 
-@pytest.mark.parametrize("T", [129, 3000])
+@pytest.mark.parametrize("T", [1100, 3000])
 def test_waits_that_run_out(T):
     """The failure path's check sets the word and leaves the outputs as they are; short sequences wait for nothing."""
     z = make(2, T, 72, "bf16")
@@ -274,4 +285,28 @@ def test_waits_that_run_out(T):
     assert gated.gated_status() != 0 and all(torch.equal(g[n], g2[n]) for n in g)
     x, f, i = (c[n][:, :32].contiguous() for n in ("x", "f", "i"))
     gated.prism_gated_scan_forward(x, f, input_gate=i, flags=prism.PRISM_FLAG_CHECK_WAIT_TIMEOUT)
+    assert gated.gated_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 elements a tensor: the last sequence as by itself, in the same way (bit for bit), gradient and all."""
+    B, T, D = 4, 35000, 16384
+    x = torch.empty(B, T, D, dtype=torch.bfloat16, device="cuda")
+    f, d = torch.empty_like(x), torch.empty_like(x)
+    for t, s in ((x, 1), (f, 2), (d, 3)):
+        g = torch.Generator(device="cuda").manual_seed(s)
+        for b in range(B):
+            t[b].normal_(generator=g)
+    states = gated.gated_scan_states(x)
+    out, final = gated.prism_gated_scan_forward(x, f, states=states)
+    g = gated.prism_gated_scan_backward(x, f, states, d)
+    st = gated.gated_scan_states(x[3:])
+    o3, f3 = gated.prism_gated_scan_forward(x[3:], f[3:], states=st)
+    g3 = gated.prism_gated_scan_backward(x[3:], f[3:], st, d[3:])
+    assert torch.equal(out[3:], o3) and torch.equal(final[3:], f3) and torch.equal(states[3:], st)
+    assert torch.equal(g["x"][3:], g3["x"]) and torch.equal(g["forget"][3:], g3["forget"])
+    y = gated.prism_layer_norm(x)
+    n = gated.prism_layer_norm_backward(x, d)
+    assert torch.equal(y[3:], gated.prism_layer_norm(x[3:]))
+    assert torch.equal(n["x"][3:], gated.prism_layer_norm_backward(x[3:], d[3:])["x"])
     assert gated.gated_status() == 0
