@@ -13,7 +13,6 @@ struct GatedDecodeArgs;
 struct LayerNormArgs;
 
 constexpr int kGatedChunk = 64;          // tokens from one row of states to the next
-constexpr int kGatedCols = 64;           // channels of a tile: two a lane
 // Short sequences go token by token, a thread two channels: up to 8 tokens always (2 x 2 x 240 bf16: 1.8 us,
 // 3.0 in tiles), up to 32 where there are threads enough (36 x 15 x 1256 bf16: 4.0 us, 8.4 in tiles; but
 // 2 x 23 x 48 fp32 gradient: 8.6 us, 4.4 in tiles).
@@ -26,26 +25,33 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //           there are chains for all CTAs (64 x 512 x 2048: 94 us, in tiles of 128 101), 128 where few chains are
 //           long (1 x 65536 x 256: 51 us, of 64 80); without one 128 (8 x 4096 x 2048: 74 us, of 64 82), and 256
 //           where half of the SMs have no chain of their own (1 x 65536 x 4096: 293 us, of 128 318).
+//  cols     channels of a tile: 64, or 32 with twice the tokens for layers that are not wider (133 x 1677 x 24: 19 us and 28;
+//           gradient, 13 x 28973 x 32: 58 and 90) and in the gradient for few chains, which it doubles (3 x 55289 x 56: 60 us
+//           and 77; 8 x 4096 x 2048, many chains: 178 and 164).
 //  cluster  the tiles of a chain are one cluster and need no workspace: chains of up to 8 tiles where all tiles
 //           run at once (4 x 1000 x 256: 8.7 us, 11.2 by looking back), or nearly so for two tiles a chain (512 x 200 x
 //           64: 16.9 us and 18.1).  Where clusters take chain after chain they wait for the slowest of their CTAs
 //           each time (64 x 512 x 2048: 217 us and 101).
 struct GatedPlan {
-  int tile;
+  int tile, cols;
   bool cluster;
 };
 inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, int D) {
-  const long long chains = (long long)B * ((D + kGatedCols - 1) / kGatedCols);
+  const long long chains = (long long)B * ((D + 63) / 64);        // of 64 channels
   const auto fits = [&](int tile, int ctas) {      // by cluster, `ctas` on an SM
     const long long n = ((long long)T + tile - 1) / tile;
     return n == 1 || (n <= 8 && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
   };
-  if (backward) return {64, fits(64, dtype ? 2 : 1)};
-  if (dtype == 0) return {64, fits(64, 2)};
-  if (T <= 64) return {64, true};
-  if (fits(128, 2)) return {128, true};
-  if (gated) return {chains >= 256 ? 64 : 128, false};
-  return {chains <= 76 ? 256 : 128, false};
+  if (dtype == 0) return {64, 64, fits(64, backward ? 1 : 2)};
+  if (backward) {
+    if (fits(64, 2)) return {64, 64, true};
+    return D <= 32 || chains <= 76 ? GatedPlan{128, 32, false} : GatedPlan{64, 64, false};
+  }
+  if (T <= 64) return {64, 64, true};
+  if (fits(128, 2)) return {128, 64, true};
+  if (D <= 32) return {128, 32, false};
+  if (gated) return {chains >= 256 ? 64 : 128, 64, false};
+  return {chains <= 76 ? 256 : 128, 64, false};
 }
 constexpr int kLayerNormMaxD = 16384;
 

@@ -56,13 +56,12 @@ int fill_norm(const prism_layer_norm_dims* d, const void* x, const float* weight
 
 // ---- gated recurrence ----
 
-int strips_of(const prism_gated_dims* d) { return (d->D + prism::kGatedCols - 1) / prism::kGatedCols; }
 int chunks_of(const prism_gated_dims* d) { return (d->T + prism::kGatedChunk - 1) / prism::kGatedChunk; }
 prism::GatedPlan plan_of(const prism_gated_dims* d, bool backward, bool gated) {
   return prism::gated_plan(d->dtype == PRISM_F32 ? 0 : 1, backward, gated, d->B, d->T, d->D);
 }
-long long tiles_of(const prism_gated_dims* d, int tile) {
-  return (long long)d->B * strips_of(d) * (((long long)d->T + tile - 1) / tile);
+long long tiles_of(const prism_gated_dims* d, int tile, int cols) {
+  return (long long)d->B * (((long long)d->D + cols - 1) / cols) * (((long long)d->T + tile - 1) / tile);
 }
 
 int check_gated(const prism_gated_dims* d, unsigned flags) {
@@ -70,7 +69,7 @@ int check_gated(const prism_gated_dims* d, unsigned flags) {
   if (d->flags & ~flags) return PRISM_ERR_INVALID_ARG;
   const int rc = check_tokens(d->B, d->T, d->D, d->dtype);
   if (rc != PRISM_OK) return rc;
-  if ((long long)d->B * strips_of(d) > kMost || tiles_of(d, prism::kGatedChunk) > kMost) return PRISM_ERR_UNSUPPORTED;
+  if (tiles_of(d, prism::kGatedChunk, 32) > kMost) return PRISM_ERR_UNSUPPORTED;     // more than any plan has
   return PRISM_OK;
 }
 
@@ -78,7 +77,7 @@ int check_gated(const prism_gated_dims* d, unsigned flags) {
 constexpr size_t kCounter = 256;
 size_t gated_bytes(const prism_gated_dims* d, prism::GatedPlan plan) {
   if (plan.cluster || prism::gated_is_short(d->B, d->T, d->D)) return 0;
-  return kCounter + (size_t)tiles_of(d, plan.tile) * 32 * 24;
+  return kCounter + (size_t)tiles_of(d, plan.tile, plan.cols) * 32 * 24;
 }
 // with or without an input gate
 size_t gated_bytes(const prism_gated_dims* d, bool backward) {
@@ -106,13 +105,13 @@ struct GatedCall {
 };
 
 // TMA map of a [B][T][D] tensor as (D, T, B), in boxes of a tile.
-bool make_map(CUtensorMap* m, const void* p, const long long (&step)[2], const prism_gated_dims* d, int tile) {
+bool make_map(CUtensorMap* m, const void* p, const long long (&step)[2], const prism_gated_dims* d, prism::GatedPlan plan) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = prism::encode_fn();
   if (!fn) return false;
   const int size = prism::elem_bytes(d->dtype);
   const cuuint64_t dim[3] = {(cuuint64_t)d->D, (cuuint64_t)d->T, (cuuint64_t)d->B};
   const cuuint64_t stride[2] = {(cuuint64_t)step[1] * size, (cuuint64_t)step[0] * size};
-  const cuuint32_t box[3] = {prism::kGatedCols, (cuuint32_t)tile, 1}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)plan.cols, (cuuint32_t)plan.tile, 1}, one[3] = {1, 1, 1};
   return fn(m, d->dtype == PRISM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
             const_cast<void*>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -155,21 +154,20 @@ int run_gated(const prism_gated_dims* d, bool backward, const GatedCall& c, void
   a.lens = c.lens;
   a.B = d->B; a.T = d->T; a.D = d->D;
   a.NC = chunks_of(d);
-  a.strips = strips_of(d);
   a.gated = gated;
   a.check = (d->flags & PRISM_FLAG_CHECK_WAIT_TIMEOUT) != 0;
   for (int i = 0; i < c.inputs; ++i)
-    if (!make_map(&a.map[i], c.in[i], step[i], d, plan.tile)) return PRISM_ERR_CUDA;
+    if (!make_map(&a.map[i], c.in[i], step[i], d, plan)) return PRISM_ERR_CUDA;
   const long long whole[2] = {(long long)d->T * d->D, d->D};
   for (int i = 0; i < c.outputs; ++i)
-    if (!make_map(&a.to[i], c.out[i], whole, d, plan.tile)) return PRISM_ERR_CUDA;
+    if (!make_map(&a.to[i], c.out[i], whole, d, plan)) return PRISM_ERR_CUDA;
   const int rc = find_status(&a.status);
   if (rc != PRISM_OK) return rc;
   if (need) {
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<unsigned*>(w);
     a.agg = reinterpret_cast<ulonglong2*>(w + kCounter);
-    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d, plan.tile) * 32 * 16);
+    a.incl = reinterpret_cast<uint2*>(w + kCounter + (size_t)tiles_of(d, plan.tile, plan.cols) * 32 * 16);
     if (cudaMemsetAsync(workspace, 0xff, need, s) != cudaSuccess) return PRISM_ERR_CUDA;
   }
   return prism::launch_gated_scan(d->dtype == PRISM_F32 ? 0 : 1, backward, a, plan, s) == cudaSuccess ? PRISM_OK

@@ -329,6 +329,9 @@ __device__ __forceinline__ uint64_t look_far(const GatedArgs& p, long long at, i
   }
 }
 
+// A tile of CW channels by TT tokens: a lane takes two channels of R tokens, 64 / CW runs of tokens side by side in a warp.
+template <int CW, int TT, int R> constexpr int kGatedThreads = TT / R * (CW / 2);
+
 // What a CTA needs to know about its tile: computed by one thread, read by all.
 struct GatedJob {
   int first, live, rank, last;
@@ -342,12 +345,12 @@ struct GatedJob {
 // With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles): they hand each other (P, L)
 // through shared memory, with one barrier of the cluster, and need neither tickets nor workspace.
 constexpr int kGatedCluster = 8;
-template <class E, int NI, int NO, int TT, int R, int S, bool CL>
+template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
 struct GatedShared {
-  static constexpr int NW = TT / R;
+  static constexpr int NW = kGatedThreads<CW, TT, R> / 32;
   static constexpr bool BACK = NI > 2 && NO > 1;
-  alignas(128) E tile[S][NI][TT][kGatedCols];
-  alignas(128) E out[NO][TT][kGatedCols];
+  alignas(128) E tile[S][NI][TT][CW];
+  alignas(128) E out[NO][TT][CW];
   ulonglong2 part[2][NW][32];                      // (P, L) of a warp's tokens, then of those before them: both channels of P, of L
   union {
     GatedFar<(NW < 8 ? NW : 8)> far;
@@ -363,9 +366,9 @@ struct GatedShared {
 };
 
 // Tickets and copies of a CTA, which one thread makes.
-template <class E, int NI, int NO, int TT, int R, int S, bool CL>
+template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
 struct GatedFeed {
-  GatedShared<E, NI, NO, TT, R, S, CL>& sm;
+  GatedShared<E, NI, NO, CW, TT, R, S, CL>& sm;
   const GatedArgs& p;
   unsigned next;
   bool lost;                                       // a copy never came: no more of them
@@ -395,13 +398,13 @@ struct GatedFeed {
       tc::bar_expect_tx(&sm.full[s], sizeof(sm.tile[s]));
 #pragma unroll
       for (int k = 0; k < NI; ++k)
-        tma_load_3d(sm.tile[s][k], &p.map[k], tl.strip * kGatedCols, tl.first, tl.b, &sm.full[s]);
+        tma_load_3d(sm.tile[s][k], &p.map[k], tl.strip * CW, tl.first, tl.b, &sm.full[s]);
     }
     draw(it + 1);                                  // ready when it is needed
   }
   __device__ __forceinline__ void store(const GatedJob& j) {
 #pragma unroll
-    for (int k = 0; k < NO; ++k) tma_store_3d(&p.to[k], sm.out[k], j.strip * kGatedCols, j.first, j.b);
+    for (int k = 0; k < NO; ++k) tma_store_3d(&p.to[k], sm.out[k], j.strip * CW, j.first, j.b);
     tc::bulk_commit();
   }
 };
@@ -441,16 +444,16 @@ __device__ __forceinline__ uint64_t load_pair(const float* p) {
 }
 
 // Forward.  Tiles of TT tokens, R a lane, TT/R warps, S stages, C CTAs an SM.
-template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
-__global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
+__global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(kGatedChunk % R == 0, "a row of states starts at a warp's tokens");
-  constexpr int NW = TT / R, NI = GATED ? 3 : 2;
-  using Shared = GatedShared<E, NI, 1, TT, R, S, CL>;
+  constexpr int NW = kGatedThreads<CW, TT, R> / 32, H = 64 / CW, NI = GATED ? 3 : 2;
+  using Shared = GatedShared<E, NI, 1, CW, TT, R, S, CL>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / (CW / 2), col = lane % (CW / 2) * 2;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, NI, 1, TT, R, S, CL> feed{sm, p, 0, false};
+  GatedFeed<E, NI, 1, CW, TT, R, S, CL> feed{sm, p, 0, false};
   if (feeder) feed.init();
   if (CL) chain_barrier(p);                        // its CTAs are there
   else __syncthreads();
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
   for (;; ++it) {
     const GatedJob job = sm.job[it % (2 * S)];
     if (!job.more) break;
-    const int s = it % S, mine = warp * R;         // the warp's first token in the tile
+    const int s = it % S, mine = (warp * H + sub) * R;    // the lane's first token in the tile
     bool ok = true;
     if (job.live > 0 && !lost) {
       ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
@@ -469,10 +472,10 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
     uint64_t a[R], u[R], P = both(1.f), L = both(0.f);
     auto token = [&](int j) {
       Two<E> x, f, i;
-      x.load(&sm.tile[s][0][mine + j][2 * lane]);
-      f.load(&sm.tile[s][1][mine + j][2 * lane]);
+      x.load(&sm.tile[s][0][mine + j][col]);
+      f.load(&sm.tile[s][1][mine + j][col]);
       if constexpr (GATED) {
-        i.load(&sm.tile[s][2][mine + j][2 * lane]);
+        i.load(&sm.tile[s][2][mine + j][col]);
         a[j] = gate_of<E>(f.get()).s;
         u[j] = mul2(sigmoid_of<E>(i.get()), x.get());
       } else {
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
       feed.load(it + S);
     }
-    const int ch = job.strip * kGatedCols + 2 * lane, step = p.strips * 32;
+    const int ch = job.strip * CW + col, step = p.strips * 32;
     const bool on = ch < p.D;
     const long long at = ((long long)job.b * p.tiles * p.strips + job.strip) * 32 + lane;
     const long long row = (long long)job.b * p.D + ch;
@@ -521,9 +524,10 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
         P = both(1.f);
         L = both(0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const ulonglong2 g = part[w][lane];
-          part[w][lane] = make_ulonglong2(P, L);
+        for (int w = 0; w < NW * H; ++w) {         // runs of tokens; lanes of other runs do the same for their channels
+          const ulonglong2 g = part[w / H][w % H * (CW / 2) + col / 2];
+          __syncwarp();
+          part[w / H][w % H * (CW / 2) + col / 2] = make_ulonglong2(P, L);
           L = fma2(g.x, L, g.y);
           P = mul2(g.x, P);
         }
@@ -553,9 +557,10 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
           P = both(1.f);
           L = both(0.f);
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const ulonglong2 g = part[w][lane];
-            part[w][lane] = make_ulonglong2(P, L);
+          for (int w = 0; w < NW * H; ++w) {         // runs of tokens; lanes of other runs do the same for their channels
+            const ulonglong2 g = part[w / H][w % H * (CW / 2) + col / 2];
+            __syncwarp();
+            part[w / H][w % H * (CW / 2) + col / 2] = make_ulonglong2(P, L);
             L = fma2(g.x, L, g.y);
             P = mul2(g.x, P);
           }
@@ -592,13 +597,13 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         h = fma2(a[j], h, u[j]);
-        Two<E>::store(&sm.out[0][mine + j][2 * lane], h);
+        Two<E>::store(&sm.out[0][mine + j][col], h);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         h = fma2(a[j], h, u[j]);
-        Two<E>::store(&sm.out[0][mine + j][2 * lane], mine + j < job.live ? h : both(0.f));
+        Two<E>::store(&sm.out[0][mine + j][col], mine + j < job.live ? h : both(0.f));
       }
     }
   }
@@ -613,16 +618,16 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_kernel(const __grid
 
 // Gradient.  The tile's states come from the row of `states` before it, what reaches it from
 // behind from the tiles after it.
-template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
-__global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
+__global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(TT % kGatedChunk == 0, "a tile starts at a row of states");
-  constexpr int NW = TT / R, NI = GATED ? 4 : 3, NO = GATED ? 3 : 2;
-  using Shared = GatedShared<E, NI, NO, TT, R, S, CL>;
+  constexpr int NW = kGatedThreads<CW, TT, R> / 32, H = 64 / CW, NI = GATED ? 4 : 3, NO = GATED ? 3 : 2;
+  using Shared = GatedShared<E, NI, NO, CW, TT, R, S, CL>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / (CW / 2), col = lane % (CW / 2) * 2;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, NI, NO, TT, R, S, CL> feed{sm, p, 0, false};
+  GatedFeed<E, NI, NO, CW, TT, R, S, CL> feed{sm, p, 0, false};
   if (feeder) feed.init();
   if (CL) chain_barrier(p);                        // its CTAs are there
   else __syncthreads();
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
   for (;; ++it) {
     const GatedJob job = sm.job[it % (2 * S)];
     if (!job.more) break;
-    const int s = it % S, mine = warp * R, ch = job.strip * kGatedCols + 2 * lane;
+    const int s = it % S, mine = (warp * H + sub) * R, ch = job.strip * CW + col;
     const bool on = ch < p.D;
     uint64_t h0 = none;                            // the tile's first state: warp 1 hands it on
     if (warp == 1 && on && job.live > 0)
@@ -648,14 +653,14 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     uint64_t a[R], c[R], w[GATED ? R : 1], v[GATED ? R : 1], P = one, L = none, r = none;
     auto token = [&](int j) {
       Two<E> f, i;
-      x[j].load(&sm.tile[s][0][mine + j][2 * lane]);
-      f.load(&sm.tile[s][1][mine + j][2 * lane]);
-      d[j].load(&sm.tile[s][2][mine + j][2 * lane]);
+      x[j].load(&sm.tile[s][0][mine + j][col]);
+      f.load(&sm.tile[s][1][mine + j][col]);
+      d[j].load(&sm.tile[s][2][mine + j][col]);
       const Gate g = gate_of<E>(f.get());
       a[j] = g.s;
       c[j] = g.c;
       if constexpr (GATED) {
-        i.load(&sm.tile[s][3][mine + j][2 * lane]);
+        i.load(&sm.tile[s][3][mine + j][col]);
         const Gate k = gate_of<E>(i.get());
         w[j] = k.s;
         v[j] = k.c;
@@ -706,9 +711,10 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
     if (warp == 1) {
       uint64_t h = h0;
 #pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        sm.start[k][lane] = h;
-        const ulonglong2 g = part[k][lane];
+      for (int k = 0; k < NW * H; ++k) {
+        const int l = k % H * (CW / 2) + col / 2;
+        sm.start[k / H][l] = h;
+        const ulonglong2 g = part[k / H][l];
         h = fma2(g.x, h, g.y);
       }
     }
@@ -720,10 +726,11 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
         P = one;
         L = none;
 #pragma unroll
-        for (int k = NW - 1; k >= 0; --k) {
-          const uint64_t q = part[k][lane].x;
-          sm.behind[k][lane] = make_ulonglong2(P, L);
-          L = fma2(q, L, back[k][lane]);
+        for (int k = NW * H - 1; k >= 0; --k) {
+          const int l = k % H * (CW / 2) + col / 2;
+          const uint64_t q = part[k / H][l].x;
+          sm.behind[k / H][l] = make_ulonglong2(P, L);
+          L = fma2(q, L, back[k / H][l]);
           P = mul2(q, P);
         }
         hand_on(p, job.rank, &sm.ahead[it & 1][job.rank][lane], make_ulonglong2(P, L));
@@ -752,10 +759,11 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
           P = one;
           L = none;
 #pragma unroll
-          for (int k = NW - 1; k >= 0; --k) {
-            const uint64_t q = part[k][lane].x;
-            sm.behind[k][lane] = make_ulonglong2(P, L);
-            L = fma2(q, L, back[k][lane]);
+          for (int k = NW * H - 1; k >= 0; --k) {
+            const int l = k % H * (CW / 2) + col / 2;
+            const uint64_t q = part[k / H][l].x;
+            sm.behind[k / H][l] = make_ulonglong2(P, L);
+            L = fma2(q, L, back[k / H][l]);
             P = mul2(q, P);
           }
           uint64_t g = none;
@@ -798,12 +806,12 @@ __global__ void __launch_bounds__(32 * TT / R, C) gated_scan_backward_kernel(con
       const bool there = mine + j < job.live;
       if constexpr (GATED) {
         const uint64_t gx = mul2(G, w[j]);
-        Two<E>::store(&sm.out[0][mine + j][2 * lane], there ? gx : none);
-        Two<E>::store(&sm.out[1][mine + j][2 * lane], there ? mul2(mul2(r, c[j]), hp[j]) : none);
-        Two<E>::store(&sm.out[NO - 1][mine + j][2 * lane], there ? mul2(mul2(gx, v[j]), xj) : none);
+        Two<E>::store(&sm.out[0][mine + j][col], there ? gx : none);
+        Two<E>::store(&sm.out[1][mine + j][col], there ? mul2(mul2(r, c[j]), hp[j]) : none);
+        Two<E>::store(&sm.out[NO - 1][mine + j][col], there ? mul2(mul2(gx, v[j]), xj) : none);
       } else {
-        Two<E>::store(&sm.out[0][mine + j][2 * lane], there ? mul2(G, c[j]) : none);
-        Two<E>::store(&sm.out[1][mine + j][2 * lane], there ? mul2(mul2(r, c[j]), fma2(xj, minus, hp[j])) : none);
+        Two<E>::store(&sm.out[0][mine + j][col], there ? mul2(G, c[j]) : none);
+        Two<E>::store(&sm.out[1][mine + j][col], there ? mul2(mul2(r, c[j]), fma2(xj, minus, hp[j])) : none);
       }
     }
   }

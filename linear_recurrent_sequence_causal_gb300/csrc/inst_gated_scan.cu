@@ -9,13 +9,14 @@ namespace prism {
 constexpr int kSMs = 152;
 
 // Persistent CTAs.  Chains by cluster: a cluster takes chain after chain; else a CTA takes tile after tile.
-template <class Shared, int TT, int R, int C, bool CL, class F>
+template <class Shared, int CW, int TT, int R, int C, bool CL, class F>
 cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& done, cudaStream_t s) {
   static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
   const cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
   a.tiles = (a.T + TT - 1) / TT;
   if (CL && a.tiles > kGatedCluster) return cudaErrorInvalidValue;
+  a.strips = (a.D + CW - 1) / CW;
   const long long chains = (long long)a.B * a.strips, most = kSMs * C / a.tiles > 0 ? kSMs * C / a.tiles : 1;
   const long long tiles = chains * a.tiles, grid = CL ? (chains < most ? chains : most) * a.tiles : tiles < kSMs * C ? tiles : kSMs * C;
   // Where 16 tiles of a chain run at once, look_near finds only runs (gradient, 1 x 55647 x 328: 91 us, 103 with
@@ -23,7 +24,7 @@ cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& do
   a.deep = grid >= 16 * chains;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(32 * TT / R);
+  cfg.blockDim = dim3(kGatedThreads<CW, TT, R>);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -35,17 +36,17 @@ cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& do
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
 cudaError_t launch_forward(const GatedArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, TT, R, S, CL>, TT, R, C, CL>(
-      gated_scan_kernel<E, GATED, TT, R, S, C, CL>, a, done, s);
+  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, CW, TT, R, S, CL>, CW, TT, R, C, CL>(
+      gated_scan_kernel<E, GATED, CW, TT, R, S, C, CL>, a, done, s);
 }
-template <class E, bool GATED, int TT, int R, int S, int C, bool CL>
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
 cudaError_t launch_backward(const GatedArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, TT, R, S, CL>, TT, R, C, CL>(
-      gated_scan_backward_kernel<E, GATED, TT, R, S, C, CL>, a, done, s);
+  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, CW, TT, R, S, CL>, CW, TT, R, C, CL>(
+      gated_scan_backward_kernel<E, GATED, CW, TT, R, S, C, CL>, a, done, s);
 }
 
 #ifndef GATED_BENCH
@@ -55,29 +56,31 @@ cudaError_t launch_scan_t(bool backward, const GatedArgs& a, GatedPlan plan, cud
   if constexpr (sizeof(E) == 2) {
     const int t = plan.tile;
     if (backward) {
-      if (plan.cluster) return launch_backward<E, GATED, 64, 16, 2, 2, true>(a, s);
-      return launch_backward<E, GATED, 64, 16, 2, 2, false>(a, s);
+      if (plan.cluster) return launch_backward<E, GATED, 64, 64, 16, 2, 2, true>(a, s);
+      if (plan.cols == 32) return launch_backward<E, GATED, 32, 128, 16, 2, 2, false>(a, s);
+      return launch_backward<E, GATED, 64, 64, 16, 2, 2, false>(a, s);
     }
     if (plan.cluster) {
-      if (t == 64) return launch_forward<E, GATED, 64, 16, 1, 4, true>(a, s);
-      return launch_forward<E, GATED, 128, 16, GATED ? 1 : 2, 2, true>(a, s);
+      if (t == 64) return launch_forward<E, GATED, 64, 64, 16, 1, 4, true>(a, s);
+      return launch_forward<E, GATED, 64, 128, 16, GATED ? 1 : 2, 2, true>(a, s);
     }
+    if (plan.cols == 32) return launch_forward<E, GATED, 32, 128, 16, GATED ? 1 : 2, 4, false>(a, s);
     if constexpr (GATED) {
-      if (t == 64) return launch_forward<E, true, 64, 16, 1, 4, false>(a, s);
-      return launch_forward<E, true, 128, 16, 1, 2, false>(a, s);
+      if (t == 64) return launch_forward<E, true, 64, 64, 16, 1, 4, false>(a, s);
+      return launch_forward<E, true, 64, 128, 16, 1, 2, false>(a, s);
     } else {
-      if (t == 256) return launch_forward<E, false, 256, 16, 2, 1, false>(a, s);
-      return launch_forward<E, false, 128, 16, 2, 2, false>(a, s);
+      if (t == 256) return launch_forward<E, false, 64, 256, 16, 2, 1, false>(a, s);
+      return launch_forward<E, false, 64, 128, 16, 2, 2, false>(a, s);
     }
   } else {
     if (backward) {
       constexpr int R = GATED ? 8 : 16, C = GATED ? 1 : 2;
-      if (plan.cluster) return launch_backward<E, GATED, 64, R, 1, C, true>(a, s);
-      return launch_backward<E, GATED, 64, R, 1, C, false>(a, s);
+      if (plan.cluster) return launch_backward<E, GATED, 64, 64, R, 1, C, true>(a, s);
+      return launch_backward<E, GATED, 64, 64, R, 1, C, false>(a, s);
     }
     constexpr int C = GATED ? 2 : 3;
-    if (plan.cluster) return launch_forward<E, GATED, 64, 16, 1, C, true>(a, s);
-    return launch_forward<E, GATED, 64, 16, 1, C, false>(a, s);
+    if (plan.cluster) return launch_forward<E, GATED, 64, 64, 16, 1, C, true>(a, s);
+    return launch_forward<E, GATED, 64, 64, 16, 1, C, false>(a, s);
   }
 }
 
