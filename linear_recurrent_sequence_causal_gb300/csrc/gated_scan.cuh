@@ -8,19 +8,28 @@
 // so it is the same kind of recurrence from the other end: r_t = a_t r_{t+1} + a_t dout_t.
 //
 // Bound by memory (a dozen flops an element of 2 or 4 bytes), but one sequence's channels are too
-// few threads to keep the memory busy token by token.  So time is cut in tiles of 64 tokens by 64
-// channels, a CTA each.  A run of tokens maps the state before it to the one behind it by
-// h -> P h + L, P the product of its a; a lane computes P and L of a few tokens, the CTA joins
+// few threads to keep the memory busy token by token.  So time is cut in tiles of 64 to 256 tokens by 64
+// channels (or 32), a CTA each.  A run of tokens maps the state before it to the one behind it by
+// h -> P h + L, P the product of its a; a lane computes P and L of 16 tokens, the CTA joins
 // those, and a tile's state comes from the tiles before it, which run at the same time: each tile
 // publishes (P, L), looks back over its predecessors to the nearest that knows its own state h,
 // applies what lies between, and publishes its h.  Inputs are read once and nothing is rounded to 16
 // bits on the way.  h is always P h + L of the tile before, whether that tile computed it or a later one did
-// from (P, L), in the same fused operation: the bits do not depend on who comes first.
+// from (P, L), in the same fused operation: the bits do not depend on who comes first.  (Chains that
+// fit a cluster, and sequences of a few tokens, go other ways: gated_plan in gated.h.)
 //
 // Tiles take their place in the order by a ticket, so a tile waits only for tiles that run
 // already.  What is published needs no flag or fence: a word that is not there yet is all ones (the
 // workspace is set to it before the launch), which no P and, by canonical(), no h is; P and L of a
 // channel are one 64-bit word.
+//
+// Measured (GB300, share of the copy rate, the workspace's clearing among it): 8 x 4096 x 2048 bf16 with both gates
+// 93 us (0.85), its gradient 155 us (0.90), 1 x 65536 x 4096 without an input gate 290 us (0.82).  What is
+// left of the first is DRAM (with the look back taken out 90 us) and 3 us of clearing; of the last, 64 chains
+// for 152 CTAs, the look back (without it 240 us).  By themselves 16 tokens a lane instead of 8 made 115 us
+// of 124 (the joins and a tile's set-up are shared by more), outputs by TMA and a tile described once 97.
+// A warp more that looks back while the others work was slower (102 us: its registers are the others'), so were
+// looks taken before the barrier (99 us: they come too early).
 #pragma once
 
 #include <cuda.h>
@@ -57,16 +66,13 @@ struct GatedDecodeArgs {
 };
 
 constexpr unsigned kAbsent = 0xffffffffu;          // not published yet
-constexpr unsigned long long kWaitNs = 1000000000ull, kCheckNs = 1000000ull;
+// Looks of a wait: about a second, and a millisecond.  They are counted, not timed: a GPU that does something else
+// meanwhile takes time from a wait but no looks.
+constexpr unsigned kWaitLooks = 1u << 20, kCheckLooks = 1u << 10;
 
 __device__ __forceinline__ unsigned canonical(float x) {
   const unsigned u = __float_as_uint(x);
   return u == kAbsent ? 0x7fffffffu : u;           // a NaN either way
-}
-__device__ __forceinline__ unsigned long long wall_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
-  return t;
 }
 // Relaxed, at the GPU's scope: each word is whole, and that is all that is needed.
 __device__ __forceinline__ ulonglong2 peek(const ulonglong2* p) {
@@ -217,8 +223,8 @@ __device__ __forceinline__ uint64_t step_over(ulonglong2 g, uint64_t h) {
 
 // PRISM_FLAG_CHECK_WAIT_TIMEOUT (one warp): a wait for a word that nobody writes yet, this tile's own state.
 __device__ __forceinline__ void look_in_vain(const GatedArgs& p, const uint2* own) {
-  const unsigned long long begin = wall_ns();
-  while (!__any_sync(0xffffffffu, peek(own).x != kAbsent || wall_ns() - begin > kCheckNs)) {}
+  unsigned n = 0;
+  while (!__any_sync(0xffffffffu, peek(own).x != kAbsent) && ++n < kCheckLooks) {}
   if ((threadIdx.x & 31) == 0) atomicOr(p.status, 1);
 }
 
@@ -229,8 +235,7 @@ constexpr int kNear = 8, kLooksNear = 2;
 __device__ __forceinline__ bool look_near(const GatedArgs& p, long long at, int step, int rank, ulonglong2 (*held)[32],
                                           uint64_t& h) {
   const int lane = threadIdx.x & 31;
-  const unsigned all = 0xffffffffu;
-  const unsigned long long begin = wall_ns();
+  unsigned looks = 0;
   int n = 0;
   h = both(0.f);
   for (bool found = false; !found;) {
@@ -252,7 +257,7 @@ __device__ __forceinline__ bool look_near(const GatedArgs& p, long long at, int 
     }
     if (found) break;
     if (n == kNear) return false;
-    if (n == before && __any_sync(all, wall_ns() - begin > kWaitNs)) {
+    if (n == before && ++looks == kWaitLooks) {
       if (lane == 0) atomicOr(p.status, 1);
       break;
     }
@@ -261,14 +266,13 @@ __device__ __forceinline__ bool look_near(const GatedArgs& p, long long at, int 
   return true;
 }
 
-constexpr int kLooks = 4;
 // All NW warps look, kLooks tiles each, in turns with a barrier; warp 0 gets the state.
+constexpr int kLooks = 4;
 template <int NW>
 struct GatedFar {
   static_assert(NW == 4 || NW == 8, "a byte a warp, in one or two words");
   ulonglong2 held[kLooks * NW][32];                // (P, L), or the state that ends the walk
   unsigned has[2][NW / 4], knows[2][NW / 4];       // a byte a warp, a bit a tile
-  int late[2];
 };
 // four bits of each byte, side by side
 __device__ __forceinline__ unsigned close_up(unsigned x) {
@@ -278,7 +282,7 @@ __device__ __forceinline__ unsigned close_up(unsigned x) {
 template <int NW>
 __device__ __forceinline__ uint64_t look_far(const GatedArgs& p, long long at, int step, int rank, GatedFar<NW>& far) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned long long begin = wall_ns();
+  unsigned looks = 0;
   for (int turn = 0;; turn ^= 1) {
     unsigned has = 0, knows = 0;
     if (warp < NW) {
@@ -297,7 +301,6 @@ __device__ __forceinline__ uint64_t look_far(const GatedArgs& p, long long at, i
         reinterpret_cast<unsigned char*>(far.knows[turn])[warp] = knows;
       }
     }
-    if (threadIdx.x == 0) far.late[turn] = wall_ns() - begin > kWaitNs;
     __syncthreads();
     has = close_up(far.has[turn][0]);
     knows = close_up(far.knows[turn][0]);
@@ -322,7 +325,7 @@ __device__ __forceinline__ uint64_t look_far(const GatedArgs& p, long long at, i
       }
       return h;
     }
-    if (far.late[turn]) {
+    if (++looks == kWaitLooks) {                   // all threads count the same
       if (threadIdx.x == 0) atomicOr(p.status, 1);
       return both(0.f);
     }
@@ -339,7 +342,7 @@ struct GatedJob {
 };
 
 // Shared memory of a CTA: S stages of NI input tiles, NO output tiles, then what warps exchange.  A CTA takes tile
-// after tile.  Copies are TMA's, a box of 64 channels by TT tokens each: the next tiles' come in while
+// after tile.  Copies are TMA's, a box of CW channels by TT tokens each: the next tiles' come in while
 // it works (a stage is free again once its values are in registers), and a tile's outputs
 // leave while it works on the next one.
 // With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles): they hand each other (P, L)
@@ -443,7 +446,7 @@ __device__ __forceinline__ uint64_t load_pair(const float* p) {
   return v.get();
 }
 
-// Forward.  Tiles of TT tokens, R a lane, TT/R warps, S stages, C CTAs an SM.
+// Forward.  S stages, C CTAs an SM.
 template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
 __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(kGatedChunk % R == 0, "a row of states starts at a warp's tokens");
@@ -617,7 +620,8 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
 }
 
 // Gradient.  The tile's states come from the row of `states` before it, what reaches it from
-// behind from the tiles after it.
+// behind from the tiles after it.  Gates and inputs of a lane's tokens stay in registers between the two ends (a, 1 - a, w,
+// 1 - w, x, dout, h: 250 registers at 16 tokens); recomputing the gates instead would fill the SM's exponential unit.
 template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
 __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(TT % kGatedChunk == 0, "a tile starts at a row of states");
@@ -950,7 +954,7 @@ __global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kerne
   if (p.s_out) Two<float>::store(p.s_out + row, r);
 }
 
-// One token: a lane takes two channels of one sequence.
+// One token: a lane takes two channels of one sequence.  512 sequences of 4096 channels, bf16: 5.8 us (0.85 of the copy rate).
 constexpr int kGatedDecodeThreads = 128;
 template <class E, bool GATED>
 __global__ void __launch_bounds__(kGatedDecodeThreads) gated_decode_kernel(GatedDecodeArgs p) {
