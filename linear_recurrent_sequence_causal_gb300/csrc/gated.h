@@ -29,10 +29,12 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //  cols     channels of a tile: 64, or 32 with twice the tokens for layers that are not wider (133 x 1677 x 24: 19 us and 28;
 //           gradient, 13 x 28973 x 32: 58 and 90) and in the gradient for few chains, which it doubles (3 x 55289 x 56: 60 us
 //           and 77; 8 x 4096 x 2048, many chains: 178 and 164).
-//  cluster  the tiles of a chain are one cluster and need no workspace: chains of up to 8 tiles where all tiles
-//           run at once (4 x 1000 x 256: 8.7 us, 11.2 by looking back), or nearly so for two tiles a chain (512 x 200 x
-//           64: 16.9 us and 18.1).  Where clusters take chain after chain they wait for the slowest of their CTAs
-//           each time (64 x 512 x 2048: 217 us and 101).
+//  cluster  the tiles of a chain are one cluster and need no workspace to be got and cleared: chains of up to 16 tiles
+//           where all tiles run at once (4 x 1000 x 256: 8.7 us, 11.2 by looking back; 4 x 1021 x 256 fp32, clusters of 16:
+//           14.7 us a call, 20.9, of it 10.6 and 8.1 on the GPU), or nearly so for two tiles a chain (512 x 200 x 64:
+//           16.9 us and 18.1).  Where clusters take chain after chain they wait for the slowest of their CTAs each time
+//           (64 x 512 x 2048: 217 us and 101).
+constexpr int kGatedCluster = 16;
 struct GatedPlan {
   int tile, cols;
   bool cluster;
@@ -41,9 +43,9 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
   const long long chains = (long long)B * ((D + 63) / 64);        // of 64 channels
   const auto fits = [&](int tile, int ctas) {      // by cluster, `ctas` on an SM
     const long long n = ((long long)T + tile - 1) / tile;
-    return n == 1 || (n <= 8 && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
+    return n == 1 || (n <= kGatedCluster && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
   };
-  if (dtype == 0) return {64, 64, fits(64, backward ? 1 : 2)};
+  if (dtype == 0) return {64, 64, fits(64, backward && gated ? 1 : 2)};
   if (backward) {
     if (fits(64, 2)) return {64, 64, true};
     return D <= 32 || chains <= 76 ? GatedPlan{128, 32, false} : GatedPlan{64, 64, false};

@@ -345,9 +345,9 @@ struct GatedJob {
 // after tile.  Copies are TMA's, a box of CW channels by TT tokens each: the next tiles' come in while
 // it works (a stage is free again once its values are in registers), and a tile's outputs
 // leave while it works on the next one.
-// With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles): they hand each other (P, L)
+// With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles; more than 8 have to be
+// allowed): they hand each other (P, L)
 // through shared memory, with one barrier of the cluster, and need neither tickets nor workspace.
-constexpr int kGatedCluster = 8;
 template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
 struct GatedShared {
   static constexpr int NW = kGatedThreads<CW, TT, R> / 32;

@@ -12,10 +12,11 @@ constexpr int kSMs = 152;
 template <class Shared, int CW, int TT, int R, int C, bool CL, class F>
 cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& done, cudaStream_t s) {
   static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
-  const cudaError_t e = allow_smem(fn, sizeof(Shared), done);
+  cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
   a.tiles = (a.T + TT - 1) / TT;
   if (CL && a.tiles > kGatedCluster) return cudaErrorInvalidValue;
+  if (CL && a.tiles > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   a.strips = (a.D + CW - 1) / CW;
   const long long chains = (long long)a.B * a.strips, most = kSMs * C / a.tiles > 0 ? kSMs * C / a.tiles : 1;
   const long long tiles = chains * a.tiles, grid = CL ? (chains < most ? chains : most) * a.tiles : tiles < kSMs * C ? tiles : kSMs * C;
@@ -56,7 +57,7 @@ cudaError_t launch_scan_t(bool backward, const GatedArgs& a, GatedPlan plan, cud
   if constexpr (sizeof(E) == 2) {
     const int t = plan.tile;
     if (backward) {
-      if (plan.cluster) return launch_backward<E, GATED, 64, 64, 16, 2, 2, true>(a, s);
+      if (plan.cluster) return launch_backward<E, GATED, 64, 64, 16, 1, 2, true>(a, s);
       if (plan.cols == 32) return launch_backward<E, GATED, 32, 128, 16, 2, 2, false>(a, s);
       return launch_backward<E, GATED, 64, 64, 16, 2, 2, false>(a, s);
     }

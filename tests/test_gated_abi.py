@@ -155,7 +155,7 @@ def test_short_sequences_need_no_workspace(lib):
         assert lib.prism_gated_scan_backward_workspace_bytes(a(scan_dims(T=back, **many))) == 0
         assert lib.prism_gated_scan_backward_workspace_bytes(a(scan_dims(T=back + 1, **many))) > 0
         assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=500, dtype=dtype))) == 0        # a cluster a chain
-        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=1025, dtype=dtype))) > 0
+        assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=2049, dtype=dtype))) > 0
         assert lib.prism_gated_scan_workspace_bytes(a(scan_dims(T=32, **many))) == 0
 
 
