@@ -28,7 +28,10 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //           22 x 876 x 144: 11.5 us, of 128 10.1).
 //  cols     channels of a tile: 64, or 32 with twice the tokens for layers that are not wider (133 x 1677 x 24: 19 us and 28;
 //           gradient, 13 x 28973 x 32: 58 and 90) and in the gradient for few chains, which it doubles (3 x 55289 x 56: 60 us
-//           and 77; 8 x 4096 x 2048, many chains: 178 and 164).
+//           and 77; 8 x 4096 x 2048, many chains: 178 and 164).  In fp32 32, so that more than one or two CTAs fit an SM:
+//           8 x 2048 x 2048 with an input gate 90 us, of 64 channels 102, its gradient 150 and 205; tiles of 128 tokens
+//           for few chains (2 x 32082 x 96: 32 us, of 64 42; 8 x 2048 x 2048: 100 and 90) and without an input gate
+//           (1 x 51377 x 376: 56 us, of 64 x 64 65), where the gradient keeps 64 x 64 (100 x 300 x 500: 62 us, of 32 66).
 //  cluster  the tiles of a chain are one cluster and need no workspace to be got and cleared: chains of up to 16 tiles
 //           where all tiles run at once (4 x 1000 x 256: 8.7 us, 11.2 by looking back; 4 x 1021 x 256 fp32, clusters of 16:
 //           14.7 us a call, 20.9, of it 10.6 and 8.1 on the GPU), or nearly so for two tiles a chain (512 x 200 x 64:
@@ -45,7 +48,11 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
     const long long n = ((long long)T + tile - 1) / tile;
     return n == 1 || (n <= kGatedCluster && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
   };
-  if (dtype == 0) return {64, 64, fits(64, backward && gated ? 1 : 2)};
+  if (dtype == 0) {
+    if (fits(64, backward && gated ? 1 : 2)) return {64, 64, true};
+    if (backward) return {64, gated ? 32 : 64, false};
+    return {gated && chains > 76 ? 64 : 128, 32, false};
+  }
   if (backward) {
     if (fits(64, 2)) return {64, 64, true};
     return D <= 32 || chains <= 76 ? GatedPlan{128, 32, false} : GatedPlan{64, 64, false};

@@ -77,11 +77,14 @@ cudaError_t launch_scan_t(bool backward, const GatedArgs& a, GatedPlan plan, cud
     if (backward) {
       constexpr int R = GATED ? 8 : 16, C = GATED ? 1 : 2;
       if (plan.cluster) return launch_backward<E, GATED, 64, 64, R, 1, C, true>(a, s);
-      return launch_backward<E, GATED, 64, 64, R, 1, C, false>(a, s);
+      if constexpr (GATED) return launch_backward<E, true, 32, 64, 8, 1, 3, false>(a, s);
+      else return launch_backward<E, false, 64, 64, 16, 1, 2, false>(a, s);
     }
-    constexpr int C = GATED ? 2 : 3;
-    if (plan.cluster) return launch_forward<E, GATED, 64, 64, 16, 1, C, true>(a, s);
-    return launch_forward<E, GATED, 64, 64, 16, 1, C, false>(a, s);
+    if (plan.cluster) return launch_forward<E, GATED, 64, 64, 16, 1, GATED ? 2 : 3, true>(a, s);
+    if constexpr (GATED) {
+      if (plan.tile == 64) return launch_forward<E, true, 32, 64, 8, 2, 3, false>(a, s);
+    }
+    return launch_forward<E, GATED, 32, 128, 16, 1, GATED ? 2 : 3, false>(a, s);
   }
 }
 
