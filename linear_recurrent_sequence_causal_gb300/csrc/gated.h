@@ -23,9 +23,10 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //  tile     tokens of a tile, whole chunks.  An SM's shared memory and registers hold half as many tiles of twice the
 //           length, which halves what a chain hands on but leaves less beside each other.  With an input gate 64 where
 //           there are chains for all CTAs (64 x 512 x 2048: 94 us, in tiles of 128 101), 128 where few chains are
-//           long (1 x 65536 x 256: 51 us, of 64 80); without one 128 (8 x 4096 x 2048: 74 us, of 64 82), and 256
-//           where half of the SMs have no chain of their own and tiles enough (1 x 65536 x 4096: 293 us, of 128 318; but
-//           22 x 876 x 144: 11.5 us, of 128 10.1).
+//           long (1 x 65536 x 256: 51 us, of 64 80).  Without one 64 where every CTA has a chain of its own (24 x 934 x
+//           5584: 133 us, of 128 154), else 128 (8 x 4096 x 2048: 72 us, of 64 81), and 256 where half of the SMs have
+//           none and there are tiles enough (1 x 65536 x 4096: 293 us, of 128 318; but 22 x 876 x 144: 11.5 us, of 128
+//           10.1).
 //  cols     channels of a tile: 64, or 32 with twice the tokens for layers that are not wider (133 x 1677 x 24: 19 us and 28;
 //           gradient, 13 x 28973 x 32: 58 and 90) and in the gradient for few chains, which it doubles (3 x 55289 x 56: 60 us
 //           and 77; 8 x 4096 x 2048, many chains: 178 and 164).  In fp32 32, so that more than one or two CTAs fit an SM:
@@ -61,7 +62,7 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
   if (fits(128, 2)) return {128, 64, true};
   if (D <= 32) return {128, 32, false};
   if (gated) return {chains >= 256 ? 64 : 128, 64, false};
-  return {chains <= 76 && chains * T >= 304ll * 256 ? 256 : 128, 64, false};
+  return {chains >= 608 ? 64 : chains <= 76 && chains * T >= 304ll * 256 ? 256 : 128, 64, false};
 }
 constexpr int kLayerNormMaxD = 16384;
 

@@ -70,6 +70,7 @@ cudaError_t launch_scan_t(bool backward, const GatedArgs& a, GatedPlan plan, cud
       if (t == 64) return launch_forward<E, true, 64, 64, 16, 1, 4, false>(a, s);
       return launch_forward<E, true, 64, 128, 16, 1, 2, false>(a, s);
     } else {
+      if (t == 64) return launch_forward<E, false, 64, 64, 16, 2, 4, false>(a, s);
       if (t == 256) return launch_forward<E, false, 64, 256, 16, 2, 1, false>(a, s);
       return launch_forward<E, false, 64, 128, 16, 2, 2, false>(a, s);
     }

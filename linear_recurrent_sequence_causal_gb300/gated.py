@@ -69,6 +69,11 @@ def _steps(name, shape, stride):
     return _stride(stride[0] if B > 1 else T * max(stride[1], D), stride[1] if T > 1 else D)
 
 
+def _width(D, most=None):
+    if D % 8 or (most and D > most):
+        raise PrismError(2, f"the channels of a token must be a multiple of 8{f' up to {most}' if most else ''}, got {D}")
+
+
 def _out(t, side):
     """A contiguous tensor of t's shape and type."""
     if side is None and t.is_contiguous():
@@ -102,6 +107,7 @@ def _workspace(t, nbytes, device, dev, side):
 def _norm_dims(xs, xst, dtype, eps, dost):
     if len(xs) != 3:
         raise PrismError(1, f"x must be [B,T,D], got {tuple(xs)}")
+    _width(xs[2], 16384)
     d = LayerNormDims(B=xs[0], T=xs[1], D=xs[2], dtype=_dtype_code(dtype), flags=0, eps=eps,
                       x_stride=_steps("x", xs, xst))
     if dost is not None:
@@ -113,6 +119,7 @@ def _norm_dims(xs, xst, dtype, eps, dost):
 def _gated_dims(xs, dtype, xst, fst, ist, dost, flags):
     if len(xs) != 3:
         raise PrismError(1, f"x and the gates must be [B,T,D], got {tuple(xs)}")
+    _width(xs[2])
     d = GatedDims(B=xs[0], T=xs[1], D=xs[2], dtype=_dtype_code(dtype), flags=flags, x_stride=_steps("x", xs, xst),
                   f_stride=_steps("forget", xs, fst))
     if ist is not None:
@@ -129,6 +136,7 @@ def _decode_dims(xs, dtype, xst, fst, ist):
     if len(xs) != 2:
         raise PrismError(1, f"x and the gates must be [B,D], got {tuple(xs)}")
     B, D = xs
+    _width(D)
 
     def steps(name, st):
         return _steps(name, (B, 1, D), (st[0], D, st[1]))

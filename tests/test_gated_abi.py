@@ -212,6 +212,10 @@ def test_binding_refusals():
     refused(step, t(2, 16), t(2, 16), t(2, 16, dtype=f32))
     refused(step, t(2, 16), t(2, 8), t(2, 16, dtype=f32))
     refused(step, x, x, t(2, 16, dtype=f32))
+    for f, args in ((fwd, (t(2, 8, 12),) * 2), (step, (t(2, 12), t(2, 12), t(2, 12, dtype=f32))), (gated.prism_layer_norm, (t(1, 1, 16392),)),
+                    (gated.prism_layer_norm, (t(2, 8, 12),))):
+        with pytest.raises(prism.PrismError, match="multiple of 8"):
+            f(*args)
     refused(gated.prism_layer_norm, x)                                     # on the CPU
     refused(gated.prism_layer_norm, x[0])
     refused(gated.prism_layer_norm, x.half())

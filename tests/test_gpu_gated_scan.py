@@ -124,7 +124,7 @@ def test_many_tiles_and_sequences(dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gate", [True, False])
 @pytest.mark.parametrize("B,T,D", [(2000, 4, 40), (1100, 20, 40), (1300, 130, 24), (300, 64, 136), (300, 65, 136), (40, 400, 520), (4, 1000, 256), (1, 2048, 136),
-                                   (2, 900, 40), (8, 1024, 64),
+                                   (2, 900, 40), (8, 1024, 64), (620, 200, 40), (60, 200, 704),
                                    (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72)])
 def test_every_way(B, T, D, gate, dtype):
     """Token by token, a cluster a chain, looking back in tiles of each length: the rules' borders."""
