@@ -67,6 +67,7 @@ cudaError_t norm_columns(const LayerNormArgs& a, cudaStream_t s) {
 template <class E>
 cudaError_t forward_e(const LayerNormArgs& a, cudaStream_t s) {
   const int D = a.D;
+  if (D <= 32) return norm_forward<E, 4, 1, 4, 4>(a, s);
   if (D <= 64) return norm_forward<E, 8, 1, 4, 4>(a, s);
   if (D <= 128) return norm_forward<E, 16, 1, 4, 4>(a, s);
   if (D <= 256) return norm_forward<E, 16, 2, 2, 4>(a, s);
@@ -90,6 +91,7 @@ cudaError_t forward_e(const LayerNormArgs& a, cudaStream_t s) {
 template <class E>
 cudaError_t backward_e(const LayerNormArgs& a, cudaStream_t s) {
   const int D = a.D;
+  if (D <= 32) return norm_backward<E, 4, 1, 2, 2, true>(a, s);
   if (D <= 64) return norm_backward<E, 8, 1, 2, 2, true>(a, s);
   if (D <= 128) return norm_backward<E, 16, 1, 2, 2, true>(a, s);
   if constexpr (sizeof(E) == 2) {
