@@ -346,8 +346,8 @@ struct GatedJob {
 // it works (a stage is free again once its values are in registers), and a tile's outputs
 // leave while it works on the next one.
 // With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles; more than 8 have to be
-// allowed): they hand each other (P, L)
-// through shared memory, with one barrier of the cluster, and need neither tickets nor workspace.
+// allowed): they hand each other (P, L) through shared memory, with one barrier of the cluster, and need neither
+// tickets nor workspace.
 template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
 struct GatedShared {
   static constexpr int NW = kGatedThreads<CW, TT, R> / 32;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
       }
       entry = h;
     } else {
-      auto arrive = [&](uint64_t h) {                // the state before the tile is known
+      auto arrive = [&](uint64_t h) {              // the state before the tile is known
         const uint64_t end = fma2(P, h, L);
         if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
         else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
           P = both(1.f);
           L = both(0.f);
 #pragma unroll
-          for (int w = 0; w < NW * H; ++w) {         // runs of tokens; lanes of other runs do the same for their channels
+          for (int w = 0; w < NW * H; ++w) {       // runs of tokens; lanes of other runs do the same for their channels
             const ulonglong2 g = part[w / H][w % H * (CW / 2) + col / 2];
             __syncwarp();
             part[w / H][w % H * (CW / 2) + col / 2] = make_ulonglong2(P, L);
@@ -577,13 +577,13 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
           }
           if (found) arrive(h);
         } else {
-          if (job.rank == 0 && p.s_out && on)        // a sequence without tokens
+          if (job.rank == 0 && p.s_out && on)      // a sequence without tokens
             Two<float>::store(p.s_out + row, p.s_in ? load_pair(p.s_in + row) : both(0.f));
           sm.carry[lane] = both(0.f);
         }
         if (lane == 0) sm.found = found;
       }
-      if (feeder && it > 0) tc::bulk_wait_read();    // the output tile may be written again
+      if (feeder && it > 0) tc::bulk_wait_read();  // the output tile may be written again
       __syncthreads();
       if (!sm.found) {
         const uint64_t h = look_far<(NW < 8 ? NW : 8)>(p, at, step, job.rank, sm.far);
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
       }
       entry = g;
     } else {
-      auto arrive = [&](uint64_t g) {                // what comes from behind the tile is known
+      auto arrive = [&](uint64_t g) {              // what comes from behind the tile is known
         const uint64_t end = fma2(P, g, L);
         if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
         else if (p.s_out && on) Two<float>::store(p.s_out + row, end);

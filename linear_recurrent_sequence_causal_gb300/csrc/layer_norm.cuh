@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       sum[i] = total(t);
       if constexpr (BACK) sum[R + i] = total(g);
     }
-    norm_sum<NT>(sum, sm.room[turn][0]);           // after its barrier the tile is read
+    norm_sum<NT>(sum, sm.room[turn][0]);           // after it the tile is read by all
+    if (NT == 32) __syncwarp();                    // (a single warp sums without the CTA's barrier)
     if (sm.failed) {                               // a copy that never came: no other may outlive the CTA
       if (threadIdx.x == 0) {
         atomicOr(p.status, 1);
