@@ -81,7 +81,8 @@ typedef struct {
  *   states      [B, ceil(T/64), D] fp32, or NULL: the state before the tokens 0, 64, 128, ... of each
  *               sequence, which prism_gated_scan_backward reads.  Rows that start at or behind a
  *               sequence's end are left as they are.
- * Gates and states are fp32; out is rounded once.  A gate below 2^-126 counts as 0.  Tiles of a
+ * Gates and states are fp32; out is rounded once.  A gate below 2^-126 counts as 0, and so may a
+ * product of gates below it (an infinite state may become NaN there).  Tiles of a
  * sequence wait for the state of the tiles before them; the result does not depend on their
  * timing (two calls agree bit for bit).  The workspace has prism_gated_scan_workspace_bytes (0 for short
  * sequences, where no tile looks back: it may then be NULL). */
@@ -112,8 +113,8 @@ PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const v
                                            const int32_t* slots, void* out, void* stream);
 
 /* Failure detection: every wait, a tile's for the state before it and a kernel's for its own copies, is
- * bounded (about a second); one that gives up sets the library's word for the current device, which stays set until it is cleared, and the
- * call's outputs are then undefined.  Synchronises the device and returns the word in *word (0: no
+ * bounded (about a second); one that gives up sets the library's word for the current device, which
+ * stays set until it is cleared, and the call's outputs are then undefined.  Synchronises the device and returns the word in *word (0: no
  * wait gave up), clearing it when `clear` is nonzero.  PRISM_ERR_INVALID_ARG for a NULL word,
  * PRISM_ERR_CUDA when the synchronisation or the copy fails.
  *

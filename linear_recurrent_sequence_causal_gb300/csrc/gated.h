@@ -34,10 +34,23 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //           for few chains (2 x 32082 x 96: 32 us, of 64 42; 8 x 2048 x 2048: 100 and 90) and without an input gate
 //           (1 x 51377 x 376: 56 us, of 64 x 64 65), where the gradient keeps 64 x 64 (100 x 300 x 500: 62 us, of 32 66).
 //  cluster  the tiles of a chain are one cluster and need no workspace to be got and cleared: chains of up to 16 tiles
-//           where all tiles run at once (4 x 1000 x 256: 8.7 us, 11.2 by looking back; 4 x 1021 x 256 fp32, clusters of 16:
-//           14.7 us a call, 20.9, of it 10.6 and 8.1 on the GPU), or nearly so for two tiles a chain (512 x 200 x 64:
-//           16.9 us and 18.1).  Where clusters take chain after chain they wait for the slowest of their CTAs each time
-//           (64 x 512 x 2048: 217 us and 101).
+//           where all tiles run at once, or nearly so for two tiles a chain (2 x 2000 x 128 fp32: 6.1 us, by looking back 7.3).
+//           Where clusters take chain after chain they wait for the slowest of their CTAs each time (64 x 512 x 2048:
+//           217 us and 101).  Clusters of more than 8 CTAs find few places beside each other, and small CTAs find
+//           more, so (tokens x channels of a tile):
+//             64 x 64    bf16 forwards up to 64 tokens (100 x 60 x 256: 4.8 us, 128 x 64 6.6); fp32 forwards with one gate and
+//                        gradients up to 512 (gradient 4 x 500 x 512: 6.3 us, 128 x 32 7.5)
+//             128 x 64   bf16 forwards (4 x 500 x 512: 4.9 us, 128 x 32 5.7; 2 x 2000 x 128: 5.1 and 5.4)
+//             128 x 32   bf16 forwards from 513 to 1024 tokens (4 x 1000 x 256: 5.3 us, 128 x 64 6.6); fp32 forwards and
+//                        gradients from 513 (gradient 4 x 1000 x 256: 7.2 us, 64 x 64 10.4, by looking back 8.3; fp32 6.3,
+//                        64 x 32 6.9, looking back 8.3)
+//             64 x 32    fp32 with both gates up to 512 (100 x 100 x 256: 11.5 us, 64 x 64 16.0; gradient 4 x 500 x 256: 5.7 and
+//                        10.1); it has no room for two CTAs of 128 tokens in the gradient, which looks back from
+//                        513 tokens on (2 x 2000 x 128: 8.4 us, 128 x 32 13.0)
+//           One tile needs no cluster, only the way through shared memory.  The gradient goes by 64 x 32 up to 64 tokens
+//           (100 x 60 x 256: 7.2 us, 64 x 64 8.5; but fp32 with both gates 10.9 and 9.9) and by 128 x 32 up to 128 while chains are few
+//           (100 x 100 x 256: 12.5 us, looking back 14.1; 300 x 100 x 256: 34 and 29.5), as fp32 with one gate does forwards
+//           (100 x 100 x 256: 7.6 us, 64 x 64 9.2).
 constexpr int kGatedCluster = 16;
 struct GatedPlan {
   int tile, cols;
@@ -45,21 +58,34 @@ struct GatedPlan {
 };
 inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, int D) {
   const long long chains = (long long)B * ((D + 63) / 64);        // of 64 channels
-  const auto fits = [&](int tile, int ctas) {      // by cluster, `ctas` on an SM
+  const auto fits = [&](int tile, int ctas) {      // by cluster, `ctas` tiles of 64 channels on an SM
     const long long n = ((long long)T + tile - 1) / tile;
     return n == 1 || (n <= kGatedCluster && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
   };
-  if (dtype == 0) {
-    if (fits(64, backward && gated ? 1 : 2)) return {64, 64, true};
-    if (backward) return {64, gated ? 32 : 64, false};
-    return {gated && chains > 76 ? 64 : 128, 32, false};
+  if (dtype == 0 && gated) {
+    if (backward) {
+      if (T <= 64) return {64, 64, true};
+      return {64, 32, T <= 512 && fits(64, 1)};
+    }
+    if (T <= 512 && fits(64, 2)) return {64, 32, true};
+    if (T > 512 && fits(128, 1)) return {128, 32, true};
+    return {chains > 76 ? 64 : 128, 32, false};
   }
   if (backward) {
-    if (fits(64, 2)) return {64, 64, true};
+    if (T <= 64) return {64, 32, true};
+    if (T <= 128 && chains <= 608) return {128, 32, true};
+    if (T > 128 && T <= 512 && fits(64, 2)) return {64, 64, true};
+    if (T > 512 && fits(128, 1)) return {128, 32, true};
+    if (dtype == 0) return {64, 64, false};
     return D <= 32 || chains <= 76 ? GatedPlan{128, 32, false} : GatedPlan{64, 64, false};
   }
   if (T <= 64) return {64, 64, true};
-  if (fits(128, 2)) return {128, 64, true};
+  if (dtype == 0) {
+    if (T <= 128) return {128, 32, true};
+    if (T <= 512 && fits(64, 2)) return {64, 64, true};
+    return {128, 32, T > 512 && fits(128, 1)};
+  }
+  if (fits(128, 2)) return {128, T > 512 && T <= 1024 ? 32 : 64, true};
   if (D <= 32) return {128, 32, false};
   if (gated) return {chains >= 256 ? 64 : 128, 64, false};
   return {chains >= 608 ? 64 : chains <= 76 && chains * T >= 304ll * 256 ? 256 : 128, 64, false};

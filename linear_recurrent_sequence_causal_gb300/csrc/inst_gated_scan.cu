@@ -10,8 +10,9 @@ constexpr int kSMs = 152;
 
 // Persistent CTAs.  Chains by cluster: a cluster takes chain after chain; else a CTA takes tile after tile.
 template <class Shared, int CW, int TT, int R, int C, bool CL, class F>
-cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& done, cudaStream_t s) {
+cudaError_t launch_tiles(F* fn, GatedArgs a, GatedPlan plan, std::atomic<unsigned long long>& done, cudaStream_t s) {
   static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
+  if (plan.tile != TT || plan.cols != CW || plan.cluster != CL) return cudaErrorInvalidValue;      // the maps' boxes
   cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
   a.tiles = (a.T + TT - 1) / TT;
@@ -38,55 +39,75 @@ cudaError_t launch_tiles(F* fn, GatedArgs a, std::atomic<unsigned long long>& do
 }
 
 template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
-cudaError_t launch_forward(const GatedArgs& a, cudaStream_t s) {
+cudaError_t launch_forward(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, CW, TT, R, S, CL>, CW, TT, R, C, CL>(
-      gated_scan_kernel<E, GATED, CW, TT, R, S, C, CL>, a, done, s);
+      gated_scan_kernel<E, GATED, CW, TT, R, S, C, CL>, a, plan, done, s);
 }
 template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
-cudaError_t launch_backward(const GatedArgs& a, cudaStream_t s) {
+cudaError_t launch_backward(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, CW, TT, R, S, CL>, CW, TT, R, C, CL>(
-      gated_scan_backward_kernel<E, GATED, CW, TT, R, S, C, CL>, a, done, s);
+      gated_scan_backward_kernel<E, GATED, CW, TT, R, S, C, CL>, a, plan, done, s);
 }
 
 #ifndef GATED_BENCH
-// Stages and CTAs an SM are what its shared memory and registers hold.
+// The variants that gated_plan chooses from.  Stages and CTAs an SM are what its shared memory and registers hold.
+template <class E, bool GATED>
+cudaError_t launch_forward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
+  const int t = plan.tile, c = plan.cols;
+  if constexpr (sizeof(E) == 2) {
+    constexpr int S = GATED ? 1 : 2;
+    if (plan.cluster) {
+      if (t == 64) return launch_forward<E, GATED, 64, 64, 16, 1, 4, true>(a, plan, s);
+      if (c == 32) return launch_forward<E, GATED, 32, 128, 16, 1, 4, true>(a, plan, s);
+      return launch_forward<E, GATED, 64, 128, 16, S, 2, true>(a, plan, s);
+    }
+    if (c == 32) return launch_forward<E, GATED, 32, 128, 16, S, 4, false>(a, plan, s);
+    if (t == 64) return launch_forward<E, GATED, 64, 64, 16, S, 4, false>(a, plan, s);
+    if constexpr (!GATED) {
+      if (t == 256) return launch_forward<E, false, 64, 256, 16, 2, 1, false>(a, plan, s);
+    }
+    return launch_forward<E, GATED, 64, 128, 16, S, 2, false>(a, plan, s);
+  } else if constexpr (GATED) {
+    if (plan.cluster) {
+      if (t == 64) return launch_forward<E, true, 32, 64, 8, 1, 4, true>(a, plan, s);
+      return launch_forward<E, true, 32, 128, 16, 1, 2, true>(a, plan, s);
+    }
+    if (t == 64) return launch_forward<E, true, 32, 64, 8, 2, 3, false>(a, plan, s);
+    return launch_forward<E, true, 32, 128, 16, 1, 2, false>(a, plan, s);
+  } else {
+    if (plan.cluster) {
+      if (t == 64) return launch_forward<E, false, 64, 64, 16, 1, 3, true>(a, plan, s);
+      return launch_forward<E, false, 32, 128, 16, 1, 3, true>(a, plan, s);
+    }
+    return launch_forward<E, false, 32, 128, 16, 1, 3, false>(a, plan, s);
+  }
+}
+template <class E, bool GATED>
+cudaError_t launch_backward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
+  const int t = plan.tile, c = plan.cols;
+  if constexpr (sizeof(E) == 4 && GATED) {
+    if (c == 64) return launch_backward<E, true, 64, 64, 8, 1, 1, true>(a, plan, s);
+    if (plan.cluster) return launch_backward<E, true, 32, 64, 8, 1, 2, true>(a, plan, s);
+    return launch_backward<E, true, 32, 64, 8, 1, 3, false>(a, plan, s);
+  } else {
+    if (plan.cluster) {
+      if (t == 128) return launch_backward<E, GATED, 32, 128, 16, 1, 2, true>(a, plan, s);
+      if (c == 64) return launch_backward<E, GATED, 64, 64, 16, 1, 2, true>(a, plan, s);
+      return launch_backward<E, GATED, 32, 64, 8, 1, sizeof(E) == 2 && !GATED ? 4 : 3, true>(a, plan, s);
+    }
+    if constexpr (sizeof(E) == 2) {
+      if (c == 32) return launch_backward<E, GATED, 32, 128, 16, 2, 2, false>(a, plan, s);
+      return launch_backward<E, GATED, 64, 64, 16, 2, 2, false>(a, plan, s);
+    } else {
+      return launch_backward<E, false, 64, 64, 16, 1, 2, false>(a, plan, s);
+    }
+  }
+}
 template <class E, bool GATED>
 cudaError_t launch_scan_t(bool backward, const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
-  if constexpr (sizeof(E) == 2) {
-    const int t = plan.tile;
-    if (backward) {
-      if (plan.cluster) return launch_backward<E, GATED, 64, 64, 16, 1, 2, true>(a, s);
-      if (plan.cols == 32) return launch_backward<E, GATED, 32, 128, 16, 2, 2, false>(a, s);
-      return launch_backward<E, GATED, 64, 64, 16, 2, 2, false>(a, s);
-    }
-    if (plan.cluster) {
-      if (t == 64) return launch_forward<E, GATED, 64, 64, 16, 1, 4, true>(a, s);
-      return launch_forward<E, GATED, 64, 128, 16, GATED ? 1 : 2, 2, true>(a, s);
-    }
-    if (plan.cols == 32) return launch_forward<E, GATED, 32, 128, 16, GATED ? 1 : 2, 4, false>(a, s);
-    if constexpr (GATED) {
-      if (t == 64) return launch_forward<E, true, 64, 64, 16, 1, 4, false>(a, s);
-      return launch_forward<E, true, 64, 128, 16, 1, 2, false>(a, s);
-    } else {
-      if (t == 64) return launch_forward<E, false, 64, 64, 16, 2, 4, false>(a, s);
-      if (t == 256) return launch_forward<E, false, 64, 256, 16, 2, 1, false>(a, s);
-      return launch_forward<E, false, 64, 128, 16, 2, 2, false>(a, s);
-    }
-  } else {
-    if (backward) {
-      constexpr int R = GATED ? 8 : 16, C = GATED ? 1 : 2;
-      if (plan.cluster) return launch_backward<E, GATED, 64, 64, R, 1, C, true>(a, s);
-      if constexpr (GATED) return launch_backward<E, true, 32, 64, 8, 1, 3, false>(a, s);
-      else return launch_backward<E, false, 64, 64, 16, 1, 2, false>(a, s);
-    }
-    if (plan.cluster) return launch_forward<E, GATED, 64, 64, 16, 1, GATED ? 2 : 3, true>(a, s);
-    if constexpr (GATED) {
-      if (plan.tile == 64) return launch_forward<E, true, 32, 64, 8, 2, 3, false>(a, s);
-    }
-    return launch_forward<E, GATED, 32, 128, 16, 1, GATED ? 2 : 3, false>(a, s);
-  }
+  return backward ? launch_backward_t<E, GATED>(a, plan, s) : launch_forward_t<E, GATED>(a, plan, s);
 }
 
 cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, GatedPlan plan, cudaStream_t s) {

@@ -84,6 +84,35 @@ def test_slices_of_a_projection(gate, dtype):
         assert torch.equal(a, b)
 
 
+def time_major(t):
+    return t.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+def windows(t):
+    """Sequences that begin a token apart in one recording."""
+    B, T, D = t.shape
+    return torch.cat((t[0], t[1:, 0])).as_strided((B, T, D), (D, D, 1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("lay", [time_major, windows])
+@pytest.mark.parametrize("B,T,D", [(3, 5, 72), (5, 70, 72), (2, 300, 8), (2, 2500, 136)])
+def test_other_orders(B, T, D, lay, gate, dtype):
+    """Tokens further apart than sequences, and sequences that share tokens: the bits of contiguous inputs."""
+    c = dev(make(B, T, D, dtype, gate))
+    ways = []
+    for there in (True, False):
+        x, f, i, do = (None if c[n] is None else lay(c[n]) for n in ("x", "f", "i", "do"))
+        if there:
+            x, f, i, do = (None if t is None else t.contiguous() for t in (x, f, i, do))
+        states = gated.gated_scan_states(x)
+        out, final = gated.prism_gated_scan_forward(x, f, input_gate=i, initial_state=c["s0"], states=states)
+        g = gated.prism_gated_scan_backward(x, f, states, do, input_gate=i, d_final_state=c["ds"], want_initial_state=True)
+        ways.append((out, final, states, *(t for t in g.values() if t is not None)))
+    assert all(torch.equal(a, b) for a, b in zip(*ways)) and all(t.is_contiguous() for t in ways[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gate", [True, False])
 @pytest.mark.parametrize("T", [1, 64, 300])
@@ -125,7 +154,8 @@ def test_many_tiles_and_sequences(dtype):
 @pytest.mark.parametrize("gate", [True, False])
 @pytest.mark.parametrize("B,T,D", [(2000, 4, 40), (1100, 20, 40), (1300, 130, 24), (300, 64, 136), (300, 65, 136), (40, 400, 520), (4, 1000, 256), (1, 2048, 136),
                                    (2, 900, 40), (8, 1024, 64), (620, 200, 40), (60, 200, 704),
-                                   (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72)])
+                                   (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72), (2, 512, 136), (2, 513, 24), (3, 2000, 72),
+                                   (200, 100, 264), (30, 128, 136), (30, 129, 136)])
 def test_every_way(B, T, D, gate, dtype):
     """Token by token, a cluster a chain, looking back in tiles of each length: the rules' borders."""
     lens = torch.randint(0, T + 1, (B,), generator=torch.Generator().manual_seed(B))

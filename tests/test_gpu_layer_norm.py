@@ -82,6 +82,24 @@ def test_a_mean_far_from_zero(D):
     check(z, eps=1e-3)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 264, 2048, 4096])
+def test_other_orders(D, dtype):
+    """Tokens further apart than sequences, and sequences that share tokens: the bits of contiguous inputs."""
+    g = torch.Generator().manual_seed(D)
+    line = torch.randn(2, 90, D, generator=g).to("cuda", dtype)
+    w, b = (torch.randn(D, generator=g).cuda() for _ in range(2))
+    for step in ((D, 3 * D, 1), (D, D, 1)):
+        x, do = (t.as_strided((3, 29, D), step, t.storage_offset()) for t in line)
+        lens = torch.tensor([29, 0, 11], device="cuda", dtype=torch.int32)
+        for n in (None, lens):
+            a = gated.prism_layer_norm(x, weight=w, bias=b, seq_lens=n)
+            assert torch.equal(a, gated.prism_layer_norm(x.contiguous(), weight=w, bias=b, seq_lens=n))
+            a = gated.prism_layer_norm_backward(x, do, weight=w, bias=b, seq_lens=n)
+            c = gated.prism_layer_norm_backward(x.contiguous(), do.contiguous(), weight=w, bias=b, seq_lens=n)
+            assert all(torch.equal(a[m], c[m]) for m in c)
+
+
 def test_rows_apart():
     """A row that is not finite leaves the others alone, and the sums of the weights are not finite."""
     z = make(1, 40, 64, "f32")
