@@ -10,13 +10,13 @@
 // sums a mean far from 0 would cost the variance its bits.  Up to a warp a row is joined by shuffles,
 // above it the CTA's warps join through shared memory.  Padding is not read.
 //
-// In bf16 an element is half the bytes for the same arithmetic, so wide rows in bf16 are bound by the latency
-// of their sums unless the next rows are on their way: they come through shared memory by bulk copies
+// In bf16 an element is half the bytes for the same arithmetic, so rows in bf16 are bound by the latency of their sums
+// unless the next rows are on their way: they come through shared memory by bulk copies
 // (layer_norm_columns_kernel), a thread holds as many rows and channels as its registers do, and the arithmetic
 // is packed.  Measured (GB300): 8 x 4096 tokens of 2048, bf16: 44 us forward (0.90 of the copy rate; 64 us with a warp
 // a row and scalar arithmetic, 52 us packed without the bulk copies), 72 us gradient (0.82, of it 6 us the sums' second
-// kernel; 112 us, 96 us).  Narrow rows, and fp32, do without: 0.92 and 0.95 of the copy rate at 32768 x 2048 forward and
-// 131072 x 512 gradient in fp32, where the bulk copies take 0.84 and 0.85.
+// kernel; 112 us, 96 us).  fp32 does without where its lanes are full: 0.96 of the copy rate at 32768 x 2048 forward, 0.95 at
+// 131072 x 512 gradient (inst_layer_norm.cu says which width goes how).
 #pragma once
 
 #include "gated.h"
@@ -411,43 +411,50 @@ __device__ __forceinline__ void norm_copy(const LayerNormArgs& p, long long firs
   if (dy) tc::bulk_g2s(dy + lane * p.D, static_cast<const E*>(p.dy) + at.b * p.ds[0] + at.t * p.ds[1], bytes, bar);
 }
 
-// Wide rows, both directions: the CTA holds R rows at once, a thread 8 V channels of each, so its weights
-// and the sums for dw and db stay in registers; the next rows come in by bulk copies meanwhile.
-template <class E, int NT, int V, int R, int S, bool BACK>
+// Wider rows, both directions: G threads hold R rows at once, a thread 8 V channels of each, so its weights
+// and the sums for dw and db stay in registers; the next rows come in by bulk copies meanwhile.  G is the whole CTA,
+// or a warp or a part of one: then every warp goes its own way, with copies and barriers of its own, and rows of
+// odd widths leave few lanes empty (bf16, 160 channels: 8 lanes of 24 channels a row 46 us, 16 of 16 64 us at 419430 rows;
+// gradient 83 us, a warp of 8 115 us).
+template <class E, int NT, int G, int V, int R, int S, bool BACK>
 struct NormColumns {
-  static constexpr int Dmax = 8 * NT * V, NI = BACK ? 2 : 1;
-  alignas(128) E tile[S][NI][R * Dmax];
-  alignas(16) float room[2][2][NT / 32][NI * R];
+  static_assert(G == NT || G <= 32, "a row is the CTA's, or a part of a warp's");
+  static constexpr int Dmax = 8 * G * V, NI = BACK ? 2 : 1, W = G <= 32 ? NT / 32 : 1, rows = NT / W / G * R;
+  alignas(128) E tile[S][NI][rows * Dmax];
+  alignas(16) float room[2][2][NT / 32 / W][NI * R];
   uint64_t full[S];
   unsigned live[S], failed;
 };
 
-template <class E, int NT, int V, int R, int S, int C, bool BACK>
+template <class E, int NT, int G, int V, int R, int S, int C, bool BACK>
 __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs p) {
-  using Shared = NormColumns<E, NT, V, R, S, BACK>;
-  constexpr int NW = NT / 32, NI = Shared::NI;
+  using Shared = NormColumns<E, NT, G, V, R, S, BACK>;
+  constexpr int W = Shared::W, NI = Shared::NI, RT = Shared::rows, NP = NT / W;      // NP: threads that share a tile
   extern __shared__ __align__(128) unsigned char raw_smem[];
-  Shared& sm = *reinterpret_cast<Shared*>(raw_smem);
-  const int warp = threadIdx.x >> 5;
-  const long long rows = (long long)p.B * p.T, tiles = (rows + R - 1) / R;
+  Shared* const all = reinterpret_cast<Shared*>(raw_smem);
+  const int warp = threadIdx.x >> 5, way = W > 1 ? warp : 0, me = threadIdx.x % NP;
+  Shared& sm = all[way];
+  const int u = me % G, mine = me / G * R;         // mine: the thread's first row in the tile
+  const bool feeds = me / 32 == NP / 32 - 1;
+  const long long rows = (long long)p.B * p.T, tiles = (rows + RT - 1) / RT, stride = (long long)gridDim.x * W;
   const float inv = 1.f / (float)p.D;
   auto fill = [&](long long n, int s) {
-    if (n < tiles) norm_copy<E, R>(p, n * R, sm.tile[s][0], BACK ? sm.tile[s][NI - 1] : nullptr, &sm.live[s], &sm.full[s]);
+    if (n < tiles) norm_copy<E, RT>(p, n * RT, sm.tile[s][0], BACK ? sm.tile[s][NI - 1] : nullptr, &sm.live[s], &sm.full[s]);
   };
-  if (threadIdx.x == 0) {
+  if (me == 0) {
 #pragma unroll
     for (int s = 0; s < S; ++s) tc::bar_init(&sm.full[s], 1);
     tc::bar_fence_init();
     sm.failed = 0;
   }
   __syncthreads();
-  long long n = blockIdx.x;
-  if (warp == NW - 1)
-    for (int s = 0; s < S; ++s) fill(n + (long long)s * gridDim.x, s);
+  long long n = (long long)blockIdx.x * W + way;
+  if (feeds)
+    for (int s = 0; s < S; ++s) fill(n + s * stride, s);
   uint64_t w[V][4], dw[V][4], db[V][4];            // db: the bias, forwards
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int ch = 8 * (threadIdx.x + NT * k);
+    const int ch = 8 * (u + G * k);
     eight_or(p.w && ch < p.D ? p.w + ch : nullptr, ch < p.D ? 1.f : 0.f, w[k]);
     eight_or(!BACK && p.b && ch < p.D ? p.b + ch : nullptr, 0.f, db[k]);
 #pragma unroll
@@ -456,9 +463,9 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
   __syncthreads();                                 // the first tiles' live rows
   int s = 0, turn = 0;
   unsigned parity = 0;
-  for (; n < tiles; n += gridDim.x, turn ^= 1) {
+  for (; n < tiles; n += stride, turn ^= 1) {
     if (!tc::bar_wait_long(&sm.full[s], parity)) sm.failed = 1;
-    const unsigned live = sm.live[s];
+    const unsigned live = sm.live[s] >> mine;
     uint64_t v[R][V][4], d[BACK ? R : 1][V][4];
     float sum[NI * R];                             // of x; of g
 #pragma unroll
@@ -466,15 +473,15 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       uint64_t t = both(0.f), g = both(0.f);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const int ch = 8 * (threadIdx.x + NT * k);
+        const int ch = 8 * (u + G * k);
         const bool on = ch < p.D && (live >> i & 1);
         Eight<E> f = Eight<E>();
-        if (on) f.lds(sm.tile[s][0] + i * p.D + ch);
+        if (on) f.lds(sm.tile[s][0] + (mine + i) * p.D + ch);
         f.get(v[i][k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) t = add2(t, v[i][k][j]);
         if constexpr (BACK) {
-          if (on) f.lds(sm.tile[s][1] + i * p.D + ch);
+          if (on) f.lds(sm.tile[s][1] + (mine + i) * p.D + ch);
           f.get(d[i][k]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) g = fma2(d[i][k][j], w[k][j], g);
@@ -483,17 +490,16 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       sum[i] = total(t);
       if constexpr (BACK) sum[R + i] = total(g);
     }
-    norm_sum<NT>(sum, sm.room[turn][0]);           // after it the tile is read by all
-    if (NT == 32) __syncwarp();                    // (a single warp sums without the CTA's barrier)
+    norm_sum<G>(sum, sm.room[turn][0]);            // after it the tile is read by all
+    if (NP == 32) __syncwarp();                    // (a warp sums without the CTA's barrier)
     if (sm.failed) {                               // a copy that never came: no other may outlive the CTA
-      if (threadIdx.x == 0) {
+      if (me == 0) {
         atomicOr(p.status, 1);
         for (int k = 0; k < S; ++k) tc::bar_wait_long(&sm.full[k], k < s ? parity ^ 1 : parity);
       }
-      __syncthreads();
-      return;
+      break;
     }
-    if (warp == NW - 1) fill(n + (long long)S * gridDim.x, s);
+    if (feeds) fill(n + S * stride, s);
     if (++s == S) {
       s = 0;
       parity ^= 1;
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       uint64_t t = both(0.f), g = both(0.f);
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (8 * (threadIdx.x + NT * k) < p.D)
+        if (8 * (u + G * k) < p.D)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             v[i][k][j] = add2(v[i][k][j], m);
@@ -515,11 +521,11 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       q[i] = total(t);
       if constexpr (BACK) q[R + i] = total(g);
     }
-    norm_sum<NT>(q, sm.room[turn][1]);
-    E* out = static_cast<E*>(p.out) + n * R * p.D + 8 * threadIdx.x;
+    norm_sum<G>(q, sm.room[turn][1]);
+    E* out = static_cast<E*>(p.out) + (n * RT + mine) * p.D + 8 * u;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (n * R + i >= rows) break;
+      if (n * RT + mine + i >= rows) break;
       const bool on = live >> i & 1;
       const float rstd = rsqrtf(fmaf(q[i], inv, p.eps));
       const uint64_t r = both(rstd);
@@ -530,7 +536,7 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       }
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        if (8 * (threadIdx.x + NT * k) >= p.D) continue;
+        if (8 * (u + G * k) >= p.D) continue;
         uint64_t y[4] = {};
         if (on) {
 #pragma unroll
@@ -545,19 +551,52 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
             }
           }
         }
-        Eight<E>::store(out + i * p.D + 8 * NT * k, y);
+        Eight<E>::store(out + i * p.D + 8 * G * k, y);
       }
     }
   }
   if (!BACK || (!p.dw && !p.db)) return;
   asm volatile("griddepcontrol.launch_dependents;\n");       // the sums' kernel may come up; it waits for this one's end
   float* to = p.partial + (long long)blockIdx.x * 2 * p.D;
+  if constexpr (G < 32) {                          // the warp's groups joined
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int ch = 8 * (threadIdx.x + NT * k);
-    if (ch >= p.D) continue;
-    Eight<float>::store(to + ch, dw[k]);
-    Eight<float>::store(to + p.D + ch, db[k]);
+    for (int o = G; o < 32; o *= 2)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dw[k][j] = add2(dw[k][j], __shfl_xor_sync(0xffffffffu, dw[k][j], o));
+          db[k][j] = add2(db[k][j], __shfl_xor_sync(0xffffffffu, db[k][j], o));
+        }
+  }
+  if constexpr (G <= 32) {                         // the CTA's warps joined, in order
+    static_assert(sizeof(sm.tile) >= 2 * Shared::Dmax * sizeof(float), "a warp's sums take the place of its tiles");
+    constexpr int Dmax = Shared::Dmax;
+    float* own = reinterpret_cast<float*>(sm.tile);
+    __syncwarp();
+    if (me < G)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (8 * (u + G * k) < p.D) {
+          Eight<float>::store(own + 8 * (u + G * k), dw[k]);
+          Eight<float>::store(own + Dmax + 8 * (u + G * k), db[k]);
+        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.D; c += NT) {
+      const int at = c < p.D ? c : c - p.D + Dmax;
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) t += reinterpret_cast<const float*>(all[w].tile)[at];
+      to[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int ch = 8 * (u + G * k);
+      if (ch >= p.D) continue;
+      Eight<float>::store(to + ch, dw[k]);
+      Eight<float>::store(to + p.D + ch, db[k]);
+    }
   }
 }
 

@@ -39,14 +39,19 @@ def check(z, c=None, lens=None, eps=1e-5):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("D", [8, 16, 32, 40, 64, 72, 128, 200, 256, 264, 512, 520, 1000, 1024, 2048, 2056, 4096, 5000, 8192, 8200, 16384])
+@pytest.mark.parametrize("D", [8, 16, 32, 40, 64, 72, 96, 104, 128, 136, 160, 168, 192, 200, 256, 264, 304, 312, 384, 392, 512, 520, 640, 648, 768,
+                               776, 832, 840, 1000, 1024, 1032, 1280, 1288, 1536, 1544, 2048, 2056, 2560, 2568, 4096, 4104, 5000,
+                               6144, 6152, 8192, 8200, 16384])
 def test_widths(D, dtype):
     """Every variant's largest width and the one behind it."""
     check(make(3, 7, D, dtype))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B,T,D", [(1, 1, 8), (1, 1, 2048), (40, 500, 64), (5, 700, 1000), (1, 3001, 520), (700, 3, 24)])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 8), (1, 1, 2048), (40, 500, 64), (5, 700, 1000), (1, 3001, 520), (700, 3, 24),
+                                   (1, 20000, 32), (3, 6001, 64), (1, 9000, 96), (1, 9000, 128), (2, 4001, 160), (1, 8000, 192), (1, 6000, 256),
+                                   (1, 4000, 288), (1, 4000, 384), (5, 800, 512), (3, 901, 768), (1, 2000, 800), (1, 1500, 1280), (1, 1100, 2560),
+                                   (1, 700, 6144)])
 def test_rows(B, T, D, dtype):
     check(make(B, T, D, dtype))
     check(make(B, T, D, dtype, weights=False))
