@@ -48,9 +48,12 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //                        10.1); it has no room for two CTAs of 128 tokens in the gradient, which looks back from
 //                        513 tokens on (2 x 2000 x 128: 8.4 us, 128 x 32 13.0)
 //           One tile needs no cluster, only the way through shared memory.  The gradient goes by 64 x 32 up to 64 tokens
-//           (100 x 60 x 256: 7.2 us, 64 x 64 8.5; but fp32 with both gates 10.9 and 9.9) and by 128 x 32 up to 128 while chains are few
-//           (100 x 100 x 256: 12.5 us, looking back 14.1; 300 x 100 x 256: 34 and 29.5), as fp32 with one gate does forwards
-//           (100 x 100 x 256: 7.6 us, 64 x 64 9.2).
+//           (100 x 60 x 256: 7.2 us, 64 x 64 8.5; but fp32 with both gates 10.9 and 9.9) and by 128 x 32 up to 128 while
+//           chains are few (100 x 100 x 256: 12.5 us, looking back 14.1; 300 x 100 x 256: 34 and 29.5), as fp32 with one
+//           gate does forwards (100 x 100 x 256: 7.6 us, 64 x 64 9.2).  Forwards 256 x 32 up to 256 tokens while chains are
+//           few, and fewer where a quarter of it would be padding (both gates, 512 x 200 x 64: 12.2 us, two of 128 in a cluster
+//           14.9, looking back 13.7; 225 x 250 x 256 32.1, looking back 25.3; 450 x 150 x 64 12.3 and 11.5; one gate, 46 x 230 x
+//           1160 17.7 and 18.7; fp32 128 x 200 x 64 8.0 and 10.2, 512 x 200 x 64 27.5 and 23.9).
 constexpr int kGatedCluster = 16;
 struct GatedPlan {
   int tile, cols;
@@ -69,6 +72,7 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
     }
     if (T <= 512 && fits(64, 2)) return {64, 32, true};
     if (T > 512 && fits(128, 1)) return {128, 32, true};
+    if (T <= 256 && chains <= 304) return {256, 32, true};
     return {chains > 76 ? 64 : 128, 32, false};
   }
   if (backward) {
@@ -83,8 +87,10 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
   if (dtype == 0) {
     if (T <= 128) return {128, 32, true};
     if (T <= 512 && fits(64, 2)) return {64, 64, true};
+    if (T <= 256 && chains <= 304) return {256, 32, true};
     return {128, 32, T > 512 && fits(128, 1)};
   }
+  if (T > 128 && T <= 256 && chains <= (T > 192 ? 304 : 152) * (gated ? 2 : 3)) return {256, 32, true};
   if (fits(128, 2)) return {128, T > 512 && T <= 1024 ? 32 : 64, true};
   if (D <= 32) return {128, 32, false};
   if (gated) return {chains >= 256 ? 64 : 128, 64, false};

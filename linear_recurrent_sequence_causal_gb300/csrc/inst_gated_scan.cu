@@ -60,6 +60,7 @@ cudaError_t launch_forward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s)
     constexpr int S = GATED ? 1 : 2;
     if (plan.cluster) {
       if (t == 64) return launch_forward<E, GATED, 64, 64, 16, 1, 4, true>(a, plan, s);
+      if (t == 256) return launch_forward<E, GATED, 32, 256, 16, S, 2, true>(a, plan, s);
       if (c == 32) return launch_forward<E, GATED, 32, 128, 16, 1, 4, true>(a, plan, s);
       return launch_forward<E, GATED, 64, 128, 16, S, 2, true>(a, plan, s);
     }
@@ -72,6 +73,7 @@ cudaError_t launch_forward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s)
   } else if constexpr (GATED) {
     if (plan.cluster) {
       if (t == 64) return launch_forward<E, true, 32, 64, 8, 1, 4, true>(a, plan, s);
+      if (t == 256) return launch_forward<E, true, 32, 256, 8, 1, 1, true>(a, plan, s);
       return launch_forward<E, true, 32, 128, 16, 1, 2, true>(a, plan, s);
     }
     if (t == 64) return launch_forward<E, true, 32, 64, 8, 2, 3, false>(a, plan, s);
@@ -79,6 +81,7 @@ cudaError_t launch_forward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s)
   } else {
     if (plan.cluster) {
       if (t == 64) return launch_forward<E, false, 64, 64, 16, 1, 3, true>(a, plan, s);
+      if (t == 256) return launch_forward<E, false, 32, 256, 8, 1, 1, true>(a, plan, s);
       return launch_forward<E, false, 32, 128, 16, 1, 3, true>(a, plan, s);
     }
     return launch_forward<E, false, 32, 128, 16, 1, 3, false>(a, plan, s);

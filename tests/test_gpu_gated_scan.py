@@ -155,7 +155,8 @@ def test_many_tiles_and_sequences(dtype):
 @pytest.mark.parametrize("B,T,D", [(2000, 4, 40), (1100, 20, 40), (1300, 130, 24), (300, 64, 136), (300, 65, 136), (40, 400, 520), (4, 1000, 256), (1, 2048, 136),
                                    (2, 900, 40), (8, 1024, 64), (620, 200, 40), (60, 200, 704),
                                    (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72), (2, 512, 136), (2, 513, 24), (3, 2000, 72),
-                                   (200, 100, 264), (30, 128, 136), (30, 129, 136)])
+                                   (200, 100, 264), (30, 128, 136), (30, 129, 136), (130, 250, 72), (300, 150, 64), (20, 256, 264),
+                                   (460, 192, 40), (460, 193, 40)])
 def test_every_way(B, T, D, gate, dtype):
     """Token by token, a cluster a chain, looking back in tiles of each length: the rules' borders."""
     lens = torch.randint(0, T + 1, (B,), generator=torch.Generator().manual_seed(B))
