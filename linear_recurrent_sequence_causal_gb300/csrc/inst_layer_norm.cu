@@ -71,13 +71,14 @@ cudaError_t norm_columns(const LayerNormArgs& a, cudaStream_t s, size_t* count =
 //  forward   64 channels: 4 lanes 45, 8 lanes 49; 96: 4 lanes by bulk copies 47, 16 lanes 70; 128: 8 lanes 47, 16 lanes 55;
 //            200: 49 by bulk copies, 55; 320: 16 lanes 46, a warp 56; 640: 24 channels a lane 47, 32 64; 1280: 64 threads 46,
 //            128 53; 2560: 160 threads 48, 256 51.  fp32, without bulk copies: 400: 32 lanes 81, 64 87; 1024: 64 threads
-//            82, 128 92; 2048: 128 threads 82, 256 86; 264: 16 lanes 86, 64 104
+//            82, 128 92; 2048: 128 threads 82, 256 86; 264: 16 lanes 86, 64 104; 2320: 32 channels a thread 95, 16 by bulk
+//            copies 105; 8192: 90 and 106
 //  gradient  24: by bulk copies 90, without 100; 40: 4 lanes 104, 8 lanes without 126; 96: 72 and 105; 128: 70 and 81;
 //            160: 8 lanes 82, a warp 115; 256: 16 lanes 69, a warp 78; 320: 84 and 101; 768: 24 channels a lane 72, 32 77;
 //            1280: 64 threads 79, 128 101; 2560: 160 threads 85, 256 105; 5000: 384 threads 95, 512 119.  fp32 does
 //            without bulk copies where its lanes are full (192: 129, with them 144; 512: 123 and 123; 1024: 125 and
 //            134), and takes them where they are not (136: 128, without 150; 264: 132 and 170; 384: 123 and 134; 520: 129 and
-//            188; 768: 124 and 136; 1032: 96 threads 125, 128 169)
+//            188; 768: 124 and 136; 1032: 96 threads 125, 128 169; 2320: 160 threads 134, 256 154)
 template <class E>
 cudaError_t forward_e(const LayerNormArgs& a, cudaStream_t s) {
   const int D = a.D;
@@ -105,9 +106,9 @@ cudaError_t forward_e(const LayerNormArgs& a, cudaStream_t s) {
     if (D <= 512) return norm_forward<E, 32, 2, 2, 4>(a, s);
     if (D <= 1024) return norm_forward<E, 64, 2, 2, 4>(a, s);
     if (D <= 2048) return norm_forward<E, 128, 2, 2, 4>(a, s);
-    if (D <= 4096) return norm_columns<E, 256, 256, 2, 2, 3, 2, false>(a, s);
-    if (D <= 8192) return norm_columns<E, 512, 512, 2, 2, 3, 1, false>(a, s);
-    return norm_columns<E, 512, 512, 4, 1, 3, 1, false>(a, s);
+    if (D <= 4096) return norm_forward<E, 128, 4, 1, 4>(a, s);
+    if (D <= 8192) return norm_forward<E, 256, 4, 1, 3>(a, s);
+    return norm_forward<E, 512, 4, 1, 2>(a, s);
   }
 }
 
@@ -146,6 +147,7 @@ cudaError_t backward_e(const LayerNormArgs& a, cudaStream_t s, size_t* count = n
     if (D <= 1024) return norm_backward<E, 128, 1, 2, 2, true>(a, s, count);
     if (D <= 1280) return norm_columns<E, 96, 96, 2, 2, 3, 3, true>(a, s, count);
     if (D <= 2048) return norm_columns<E, 128, 128, 2, 2, 3, 2, true>(a, s, count);
+    if (D <= 2560) return norm_columns<E, 160, 160, 2, 2, 2, 2, true>(a, s, count);
     if (D <= 4096) return norm_columns<E, 256, 256, 2, 1, 3, 2, true>(a, s, count);
     if (D <= 8192) return norm_columns<E, 512, 512, 2, 1, 3, 1, true>(a, s, count);
     return norm_columns<E, 512, 512, 4, 1, 1, 1, true>(a, s, count);

@@ -122,6 +122,7 @@ __device__ __forceinline__ void norm_sum(float (&v)[N], float (*room)[N]) {
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   } else {
+    static_assert(N <= 32 && (N & (N - 1)) == 0, "halved until each lane has one");
     const int lane = threadIdx.x & 31;
     int bit = 16;
 #pragma unroll
