@@ -58,7 +58,7 @@ def test_rows(B, T, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("D", [64, 1000, 4096])
+@pytest.mark.parametrize("D", [24, 64, 96, 160, 320, 768, 1000, 1280, 2320, 4096])
 def test_ragged_and_strided(D, dtype):
     z = make(5, 9, D, dtype)
     lens = torch.tensor([0, 9, 1, 12, 4])
@@ -75,6 +75,14 @@ def test_ragged_and_strided(D, dtype):
     none = torch.zeros(5, dtype=torch.int64)
     y, g = check(z, lens=none)
     assert (g["weight"] == 0).all() and (g["bias"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [16, 32, 64, 96, 128, 152, 192, 256, 288, 384, 512, 640, 1024])
+def test_many_ragged_rows(D, dtype):
+    """Every warp of a CTA goes over rows of its own, padding among them."""
+    lens = torch.randint(0, 71, (60,), generator=torch.Generator().manual_seed(D))
+    check(make(60, 70, D, dtype), lens=lens)
 
 
 @pytest.mark.parametrize("D", [64, 2048, 4096])
