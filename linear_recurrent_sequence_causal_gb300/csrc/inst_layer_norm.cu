@@ -75,7 +75,7 @@ cudaError_t norm_columns(const LayerNormArgs& a, cudaStream_t s, size_t* count =
 //            copies 105; 8192: 90 and 106
 //  gradient  24: by bulk copies 90, without 100; 40: 4 lanes 104, 8 lanes without 126; 96: 72 and 105; 128: 70 and 81;
 //            160: 8 lanes 82, a warp 115; 256: 16 lanes 69, a warp 78; 320: 84 and 101; 768: 24 channels a lane 72, 32 77;
-//            1280: 64 threads 79, 128 101; 2560: 160 threads 85, 256 105; 5000: 384 threads 95, 512 119.  fp32 does
+//            1280: 64 threads 79, 128 101; 2560: 160 threads 85, 256 105; 4096: 4 rows a thread 80, 2 84; 5000: 384 threads 95, 512 119.  fp32 does
 //            without bulk copies where its lanes are full (192: 129, with them 144; 512: 123 and 123; 1024: 125 and
 //            134), and takes them where they are not (136: 128, without 150; 264: 132 and 170; 384: 123 and 134; 520: 129 and
 //            188; 768: 124 and 136; 1032: 96 threads 125, 128 169; 2320: 160 threads 134, 256 154)
@@ -129,7 +129,7 @@ cudaError_t backward_e(const LayerNormArgs& a, cudaStream_t s, size_t* count = n
     if (D <= 1536) return norm_columns<E, 64, 64, 3, 2, 2, 4, true>(a, s, count);
     if (D <= 2048) return norm_columns<E, 128, 128, 2, 4, 2, 2, true>(a, s, count);
     if (D <= 2560) return norm_columns<E, 160, 160, 2, 2, 2, 3, true>(a, s, count);
-    if (D <= 4096) return norm_columns<E, 256, 256, 2, 2, 2, 2, true>(a, s, count);
+    if (D <= 4096) return norm_columns<E, 256, 256, 2, 4, 2, 1, true>(a, s, count);
     if (D <= 6144) return norm_columns<E, 384, 384, 2, 2, 2, 1, true>(a, s, count);
     if (D <= 8192) return norm_columns<E, 512, 512, 2, 2, 2, 1, true>(a, s, count);
     return norm_columns<E, 512, 512, 4, 1, 2, 1, true>(a, s, count);
