@@ -13,18 +13,19 @@ struct GatedDecodeArgs;
 struct LayerNormArgs;
 
 constexpr int kGatedChunk = 64;          // tokens from one row of states to the next
-// Short sequences go token by token, a thread two channels: up to 8 tokens always (2 x 2 x 240 bf16: 1.8 us,
-// 3.0 in tiles), up to 32 where there are threads enough (36 x 15 x 1256 bf16: 4.0 us, 8.4 in tiles; but
-// 2 x 23 x 48 fp32 gradient: 8.6 us, 4.4 in tiles).
+// Short sequences go token by token: up to 8 tokens always (2 x 2 x 240 bf16: 1.8 us, 3.0 in tiles), forwards up to 32 where
+// there are threads enough (36 x 15 x 1256 bf16: 4.0 us, 8.4 in tiles of 64).
 constexpr int kGatedShort = 32;
-constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGatedShort && (long long)B * D >= 1 << 15); }
+constexpr bool gated_is_short(bool backward, int B, int T, int D) {
+  return T <= 8 || (!backward && T <= kGatedShort && (long long)B * D >= 1 << 15);
+}
 
 // How a call's chains of tiles go (times: GB300, bf16 unless said otherwise).
-//  tile     tokens of a tile, whole chunks.  An SM's shared memory and registers hold half as many tiles of twice the
-//           length, which halves what a chain hands on but leaves less beside each other.  With an input gate 64 where
-//           there are chains for all CTAs (64 x 512 x 2048: 94 us, in tiles of 128 101), 128 where few chains are
-//           long (1 x 65536 x 256: 51 us, of 64 80).  Without one 64 where every CTA has a chain of its own (24 x 934 x
-//           5584: 133 us, of 128 154), else 128 (8 x 4096 x 2048: 72 us, of 64 81), and 256 where half of the SMs have
+//  tile     tokens of a tile, whole chunks where a chain has more than one.  An SM's shared memory and registers hold half as
+//           many tiles of twice the length, which halves what a chain hands on but leaves less beside each other.  With an
+//           input gate 64 where there are chains for all CTAs (64 x 512 x 2048: 94 us, in tiles of 128 101), 128 where few
+//           chains are long (1 x 65536 x 256: 51 us, of 64 80).  Without one 64 where every CTA has a chain of its own (24 x
+//           934 x 5584: 133 us, of 128 154), else 128 (8 x 4096 x 2048: 72 us, of 64 81), and 256 where half of the SMs have
 //           none and there are tiles enough (1 x 65536 x 4096: 293 us, of 128 318; but 22 x 876 x 144: 11.5 us, of 128
 //           10.1).
 //  cols     channels of a tile: 64, or 32 with twice the tokens for layers that are not wider (133 x 1677 x 24: 19 us and 28;
@@ -47,7 +48,8 @@ constexpr bool gated_is_short(int B, int T, int D) { return T <= 8 || (T <= kGat
 //             64 x 32    fp32 with both gates up to 512 (100 x 100 x 256: 11.5 us, 64 x 64 16.0; gradient 4 x 500 x 256: 5.7 and
 //                        10.1); it has no room for two CTAs of 128 tokens in the gradient, which looks back from
 //                        513 tokens on (2 x 2000 x 128: 8.4 us, 128 x 32 13.0)
-//           One tile needs no cluster, only the way through shared memory.  The gradient goes by 64 x 32 up to 64 tokens
+//           One tile needs no cluster, only the way through shared memory.  The gradient goes by 16 x 64 up to 16 tokens (381 x 12 x
+//           6696: 115 us, 32 x 64 187) and 32 x 64 up to 32 (400 x 30 x 2048: 77 us, 64 x 32 171), by 64 x 32 up to 64 tokens
 //           (100 x 60 x 256: 7.2 us, 64 x 64 8.5; but fp32 with both gates 10.9 and 9.9) and by 128 x 32 up to 128 while
 //           chains are few (100 x 100 x 256: 12.5 us, looking back 14.1; 300 x 100 x 256: 34 and 29.5), as fp32 with one
 //           gate does forwards (100 x 100 x 256: 7.6 us, 64 x 64 9.2).  Forwards 256 x 32 up to 256 tokens while chains are
@@ -65,6 +67,7 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
     const long long n = ((long long)T + tile - 1) / tile;
     return n == 1 || (n <= kGatedCluster && chains * n <= 152ll * ctas * (n == 2 ? 4 : 1));
   };
+  if (backward && T <= 32) return {T <= 16 ? 16 : 32, 64, true};
   if (dtype == 0 && gated) {
     if (backward) {
       if (T <= 64) return {64, 64, true};

@@ -75,13 +75,13 @@ int check_gated(const prism_gated_dims* d, unsigned flags) {
 
 // The counter, then 16 bytes of (P, L) and 8 of h a lane and tile; nothing where no tile looks back.
 constexpr size_t kCounter = 256;
-size_t gated_bytes(const prism_gated_dims* d, prism::GatedPlan plan) {
-  if (plan.cluster || prism::gated_is_short(d->B, d->T, d->D)) return 0;
+size_t gated_bytes(const prism_gated_dims* d, bool backward, prism::GatedPlan plan) {
+  if (plan.cluster || prism::gated_is_short(backward, d->B, d->T, d->D)) return 0;
   return kCounter + (size_t)tiles_of(d, plan.tile, plan.cols) * 32 * 24;
 }
 // with or without an input gate
 size_t gated_bytes(const prism_gated_dims* d, bool backward) {
-  const size_t a = gated_bytes(d, plan_of(d, backward, true)), b = gated_bytes(d, plan_of(d, backward, false));
+  const size_t a = gated_bytes(d, backward, plan_of(d, backward, true)), b = gated_bytes(d, backward, plan_of(d, backward, false));
   return a > b ? a : b;
 }
 
@@ -144,11 +144,11 @@ int run_gated(const prism_gated_dims* d, bool backward, const GatedCall& c, void
   }
   const bool gated = c.in[backward ? 3 : 2] != nullptr;
   const prism::GatedPlan plan = plan_of(d, backward, gated);
-  const size_t need = gated_bytes(d, plan);
+  const size_t need = gated_bytes(d, backward, plan);
   if (workspace && !aligned(workspace, 256)) return PRISM_ERR_MISALIGNED;
   if (need && (!workspace || workspace_bytes < need)) return PRISM_ERR_WORKSPACE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (prism::gated_is_short(d->B, d->T, d->D)) return run_short(d, backward, c, step, s);
+  if (prism::gated_is_short(backward, d->B, d->T, d->D)) return run_short(d, backward, c, step, s);
   prism::GatedArgs a = prism::GatedArgs();
   a.s_in = c.s_in; a.s_out = c.s_out; a.states = c.states;
   a.lens = c.lens;

@@ -34,6 +34,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "gated.h"
 #include "prism_common.cuh"
 #include "tc_common.cuh"
@@ -352,12 +354,14 @@ template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
 struct GatedShared {
   static constexpr int NW = kGatedThreads<CW, TT, R> / 32;
   static constexpr bool BACK = NI > 2 && NO > 1;
+  static constexpr int chain = TT < kGatedChunk ? 1 : kGatedCluster;       // tiles of a cluster
+  struct Nothing {};
   alignas(128) E tile[S][NI][TT][CW];
   alignas(128) E out[NO][TT][CW];
   ulonglong2 part[2][NW][32];                      // (P, L) of a warp's tokens, then of those before them: both channels of P, of L
   union {
-    GatedFar<(NW < 8 ? NW : 8)> far;
-    ulonglong2 ahead[CL ? 2 : 1][kGatedCluster][32];       // CL: (P, L) of the chain's tiles, by rank
+    std::conditional_t<CL, Nothing, GatedFar<(NW < 8 ? NW : 8)>> far;
+    ulonglong2 ahead[CL ? 2 : 1][CL ? chain : 1][32];      // CL: (P, L) of the chain's tiles, by rank
   };
   int found;                                       // the state came by look_near
   uint64_t carry[32];                              // what reaches the tile
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
 // 1 - w, x, dout, h: 250 registers at 16 tokens); recomputing the gates instead would fill the SM's exponential unit.
 template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
 __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
-  static_assert(TT % kGatedChunk == 0, "a tile starts at a row of states");
+  static_assert(TT % kGatedChunk == 0 || (CL && TT < kGatedChunk), "a tile starts at a row of states, or is the only one");
   constexpr int NW = kGatedThreads<CW, TT, R> / 32, H = 64 / CW, NI = GATED ? 4 : 3, NO = GATED ? 3 : 2;
   using Shared = GatedShared<E, NI, NO, CW, TT, R, S, CL>;
   extern __shared__ __align__(128) unsigned char raw[];
@@ -828,9 +832,10 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
   }
 }
 
-// Short sequences, up to kGatedShort tokens: a thread takes two channels of one sequence from token to token,
+// Short sequences, up to kGatedShort tokens: a thread takes 2 P channels of one sequence from token to token,
 // and nothing waits for anything.  (A tile of 64 tokens would be mostly padding: 512 sequences of 4
-// tokens, 1512 channels, fp32, took 47 us in tiles.)
+// tokens, 1512 channels, fp32, took 47 us in tiles.)  P = 2 where there are threads enough: 1000 x 8 x 4096 bf16 66 us,
+// 82 with P = 1; 8 x 4 x 2048 2.5 and 2.4.
 struct GatedShortArgs {
   const void *x, *f, *i, *dy;                      // i null: w = 1 - a
   long long xs[2], fs[2], is[2], ds[2];            // strides: sequence, token (elements)
@@ -842,28 +847,76 @@ struct GatedShortArgs {
 };
 constexpr int kGatedShortThreads = 128, kGatedAhead = 8;   // tokens whose loads are in flight together
 
-struct GatedShortPlace {
-  int b, ch, len;
-  __device__ __forceinline__ GatedShortPlace(const GatedShortArgs& p, long long n) {
-    b = (int)(n / (p.D / 2));
-    ch = 2 * (int)(n - (long long)b * (p.D / 2));
-    len = b < p.B ? p.lens ? min(max(__ldg(p.lens + b), 0), p.T) : p.T : 0;
+// 2 P neighbouring channels, as Two.
+template <class E, int P> struct Some {
+  Two<E> r[P];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (P == 1) {
+      r[0].load(p);
+    } else if constexpr (sizeof(E) == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      r[0].r = make_float2(v.x, v.y);
+      r[1].r = make_float2(v.z, v.w);
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      r[0].r = v.x;
+      r[1].r = v.y;
+    }
+  }
+  __device__ __forceinline__ uint64_t get(int k) const { return r[k].get(); }
+  static __device__ __forceinline__ void store(E* p, const uint64_t (&v)[P]) {
+    if constexpr (P == 1) {
+      Two<E>::store(p, v[0]);
+    } else if constexpr (sizeof(E) == 4) {
+      float4 f;
+      unpack2(v[0], f.x, f.y);
+      unpack2(v[1], f.z, f.w);
+      *reinterpret_cast<float4*>(p) = f;
+    } else {
+      float a, b, c, d;
+      unpack2(v[0], a, b);
+      unpack2(v[1], c, d);
+      const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(a, b), __floats2bfloat162_rn(c, d)};
+      uint2 u;
+      memcpy(&u, h, 8);
+      *reinterpret_cast<uint2*>(p) = u;
+    }
   }
 };
 
-template <class E, bool GATED>
+template <int P>
+struct GatedShortPlace {
+  int b, ch, len;
+  __device__ __forceinline__ GatedShortPlace(const GatedShortArgs& p, long long n) {
+    const int per = p.D / (2 * P);
+    b = (int)(n / per);
+    ch = 2 * P * (int)(n - (long long)b * per);
+    len = b < p.B ? p.lens ? min(max(__ldg(p.lens + b), 0), p.T) : p.T : 0;
+  }
+};
+template <int P>
+__device__ __forceinline__ void state_or_none(const float* p, uint64_t (&h)[P]) {
+  Some<float, P> v;
+  if (p) v.load(p);
+#pragma unroll
+  for (int k = 0; k < P; ++k) h[k] = p ? v.get(k) : both(0.f);
+}
+
+template <class E, bool GATED, int P>
 __global__ void __launch_bounds__(kGatedShortThreads) gated_short_kernel(GatedShortArgs p) {
-  const GatedShortPlace at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
+  const GatedShortPlace<P> at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
   if (at.b >= p.B) return;
   const E* x = static_cast<const E*>(p.x) + at.b * p.xs[0] + at.ch;
   const E* f = static_cast<const E*>(p.f) + at.b * p.fs[0] + at.ch;
   const E* i = GATED ? static_cast<const E*>(p.i) + at.b * p.is[0] + at.ch : nullptr;
   E* out = static_cast<E*>(p.out) + (long long)at.b * p.T * p.D + at.ch;
   const long long row = (long long)at.b * p.D + at.ch;
-  uint64_t h = p.s_in ? load_pair(p.s_in + row) : both(0.f);
-  if (p.states && at.len > 0) Two<float>::store(p.states + row, h);    // T <= 64: one row a sequence
+  uint64_t h[P], none[P];
+  state_or_none<P>(p.s_in ? p.s_in + row : nullptr, h);
+  state_or_none<P>(nullptr, none);
+  if (p.states && at.len > 0) Some<float, P>::store(p.states + row, h);    // T <= 64: one row a sequence
   for (int t0 = 0; t0 < p.T; t0 += kGatedAhead) {
-    Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead];
+    Some<E, P> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead];
 #pragma unroll
     for (int j = 0; j < kGatedAhead; ++j)
       if (t0 + j < at.len) {
@@ -874,21 +927,28 @@ __global__ void __launch_bounds__(kGatedShortThreads) gated_short_kernel(GatedSh
 #pragma unroll
     for (int j = 0; j < kGatedAhead; ++j)
       if (t0 + j < p.T) {
-        if (t0 + j < at.len) {
-          const Gate g = gate_of<E>(rf[j].get());
-          h = fma2(g.s, h, mul2(GATED ? sigmoid_of<E>(ri[j].get()) : g.c, rx[j].get()));
-        }
-        Two<E>::store(out + (long long)(t0 + j) * p.D, t0 + j < at.len ? h : both(0.f));
+        const bool there = t0 + j < at.len;
+        if (there)
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const Gate g = gate_of<E>(rf[j].get(k));
+            h[k] = fma2(g.s, h[k], mul2(GATED ? sigmoid_of<E>(ri[j].get(k)) : g.c, rx[j].get(k)));
+          }
+        E* to = out + (long long)(t0 + j) * p.D;
+        if (there) Some<E, P>::store(to, h);
+        else Some<E, P>::store(to, none);
       }
   }
-  if (p.s_out) Two<float>::store(p.s_out + row, h);
+  if (p.s_out) Some<float, P>::store(p.s_out + row, h);
 }
 
-// Gradient of up to N tokens: forwards for the states before every token, which stay in registers, then
-// backwards.  Where all tokens' loads are in flight together (N = kGatedAhead) nothing is read twice.
-template <class E, bool GATED, int N>
+// Gradient of up to kGatedAhead tokens, two channels a thread: forwards for the states before every token, which stay in
+// registers like the inputs, then backwards.  (More channels a thread leave less beside each other: 1000 x 8 x 4096 bf16
+// 102 us, four channels 104.  Longer sequences go in tiles of 16 and 32 tokens: 381 x 12 x 6696 bf16 115 us, 200 when they came
+// through here in blocks.)
+template <class E, bool GATED>
 __global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kernel(GatedShortArgs p) {
-  const GatedShortPlace at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
+  const GatedShortPlace<1> at(p, (long long)blockIdx.x * kGatedShortThreads + threadIdx.x);
   if (at.b >= p.B) return;
   const E* x = static_cast<const E*>(p.x) + at.b * p.xs[0] + at.ch;
   const E* f = static_cast<const E*>(p.f) + at.b * p.fs[0] + at.ch;
@@ -898,58 +958,46 @@ __global__ void __launch_bounds__(kGatedShortThreads) gated_short_backward_kerne
   E *dx = static_cast<E*>(p.out) + o, *df = static_cast<E*>(p.df) + o, *di = GATED ? static_cast<E*>(p.di) + o : nullptr;
   const uint64_t none = both(0.f), minus = both(-1.f);
   Two<E> rx[kGatedAhead], rf[kGatedAhead], ri[kGatedAhead], rd[kGatedAhead];
-  auto load = [&](int t0, bool with_d) {
+  uint64_t h = at.len > 0 ? load_pair(p.states + row) : none, before[kGatedAhead];
 #pragma unroll
-    for (int j = 0; j < kGatedAhead; ++j)
-      if (t0 + j < at.len) {
-        rx[j].load(x + (t0 + j) * p.xs[1]);
-        rf[j].load(f + (t0 + j) * p.fs[1]);
-        if (GATED) ri[j].load(i + (t0 + j) * p.is[1]);
-        if (with_d) rd[j].load(d + (t0 + j) * p.ds[1]);
-      }
-  };
-  uint64_t h = at.len > 0 ? load_pair(p.states + row) : none, before[N];
+  for (int j = 0; j < kGatedAhead; ++j)
+    if (j < at.len) {
+      rx[j].load(x + j * p.xs[1]);
+      rf[j].load(f + j * p.fs[1]);
+      if (GATED) ri[j].load(i + j * p.is[1]);
+      rd[j].load(d + j * p.ds[1]);
+    }
 #pragma unroll
-  for (int t0 = 0; t0 < N; t0 += kGatedAhead) {
-    if (t0 >= at.len) break;
-    load(t0, N == kGatedAhead);
-#pragma unroll
-    for (int j = 0; j < kGatedAhead; ++j) {
-      before[t0 + j] = h;
-      if (t0 + j < at.len) {
-        const Gate g = gate_of<E>(rf[j].get());
-        h = fma2(g.s, h, mul2(GATED ? sigmoid_of<E>(ri[j].get()) : g.c, rx[j].get()));
-      }
+  for (int j = 0; j < kGatedAhead; ++j) {
+    before[j] = h;
+    if (j < at.len) {
+      const Gate g = gate_of<E>(rf[j].get());
+      h = fma2(g.s, h, mul2(GATED ? sigmoid_of<E>(ri[j].get()) : g.c, rx[j].get()));
     }
   }
   uint64_t r = p.s_in ? load_pair(p.s_in + row) : none;
 #pragma unroll
-  for (int t0 = N - kGatedAhead; t0 >= 0; t0 -= kGatedAhead) {
-    if (t0 >= p.T) continue;
-    if (N > kGatedAhead) load(t0, true);
-#pragma unroll
-    for (int j = kGatedAhead - 1; j >= 0; --j) {
-      if (t0 + j >= p.T) continue;
-      const long long to = (long long)(t0 + j) * p.D;
-      uint64_t gx = none, gf = none, gi = none;
-      if (t0 + j < at.len) {
-        const Gate g = gate_of<E>(rf[j].get());
-        const uint64_t xj = rx[j].get(), G = add2(rd[j].get(), r);
-        r = mul2(g.s, G);
-        if constexpr (GATED) {
-          const Gate w = gate_of<E>(ri[j].get());
-          gx = mul2(G, w.s);
-          gf = mul2(mul2(r, g.c), before[t0 + j]);
-          gi = mul2(mul2(gx, w.c), xj);
-        } else {
-          gx = mul2(G, g.c);
-          gf = mul2(mul2(r, g.c), fma2(xj, minus, before[t0 + j]));
-        }
+  for (int j = kGatedAhead - 1; j >= 0; --j) {
+    if (j >= p.T) continue;
+    const long long to = (long long)j * p.D;
+    uint64_t gx = none, gf = none, gi = none;
+    if (j < at.len) {
+      const Gate g = gate_of<E>(rf[j].get());
+      const uint64_t xj = rx[j].get(), G = add2(rd[j].get(), r);
+      r = mul2(g.s, G);
+      if constexpr (GATED) {
+        const Gate w = gate_of<E>(ri[j].get());
+        gx = mul2(G, w.s);
+        gf = mul2(mul2(r, g.c), before[j]);
+        gi = mul2(mul2(gx, w.c), xj);
+      } else {
+        gx = mul2(G, g.c);
+        gf = mul2(mul2(r, g.c), fma2(xj, minus, before[j]));
       }
-      Two<E>::store(dx + to, gx);
-      Two<E>::store(df + to, gf);
-      if (GATED) Two<E>::store(di + to, gi);
     }
+    Two<E>::store(dx + to, gx);
+    Two<E>::store(df + to, gf);
+    if (GATED) Two<E>::store(di + to, gi);
   }
   if (p.s_out) Two<float>::store(p.s_out + row, r);
 }

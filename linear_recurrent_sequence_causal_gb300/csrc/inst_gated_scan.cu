@@ -16,7 +16,7 @@ cudaError_t launch_tiles(F* fn, GatedArgs a, GatedPlan plan, std::atomic<unsigne
   cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
   a.tiles = (a.T + TT - 1) / TT;
-  if (CL && a.tiles > kGatedCluster) return cudaErrorInvalidValue;
+  if (CL && a.tiles > (TT < kGatedChunk ? 1 : kGatedCluster)) return cudaErrorInvalidValue;
   if (CL && a.tiles > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   a.strips = (a.D + CW - 1) / CW;
   const long long chains = (long long)a.B * a.strips, most = kSMs * C / a.tiles > 0 ? kSMs * C / a.tiles : 1;
@@ -91,11 +91,16 @@ template <class E, bool GATED>
 cudaError_t launch_backward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   const int t = plan.tile, c = plan.cols;
   if constexpr (sizeof(E) == 4 && GATED) {
+    if (t == 16) return launch_backward<E, true, 64, 16, 4, 1, 4, true>(a, plan, s);
+    if (t == 32) return launch_backward<E, true, 64, 32, 4, 1, 2, true>(a, plan, s);
     if (c == 64) return launch_backward<E, true, 64, 64, 8, 1, 1, true>(a, plan, s);
     if (plan.cluster) return launch_backward<E, true, 32, 64, 8, 1, 2, true>(a, plan, s);
     return launch_backward<E, true, 32, 64, 8, 1, 3, false>(a, plan, s);
   } else {
     if (plan.cluster) {
+      constexpr int S = sizeof(E) == 2 && !GATED ? 2 : 1;
+      if (t == 16) return launch_backward<E, GATED, 64, 16, 4, S, 6, true>(a, plan, s);
+      if (t == 32) return launch_backward<E, GATED, 64, 32, sizeof(E) == 2 ? 8 : 4, S, sizeof(E) == 2 ? 4 : 3, true>(a, plan, s);
       if (t == 128) return launch_backward<E, GATED, 32, 128, 16, 1, 2, true>(a, plan, s);
       if (c == 64) return launch_backward<E, GATED, 64, 64, 16, 1, 2, true>(a, plan, s);
       return launch_backward<E, GATED, 32, 64, 8, 1, sizeof(E) == 2 && !GATED ? 4 : 3, true>(a, plan, s);
@@ -122,10 +127,11 @@ cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, Gate
 
 template <class E, bool GATED>
 cudaError_t launch_short_t(bool backward, const GatedShortArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)(((long long)a.B * (a.D / 2) + kGatedShortThreads - 1) / kGatedShortThreads);
-  if (backward && a.T <= kGatedAhead) gated_short_backward_kernel<E, GATED, kGatedAhead><<<grid, kGatedShortThreads, 0, s>>>(a);
-  else if (backward) gated_short_backward_kernel<E, GATED, kGatedShort><<<grid, kGatedShortThreads, 0, s>>>(a);
-  else gated_short_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
+  const int P = !backward && (long long)a.B * a.D >= 1 << 17 ? 2 : 1;
+  const unsigned grid = (unsigned)(((long long)a.B * (a.D / (2 * P)) + kGatedShortThreads - 1) / kGatedShortThreads);
+  if (backward) gated_short_backward_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
+  else if (P == 2) gated_short_kernel<E, GATED, 2><<<grid, kGatedShortThreads, 0, s>>>(a);
+  else gated_short_kernel<E, GATED, 1><<<grid, kGatedShortThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

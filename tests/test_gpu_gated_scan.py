@@ -66,7 +66,8 @@ def check(z, c, *, resumed=True, lens=None):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gate", [True, False])
 @pytest.mark.parametrize("B,T,D", [(1, 1, 8), (2, 1, 64), (3, 7, 72), (1, 63, 40), (2, 64, 128), (1, 65, 8), (2, 129, 200),
-                                   (1, 700, 64), (3, 257, 136), (1, 4100, 16)])
+                                   (1, 700, 64), (3, 257, 136), (1, 4100, 16), (2, 8, 72), (2, 9, 72), (3, 16, 136), (3, 17, 72), (2, 32, 200),
+                                   (2, 33, 72)])
 def test_scan(B, T, D, gate, dtype):
     z = make(B, T, D, dtype, gate)
     check(z, dev(z))
@@ -97,7 +98,7 @@ def windows(t):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gate", [True, False])
 @pytest.mark.parametrize("lay", [time_major, windows])
-@pytest.mark.parametrize("B,T,D", [(3, 5, 72), (5, 70, 72), (2, 300, 8), (2, 2500, 136)])
+@pytest.mark.parametrize("B,T,D", [(3, 5, 72), (500, 7, 264), (4, 14, 72), (5, 30, 40), (5, 70, 72), (2, 300, 8), (2, 2500, 136)])
 def test_other_orders(B, T, D, lay, gate, dtype):
     """Tokens further apart than sequences, and sequences that share tokens: the bits of contiguous inputs."""
     c = dev(make(B, T, D, dtype, gate))
@@ -115,7 +116,7 @@ def test_other_orders(B, T, D, lay, gate, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("gate", [True, False])
-@pytest.mark.parametrize("T", [1, 64, 300])
+@pytest.mark.parametrize("T", [1, 7, 16, 30, 64, 300])
 def test_ragged(T, gate, dtype):
     """Lengths of none, one, a tile's border and past the end; padding is NaN and reaches nothing."""
     lens = torch.tensor([0, 1, min(T, 64), min(T, 65), T, T + 9, -3, T // 2])
@@ -156,7 +157,7 @@ def test_many_tiles_and_sequences(dtype):
                                    (2, 900, 40), (8, 1024, 64), (620, 200, 40), (60, 200, 704),
                                    (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72), (2, 512, 136), (2, 513, 24), (3, 2000, 72),
                                    (200, 100, 264), (30, 128, 136), (30, 129, 136), (130, 250, 72), (300, 150, 64), (20, 256, 264),
-                                   (460, 192, 40), (460, 193, 40)])
+                                   (460, 192, 40), (460, 193, 40), (700, 16, 72), (500, 32, 72), (600, 8, 264), (700, 20, 264)])
 def test_every_way(B, T, D, gate, dtype):
     """Token by token, a cluster a chain, looking back in tiles of each length: the rules' borders."""
     lens = torch.randint(0, T + 1, (B,), generator=torch.Generator().manual_seed(B))
