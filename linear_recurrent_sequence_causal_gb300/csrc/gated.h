@@ -48,18 +48,20 @@ constexpr bool gated_is_short(bool backward, int B, int T, int D) {
 //             64 x 32    fp32 with both gates up to 512 (100 x 100 x 256: 11.5 us, 64 x 64 16.0; gradient 4 x 500 x 256: 5.7 and
 //                        10.1); it has no room for two CTAs of 128 tokens in the gradient, which looks back from
 //                        513 tokens on (2 x 2000 x 128: 8.4 us, 128 x 32 13.0)
-//           One tile needs no cluster, only the way through shared memory.  The gradient goes by 16 x 64 up to 16 tokens (381 x 12 x
-//           6696: 115 us, 32 x 64 187) and 32 x 64 up to 32 (400 x 30 x 2048: 77 us, 64 x 32 171), by 64 x 32 up to 64 tokens
-//           (100 x 60 x 256: 7.2 us, 64 x 64 8.5; but fp32 with both gates 10.9 and 9.9) and by 128 x 32 up to 128 while
-//           chains are few (100 x 100 x 256: 12.5 us, looking back 14.1; 300 x 100 x 256: 34 and 29.5), as fp32 with one
-//           gate does forwards (100 x 100 x 256: 7.6 us, 64 x 64 9.2).  Forwards 256 x 32 up to 256 tokens while chains are
-//           few, and fewer where a quarter of it would be padding (both gates, 512 x 200 x 64: 12.2 us, two of 128 in a cluster
-//           14.9, looking back 13.7; 225 x 250 x 256 32.1, looking back 25.3; 450 x 150 x 64 12.3 and 11.5; one gate, 46 x 230 x
-//           1160 17.7 and 18.7; fp32 128 x 200 x 64 8.0 and 10.2, 512 x 200 x 64 27.5 and 23.9).
+//           A chain of one tile needs no cluster, nor room for one, which makes place for a stage or a CTA more.
+//           Gradients go by 16 x 64 up to 16 tokens (381 x 12 x 6696: 115 us, 32 x 64 187), 32 x 64 up to 32 (400 x 30 x 2048: 77
+//           us, 64 x 32 155), 64 x 32 up to 64 (400 x 60 x 2048: 155 us, with a cluster's room 183, 64 x 64 152; 1000 x 60 x 64:
+//           12.6, 13.9 and 15.7), and by 128 x 32 up to 128 while chains are few (100 x 100 x 256: 12.5 us, looking back 14.1;
+//           300 x 100 x 256: 34 and 29.5), as fp32 with one gate does forwards (100 x 100 x 256: 7.6 us, 64 x 64 9.2).
+//           Forwards 64 tokens go by 64 x 64, in fp32 by 64 x 32 (400 x 60 x 2048, one gate 93 us, 64 x 64 115), and up to 256 by
+//           256 x 32 while chains are few, and fewer where a quarter of it would be padding (both gates, 512 x 200 x 64: 12.2
+//           us, two of 128 in a cluster 14.9, looking back 13.7; 225 x 250 x 256 32.1, looking back 25.3; 450 x 150 x 64 12.3
+//           and 11.5; one gate, 46 x 230 x 1160 17.7 and 18.7; fp32 128 x 200 x 64 8.0 and 10.2, 512 x 200 x 64 27.5 and 23.9).
 constexpr int kGatedCluster = 16;
+constexpr int kLookBack = 0, kCluster = 1, kAlone = 2;         // kAlone: a chain is one tile
 struct GatedPlan {
   int tile, cols;
-  bool cluster;
+  bool cluster;                          // or alone
 };
 inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, int D) {
   const long long chains = (long long)B * ((D + 63) / 64);        // of 64 channels
@@ -69,10 +71,7 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
   };
   if (backward && T <= 32) return {T <= 16 ? 16 : 32, 64, true};
   if (dtype == 0 && gated) {
-    if (backward) {
-      if (T <= 64) return {64, 64, true};
-      return {64, 32, T <= 512 && fits(64, 1)};
-    }
+    if (backward) return {64, 32, T <= 512 && fits(64, 1)};
     if (T <= 512 && fits(64, 2)) return {64, 32, true};
     if (T > 512 && fits(128, 1)) return {128, 32, true};
     if (T <= 256 && chains <= 304) return {256, 32, true};
@@ -86,7 +85,7 @@ inline GatedPlan gated_plan(int dtype, bool backward, bool gated, int B, int T, 
     if (dtype == 0) return {64, 64, false};
     return D <= 32 || chains <= 76 ? GatedPlan{128, 32, false} : GatedPlan{64, 64, false};
   }
-  if (T <= 64) return {64, 64, true};
+  if (T <= 64) return {64, dtype == 0 ? 32 : 64, true};
   if (dtype == 0) {
     if (T <= 128) return {128, 32, true};
     if (T <= 512 && fits(64, 2)) return {64, 64, true};

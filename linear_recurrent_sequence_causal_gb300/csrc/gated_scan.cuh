@@ -347,14 +347,15 @@ struct GatedJob {
 // after tile.  Copies are TMA's, a box of CW channels by TT tokens each: the next tiles' come in while
 // it works (a stage is free again once its values are in registers), and a tile's outputs
 // leave while it works on the next one.
-// With CL the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles; more than 8 have to be
+// With kCluster the tiles of a chain are the CTAs of a cluster (up to kGatedCluster tiles; more than 8 have to be
 // allowed): they hand each other (P, L) through shared memory, with one barrier of the cluster, and need neither
-// tickets nor workspace.
-template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
+// tickets nor workspace.  With kAlone a chain is one tile.
+template <class E, int NI, int NO, int CW, int TT, int R, int S, int WAY>
 struct GatedShared {
+  static constexpr bool CL = WAY != kLookBack;
   static constexpr int NW = kGatedThreads<CW, TT, R> / 32;
   static constexpr bool BACK = NI > 2 && NO > 1;
-  static constexpr int chain = TT < kGatedChunk ? 1 : kGatedCluster;       // tiles of a cluster
+  static constexpr int chain = WAY == kAlone ? 1 : kGatedCluster;        // tiles of a cluster
   struct Nothing {};
   alignas(128) E tile[S][NI][TT][CW];
   alignas(128) E out[NO][TT][CW];
@@ -373,9 +374,10 @@ struct GatedShared {
 };
 
 // Tickets and copies of a CTA, which one thread makes.
-template <class E, int NI, int NO, int CW, int TT, int R, int S, bool CL>
+template <class E, int NI, int NO, int CW, int TT, int R, int S, int WAY>
 struct GatedFeed {
-  GatedShared<E, NI, NO, CW, TT, R, S, CL>& sm;
+  static constexpr bool CL = WAY != kLookBack;
+  GatedShared<E, NI, NO, CW, TT, R, S, WAY>& sm;
   const GatedArgs& p;
   unsigned next;
   bool lost;                                       // a copy never came: no more of them
@@ -451,16 +453,17 @@ __device__ __forceinline__ uint64_t load_pair(const float* p) {
 }
 
 // Forward.  S stages, C CTAs an SM.
-template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, int WAY>
 __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel(const __grid_constant__ GatedArgs p) {
   static_assert(kGatedChunk % R == 0, "a row of states starts at a warp's tokens");
   constexpr int NW = kGatedThreads<CW, TT, R> / 32, H = 64 / CW, NI = GATED ? 3 : 2;
-  using Shared = GatedShared<E, NI, 1, CW, TT, R, S, CL>;
+  constexpr bool CL = WAY != kLookBack;
+  using Shared = GatedShared<E, NI, 1, CW, TT, R, S, WAY>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / (CW / 2), col = lane % (CW / 2) * 2;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, NI, 1, CW, TT, R, S, CL> feed{sm, p, 0, false};
+  GatedFeed<E, NI, 1, CW, TT, R, S, WAY> feed{sm, p, 0, false};
   if (feeder) feed.init();
   if (CL) chain_barrier(p);                        // its CTAs are there
   else __syncthreads();
@@ -626,16 +629,17 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
 // Gradient.  The tile's states come from the row of `states` before it, what reaches it from
 // behind from the tiles after it.  Gates and inputs of a lane's tokens stay in registers between the two ends (a, 1 - a, w,
 // 1 - w, x, dout, h: 250 registers at 16 tokens); recomputing the gates instead would fill the SM's exponential unit.
-template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, int WAY>
 __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backward_kernel(const __grid_constant__ GatedArgs p) {
-  static_assert(TT % kGatedChunk == 0 || (CL && TT < kGatedChunk), "a tile starts at a row of states, or is the only one");
+  static_assert(TT % kGatedChunk == 0 || (WAY == kAlone && TT < kGatedChunk), "a tile starts at a row of states, or is the only one");
   constexpr int NW = kGatedThreads<CW, TT, R> / 32, H = 64 / CW, NI = GATED ? 4 : 3, NO = GATED ? 3 : 2;
-  using Shared = GatedShared<E, NI, NO, CW, TT, R, S, CL>;
+  constexpr bool CL = WAY != kLookBack;
+  using Shared = GatedShared<E, NI, NO, CW, TT, R, S, WAY>;
   extern __shared__ __align__(128) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / (CW / 2), col = lane % (CW / 2) * 2;
   const bool feeder = threadIdx.x == 32 * (NW - 1);
-  GatedFeed<E, NI, NO, CW, TT, R, S, CL> feed{sm, p, 0, false};
+  GatedFeed<E, NI, NO, CW, TT, R, S, WAY> feed{sm, p, 0, false};
   if (feeder) feed.init();
   if (CL) chain_barrier(p);                        // its CTAs are there
   else __syncthreads();

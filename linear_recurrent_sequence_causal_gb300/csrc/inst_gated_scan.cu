@@ -9,14 +9,15 @@ namespace prism {
 constexpr int kSMs = 152;
 
 // Persistent CTAs.  Chains by cluster: a cluster takes chain after chain; else a CTA takes tile after tile.
-template <class Shared, int CW, int TT, int R, int C, bool CL, class F>
+template <class Shared, int CW, int TT, int R, int C, int WAY, class F>
 cudaError_t launch_tiles(F* fn, GatedArgs a, GatedPlan plan, std::atomic<unsigned long long>& done, cudaStream_t s) {
   static_assert(C * (sizeof(Shared) + 1024) <= 228 * 1024, "C CTAs on an SM");
+  constexpr bool CL = WAY != kLookBack;
   if (plan.tile != TT || plan.cols != CW || plan.cluster != CL) return cudaErrorInvalidValue;      // the maps' boxes
   cudaError_t e = allow_smem(fn, sizeof(Shared), done);
   if (e != cudaSuccess) return e;
   a.tiles = (a.T + TT - 1) / TT;
-  if (CL && a.tiles > (TT < kGatedChunk ? 1 : kGatedCluster)) return cudaErrorInvalidValue;
+  if (CL && a.tiles > (WAY == kAlone ? 1 : kGatedCluster)) return cudaErrorInvalidValue;
   if (CL && a.tiles > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   a.strips = (a.D + CW - 1) / CW;
   const long long chains = (long long)a.B * a.strips, most = kSMs * C / a.tiles > 0 ? kSMs * C / a.tiles : 1;
@@ -38,17 +39,17 @@ cudaError_t launch_tiles(F* fn, GatedArgs a, GatedPlan plan, std::atomic<unsigne
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
-template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, int WAY>
 cudaError_t launch_forward(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, CW, TT, R, S, CL>, CW, TT, R, C, CL>(
-      gated_scan_kernel<E, GATED, CW, TT, R, S, C, CL>, a, plan, done, s);
+  return launch_tiles<GatedShared<E, GATED ? 3 : 2, 1, CW, TT, R, S, WAY>, CW, TT, R, C, WAY>(
+      gated_scan_kernel<E, GATED, CW, TT, R, S, C, WAY>, a, plan, done, s);
 }
-template <class E, bool GATED, int CW, int TT, int R, int S, int C, bool CL>
+template <class E, bool GATED, int CW, int TT, int R, int S, int C, int WAY>
 cudaError_t launch_backward(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, CW, TT, R, S, CL>, CW, TT, R, C, CL>(
-      gated_scan_backward_kernel<E, GATED, CW, TT, R, S, C, CL>, a, plan, done, s);
+  return launch_tiles<GatedShared<E, GATED ? 4 : 3, GATED ? 3 : 2, CW, TT, R, S, WAY>, CW, TT, R, C, WAY>(
+      gated_scan_backward_kernel<E, GATED, CW, TT, R, S, C, WAY>, a, plan, done, s);
 }
 
 #ifndef GATED_BENCH
@@ -56,61 +57,59 @@ cudaError_t launch_backward(const GatedArgs& a, GatedPlan plan, cudaStream_t s) 
 template <class E, bool GATED>
 cudaError_t launch_forward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   const int t = plan.tile, c = plan.cols;
+  const bool alone = plan.cluster && a.T <= t;
   if constexpr (sizeof(E) == 2) {
     constexpr int S = GATED ? 1 : 2;
     if (plan.cluster) {
-      if (t == 64) return launch_forward<E, GATED, 64, 64, 16, 1, 4, true>(a, plan, s);
-      if (t == 256) return launch_forward<E, GATED, 32, 256, 16, S, 2, true>(a, plan, s);
-      if (c == 32) return launch_forward<E, GATED, 32, 128, 16, 1, 4, true>(a, plan, s);
-      return launch_forward<E, GATED, 64, 128, 16, S, 2, true>(a, plan, s);
+      if (t == 64) return launch_forward<E, GATED, 64, 64, 16, S, 4, kAlone>(a, plan, s);
+      if (t == 256) return launch_forward<E, GATED, 32, 256, 16, S, 2, kAlone>(a, plan, s);
+      if (c == 32) return launch_forward<E, GATED, 32, 128, 16, 1, 4, kCluster>(a, plan, s);
+      return launch_forward<E, GATED, 64, 128, 16, S, 2, kCluster>(a, plan, s);
     }
-    if (c == 32) return launch_forward<E, GATED, 32, 128, 16, S, 4, false>(a, plan, s);
-    if (t == 64) return launch_forward<E, GATED, 64, 64, 16, S, 4, false>(a, plan, s);
+    if (c == 32) return launch_forward<E, GATED, 32, 128, 16, S, 4, kLookBack>(a, plan, s);
+    if (t == 64) return launch_forward<E, GATED, 64, 64, 16, S, 4, kLookBack>(a, plan, s);
     if constexpr (!GATED) {
-      if (t == 256) return launch_forward<E, false, 64, 256, 16, 2, 1, false>(a, plan, s);
+      if (t == 256) return launch_forward<E, false, 64, 256, 16, 2, 1, kLookBack>(a, plan, s);
     }
-    return launch_forward<E, GATED, 64, 128, 16, S, 2, false>(a, plan, s);
-  } else if constexpr (GATED) {
-    if (plan.cluster) {
-      if (t == 64) return launch_forward<E, true, 32, 64, 8, 1, 4, true>(a, plan, s);
-      if (t == 256) return launch_forward<E, true, 32, 256, 8, 1, 1, true>(a, plan, s);
-      return launch_forward<E, true, 32, 128, 16, 1, 2, true>(a, plan, s);
-    }
-    if (t == 64) return launch_forward<E, true, 32, 64, 8, 2, 3, false>(a, plan, s);
-    return launch_forward<E, true, 32, 128, 16, 1, 2, false>(a, plan, s);
+    return launch_forward<E, GATED, 64, 128, 16, S, 2, kLookBack>(a, plan, s);
   } else {
     if (plan.cluster) {
-      if (t == 64) return launch_forward<E, false, 64, 64, 16, 1, 3, true>(a, plan, s);
-      if (t == 256) return launch_forward<E, false, 32, 256, 8, 1, 1, true>(a, plan, s);
-      return launch_forward<E, false, 32, 128, 16, 1, 3, true>(a, plan, s);
+      if (t == 64 && alone) return launch_forward<E, GATED, 32, 64, 8, 2, GATED ? 3 : 4, kAlone>(a, plan, s);
+      if (t == 256) return launch_forward<E, GATED, 32, 256, 8, 1, 1, kAlone>(a, plan, s);
+      if (t == 128) return launch_forward<E, GATED, 32, 128, 16, 1, GATED ? 2 : 3, kCluster>(a, plan, s);
+      if constexpr (GATED) return launch_forward<E, true, 32, 64, 8, 1, 4, kCluster>(a, plan, s);
+      else return launch_forward<E, false, 64, 64, 16, 1, 3, kCluster>(a, plan, s);
     }
-    return launch_forward<E, false, 32, 128, 16, 1, 3, false>(a, plan, s);
+    if constexpr (GATED) {
+      if (t == 64) return launch_forward<E, true, 32, 64, 8, 2, 3, kLookBack>(a, plan, s);
+    }
+    return launch_forward<E, GATED, 32, 128, 16, 1, GATED ? 2 : 3, kLookBack>(a, plan, s);
   }
 }
 template <class E, bool GATED>
 cudaError_t launch_backward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
   const int t = plan.tile, c = plan.cols;
-  if constexpr (sizeof(E) == 4 && GATED) {
-    if (t == 16) return launch_backward<E, true, 64, 16, 4, 1, 4, true>(a, plan, s);
-    if (t == 32) return launch_backward<E, true, 64, 32, 4, 1, 2, true>(a, plan, s);
-    if (c == 64) return launch_backward<E, true, 64, 64, 8, 1, 1, true>(a, plan, s);
-    if (plan.cluster) return launch_backward<E, true, 32, 64, 8, 1, 2, true>(a, plan, s);
-    return launch_backward<E, true, 32, 64, 8, 1, 3, false>(a, plan, s);
+  const bool alone = plan.cluster && a.T <= t;
+  constexpr bool wide = sizeof(E) == 4;
+  constexpr int S = !wide && !GATED ? 2 : 1;
+  if (t == 16) return launch_backward<E, GATED, 64, 16, 4, S, wide && GATED ? 4 : 6, kAlone>(a, plan, s);
+  if (t == 32) return launch_backward<E, GATED, 64, 32, wide ? 4 : 8, S, !wide ? 4 : GATED ? 2 : 3, kAlone>(a, plan, s);
+  if (t == 64 && c == 32 && alone) return launch_backward<E, GATED, 32, 64, 8, S, wide && GATED ? 3 : 4, kAlone>(a, plan, s);
+  if constexpr (wide && GATED) {
+    if (plan.cluster) return launch_backward<E, true, 32, 64, 8, 1, 2, kCluster>(a, plan, s);
+    return launch_backward<E, true, 32, 64, 8, 1, 3, kLookBack>(a, plan, s);
   } else {
+    if constexpr (S == 2) {
+      if (t == 128 && alone) return launch_backward<E, GATED, 32, 128, 16, 2, 2, kAlone>(a, plan, s);
+    }
     if (plan.cluster) {
-      constexpr int S = sizeof(E) == 2 && !GATED ? 2 : 1;
-      if (t == 16) return launch_backward<E, GATED, 64, 16, 4, S, 6, true>(a, plan, s);
-      if (t == 32) return launch_backward<E, GATED, 64, 32, sizeof(E) == 2 ? 8 : 4, S, sizeof(E) == 2 ? 4 : 3, true>(a, plan, s);
-      if (t == 128) return launch_backward<E, GATED, 32, 128, 16, 1, 2, true>(a, plan, s);
-      if (c == 64) return launch_backward<E, GATED, 64, 64, 16, 1, 2, true>(a, plan, s);
-      return launch_backward<E, GATED, 32, 64, 8, 1, sizeof(E) == 2 && !GATED ? 4 : 3, true>(a, plan, s);
+      if (t == 128) return launch_backward<E, GATED, 32, 128, 16, 1, 2, kCluster>(a, plan, s);
+      return launch_backward<E, GATED, 64, 64, 16, 1, 2, kCluster>(a, plan, s);
     }
-    if constexpr (sizeof(E) == 2) {
-      if (c == 32) return launch_backward<E, GATED, 32, 128, 16, 2, 2, false>(a, plan, s);
-      return launch_backward<E, GATED, 64, 64, 16, 2, 2, false>(a, plan, s);
-    } else {
-      return launch_backward<E, false, 64, 64, 16, 1, 2, false>(a, plan, s);
+    if constexpr (!wide) {
+      if (c == 32) return launch_backward<E, GATED, 32, 128, 16, 2, 2, kLookBack>(a, plan, s);
     }
+    return launch_backward<E, GATED, 64, 64, 16, wide ? 1 : 2, 2, kLookBack>(a, plan, s);
   }
 }
 template <class E, bool GATED>

@@ -157,7 +157,8 @@ def test_many_tiles_and_sequences(dtype):
                                    (2, 900, 40), (8, 1024, 64), (620, 200, 40), (60, 200, 704),
                                    (1, 1024, 72), (1, 1025, 72), (2, 520, 64), (1, 3000, 72), (2, 512, 136), (2, 513, 24), (3, 2000, 72),
                                    (200, 100, 264), (30, 128, 136), (30, 129, 136), (130, 250, 72), (300, 150, 64), (20, 256, 264),
-                                   (460, 192, 40), (460, 193, 40), (700, 16, 72), (500, 32, 72), (600, 8, 264), (700, 20, 264)])
+                                   (460, 192, 40), (460, 193, 40), (700, 16, 72), (500, 32, 72), (600, 8, 264), (700, 20, 264),
+                                   (900, 50, 72), (350, 100, 72)])
 def test_every_way(B, T, D, gate, dtype):
     """Token by token, a cluster a chain, looking back in tiles of each length: the rules' borders."""
     lens = torch.randint(0, T + 1, (B,), generator=torch.Generator().manual_seed(B))
