@@ -101,7 +101,8 @@ def _workspace(t, nbytes, device, dev, side):
     return t, t.data_ptr(), nbytes
 
 
-# The checked dims of a call by shapes, strides and settings, as in ``linattn``.
+# The checked dims of a call by shapes, strides and settings, as in ``linattn``, with their workspace and the shapes of what
+# goes with them.
 
 @functools.lru_cache(maxsize=256)
 def _norm_dims(xs, xst, dtype, eps, dost):
@@ -112,7 +113,7 @@ def _norm_dims(xs, xst, dtype, eps, dost):
                       x_stride=_steps("x", xs, xst))
     if dost is not None:
         d.do_stride = _steps("d_out", xs, dost)
-    return d, ctypes.addressof(d), int(load().prism_layer_norm_workspace_bytes(ctypes.addressof(d)))
+    return d, ctypes.addressof(d), int(load().prism_layer_norm_workspace_bytes(ctypes.addressof(d))), xs[2:], xs[:1]
 
 
 @functools.lru_cache(maxsize=256)
@@ -128,7 +129,7 @@ def _gated_dims(xs, dtype, xst, fst, ist, dost, flags):
         d.do_stride = _steps("d_out", xs, dost)
     rows = torch.Size((xs[0], -(-xs[1] // PRISM_GATED_CHUNK), xs[2]))
     size = load().prism_gated_scan_workspace_bytes if dost is None else load().prism_gated_scan_backward_workspace_bytes
-    return d, ctypes.addressof(d), int(size(ctypes.addressof(d))), rows
+    return d, ctypes.addressof(d), int(size(ctypes.addressof(d))), rows, rows[::2], xs[:1]
 
 
 @functools.lru_cache(maxsize=256)
@@ -145,21 +146,19 @@ def _decode_dims(xs, dtype, xst, fst, ist):
                   f_stride=steps("forget", fst))
     if ist is not None:
         d.i_stride = steps("input_gate", ist)
-    return d, ctypes.addressof(d)
+    return d, ctypes.addressof(d), xs[:1]
 
 
 def prism_layer_norm(x, *, weight=None, bias=None, eps=1e-5, seq_lens=None, out=None, stream=None):
     """Layer norm of every token of x [B,T,D]: (x - mean) / sqrt(var + eps) * weight + bias, ``weight``
     and ``bias`` [D] fp32 (None: ones, zeros).  Returns out [B,T,D], contiguous, in x's type,
     0 at padding tokens."""
-    xs = x.shape
-    keep, dims, _ = _norm_dims(xs, x.stride(), x.dtype, float(eps), None)
+    keep, dims, _, D, B = _norm_dims(x.shape, x.stride(), x.dtype, float(eps), None)
     dev, raw, side = _stream(x, stream)
     if side is not None:
         _used(side, x, weight, bias, seq_lens, out)
-    D = xs[2:]
     w, b = _whole("weight", weight, D, torch.float32, dev), _whole("bias", bias, D, torch.float32, dev)
-    lens = _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev)
+    lens = _whole("seq_lens", seq_lens, B, torch.int32, dev)
     out, to = _result("out", out, x, dev, side)
     _call(dev, load().prism_layer_norm, dims, x.data_ptr(), w, b, lens, to, raw)
     return out
@@ -172,15 +171,14 @@ def prism_layer_norm_backward(x, d_out, *, weight=None, bias=None, eps=1e-5, seq
     outputs with the same keys."""
     xs = x.shape
     _like("d_out", d_out, xs, x.dtype)
-    keep, dims, nbytes = _norm_dims(xs, x.stride(), x.dtype, float(eps), d_out.stride())
+    keep, dims, nbytes, D, B = _norm_dims(xs, x.stride(), x.dtype, float(eps), d_out.stride())
     dev, raw, side = _stream(x, stream)
-    D = xs[2:]
     g = dict(grads) if grads else {}
     if side is not None:
         _used(side, x, d_out, weight, bias, seq_lens, workspace, *g.values())
     w = _whole("weight", weight, D, torch.float32, dev)
     _whole("bias", bias, D, torch.float32, dev)
-    lens, dy = _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev), _strided("d_out", d_out, dev)
+    lens, dy = _whole("seq_lens", seq_lens, B, torch.int32, dev), _strided("d_out", d_out, dev)
     g["x"], dx = _result("grads['x']", g.get("x"), x, dev, side)
     to = {}
     for n, t in (("weight", weight), ("bias", bias)):
@@ -218,14 +216,13 @@ def prism_gated_scan_forward(x, forget, *, input_gate=None, initial_state=None, 
     [B,T,D] in x's type, and the last one in fp32 (None when ``want_state`` is False and none was passed;
     it may be initial_state itself).  ``states`` (see gated_scan_states) is filled for the backward pass."""
     xs, dt, ist = _gates(x, forget, input_gate)
-    keep, dims, nbytes, rows = _gated_dims(xs, dt, x.stride(), forget.stride(), ist, None, int(flags))
+    keep, dims, nbytes, rows, ss, B = _gated_dims(xs, dt, x.stride(), forget.stride(), ist, None, int(flags))
     dev, raw, side = _stream(x, stream)
-    ss = rows[::2]
     if side is not None:
         _used(side, x, forget, input_gate, initial_state, out, final_state, states, seq_lens, workspace)
     f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
     s0, st = _whole("initial_state", initial_state, ss, torch.float32, dev), _whole("states", states, rows, torch.float32, dev)
-    lens = _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev)
+    lens = _whole("seq_lens", seq_lens, B, torch.int32, dev)
     out, to = _result("out", out, x, dev, side)
     if final_state is None and want_state:
         final_state = _new(ss, torch.float32, x.device, side)
@@ -245,15 +242,14 @@ def prism_gated_scan_backward(x, forget, states, d_out, *, input_gate=None, d_fi
     ``want_initial_state``).  ``grads`` may pass preallocated outputs with the same keys."""
     xs, dt, ist = _gates(x, forget, input_gate)
     _like("d_out", d_out, xs, dt)
-    keep, dims, nbytes, rows = _gated_dims(xs, dt, x.stride(), forget.stride(), ist, d_out.stride(), int(flags))
+    keep, dims, nbytes, rows, ss, B = _gated_dims(xs, dt, x.stride(), forget.stride(), ist, d_out.stride(), int(flags))
     dev, raw, side = _stream(x, stream)
-    ss = rows[::2]
     g = dict(grads) if grads else {}
     if side is not None:
         _used(side, x, forget, input_gate, states, d_out, d_final_state, seq_lens, workspace, *g.values())
     f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
     st, dy = _whole("states", states, rows, torch.float32, dev), _strided("d_out", d_out, dev)
-    s1, lens = _whole("d_final_state", d_final_state, ss, torch.float32, dev), _whole("seq_lens", seq_lens, xs[:1], torch.int32, dev)
+    s1, lens = _whole("d_final_state", d_final_state, ss, torch.float32, dev), _whole("seq_lens", seq_lens, B, torch.int32, dev)
     g["x"], dx = _result("grads['x']", g.get("x"), x, dev, side)
     g["forget"], df = _result("grads['forget']", g.get("forget"), forget, dev, side)
     if input_gate is not None:
@@ -275,13 +271,13 @@ def prism_gated_scan_decode_step(x, forget, state, *, input_gate=None, slots=Non
     ``slots`` [B] int32 says which state each sequence has (None: its own index; outside 0..N-1: the
     sequence is not there, its output is 0).  Returns out [B,D] in x's type."""
     xs, dt, ist = _gates(x, forget, input_gate)
-    keep, dims = _decode_dims(xs, dt, x.stride(), forget.stride(), ist)
+    keep, dims, B = _decode_dims(xs, dt, x.stride(), forget.stride(), ist)
     dev, raw, side = _stream(x, stream)
     N = state.shape[0]
     if side is not None:
         _used(side, x, forget, input_gate, state, slots, out)
     f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
-    st, at = _whole("state", state, (N, xs[1]), torch.float32, dev), _whole("slots", slots, xs[:1], torch.int32, dev)
+    st, at = _whole("state", state, (N, xs[1]), torch.float32, dev), _whole("slots", slots, B, torch.int32, dev)
     out, to = _result("out", out, x, dev, side)
     _call(dev, load().prism_gated_scan_decode_step, dims, x.data_ptr(), f, i, st, N, at, to, raw)
     return out
