@@ -3,8 +3,9 @@
 Argument checks and marshalling only, as in ``linattn``: the work runs in libprism.so's kernels,
 and a missing library raises.  Token inputs (x, the gates and the gradients that come in) are
 [B,T,D] tensors whose channels are contiguous; sequences and tokens may be strided, so slices
-of one fused projection serve as they are.  Everything else is contiguous.  All tensors of a call
-lie on x's device, which need not be the current one.
+of one fused projection serve as they are; tensors expanded over tokens or sequences are refused.
+Everything else is contiguous.  All tensors of a call lie on x's device, which need not be the
+current one.
 
 Streams are handled as in ``linattn``: a call runs on ``stream`` (default: the current one), what it
 allocates there comes from that stream's memory, and its tensors are recorded on the streams that
@@ -66,6 +67,9 @@ def _steps(name, shape, stride):
         raise PrismError(1, f"{name} is empty")
     if stride[2] != 1 and D > 1:
         raise PrismError(1, f"{name}: the channels of a token must be contiguous")
+    if (T > 1 and stride[1] < D) or (B > 1 and stride[0] <= 0):     # a step of 0 would be taken for "contiguous"
+        raise PrismError(1, f"{name}: every token must have memory of its own; an expanded tensor is not read as it lies "
+                            "(call contiguous() on it)")
     return _stride(stride[0] if B > 1 else T * max(stride[1], D), stride[1] if T > 1 else D)
 
 
