@@ -3,8 +3,9 @@
 Argument checks and marshalling only, as in ``prism``: the work runs in libprism.so's
 kernels, and a missing library raises.  Token inputs (q, k, v and the gradients that come in)
 are [B,T,H,D] tensors whose heads are contiguous; sequences and tokens may be strided, so
-slices of one fused projection serve as they are.  Everything else is contiguous.  All tensors of a
-call lie on q's device, which need not be the current one.
+slices of one fused projection serve as they are; tensors expanded over tokens or sequences are
+refused.  Everything else is contiguous.  All tensors of a call lie on q's device, which need not be
+the current one.
 
 A call runs on ``stream`` (default: the current one), ordered after what is there already.  Where
 that is not the current stream, what the call allocates comes from that stream's memory, and
@@ -82,6 +83,9 @@ def _steps(name, shape, stride):
         raise PrismError(1, f"{name} is empty")
     if stride[3] != 1 or (H > 1 and stride[2] != D):
         raise PrismError(1, f"{name}: the heads of a token must be contiguous")
+    if (T > 1 and stride[1] < H * D) or (B > 1 and stride[0] <= 0):     # a step of 0 would be taken for "contiguous"
+        raise PrismError(1, f"{name}: every token must have memory of its own; an expanded tensor is not read as it lies "
+                            "(call contiguous() on it)")
     return _stride(stride[0] if B > 1 else T * max(stride[1], H * D), stride[1] if T > 1 else H * D)
 
 
