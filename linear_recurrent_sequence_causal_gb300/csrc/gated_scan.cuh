@@ -36,6 +36,7 @@
 
 #include <type_traits>
 
+#include "copy_stages.h"
 #include "gated.h"
 #include "prism_common.cuh"
 #include "tc_common.cuh"
@@ -436,12 +437,18 @@ __device__ __forceinline__ void hand_on(const GatedArgs& p, int rank, ulonglong2
   }
 }
 
-// The way out of a wait that gave up: no copy in flight may outlive the CTA.
-template <int S>
-__device__ __forceinline__ void gated_drain(const GatedArgs& p, uint64_t* full, unsigned phase) {
+// The way out of a wait for job n's copy that gave up: no copy under way may outlive the CTA.
+template <int S, class Shared>
+__device__ __forceinline__ void gated_drain(const GatedArgs& p, Shared& sm, const CopyStages<S>& stages, int n) {
   if (threadIdx.x == 0) {
     atomicOr(p.status, 1);
-    for (int s = 0; s < S; ++s) tc::bar_wait_long(full + s, phase >> s & 1);
+    stages.under_way(
+        n,
+        [&](int m) {
+          const GatedJob& j = sm.job[m % (2 * S)];
+          return j.more && j.live > 0;
+        },
+        [&](int s, unsigned parity) { tc::bar_wait_long(&sm.full[s], parity); });
   }
   __syncthreads();
 }
@@ -467,18 +474,15 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
   if (feeder) feed.init();
   if (CL) chain_barrier(p);                        // its CTAs are there
   else __syncthreads();
-  unsigned phase = 0;                              // a bit a stage
+  CopyStages<S> stages;
   bool lost = false;
   int it = 0;
   for (;; ++it) {
     const GatedJob job = sm.job[it % (2 * S)];
     if (!job.more) break;
     const int s = it % S, mine = (warp * H + sub) * R;    // the lane's first token in the tile
-    bool ok = true;
-    if (job.live > 0 && !lost) {
-      ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
-      phase ^= 1u << s;
-    }
+    const bool copied = job.live > 0 && !lost;
+    const bool ok = !copied || tc::bar_wait_long(&sm.full[s], stages.parity(it));
     uint64_t a[R], u[R], P = both(1.f), L = both(0.f);
     auto token = [&](int j) {
       Two<E> x, f, i;
@@ -514,10 +518,11 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
     part[warp][lane] = make_ulonglong2(P, L);
     tc::fence_smem_to_async();                     // the last tile's outputs
     if (__syncthreads_or(!ok)) {                   // a copy that never came
-      gated_drain<S>(p, sm.full, phase);
+      gated_drain(p, sm, stages, it);
       if (!CL) break;
       feed.lost = lost = true;                     // the chain's others still meet at their barriers
     }
+    if (copied) stages.taken(it);
     if (feeder) {
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
       feed.load(it + S);
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
   if (CL) chain_barrier(p);                        // its CTAs are there
   else __syncthreads();
   const uint64_t none = both(0.f), one = both(1.f), minus = both(-1.f);
-  unsigned phase = 0;
+  CopyStages<S> stages;
   bool lost = false;
   int it = 0;
   for (;; ++it) {
@@ -655,11 +660,8 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
     uint64_t h0 = none;                            // the tile's first state: warp 1 hands it on
     if (warp == 1 && on && job.live > 0)
       h0 = load_pair(p.states + ((long long)job.b * p.NC + job.first / kGatedChunk) * p.D + ch);
-    bool ok = true;
-    if (job.live > 0 && !lost) {
-      ok = tc::bar_wait_long(&sm.full[s], phase >> s & 1);
-      phase ^= 1u << s;
-    }
+    const bool copied = job.live > 0 && !lost;
+    const bool ok = !copied || tc::bar_wait_long(&sm.full[s], stages.parity(it));
     Two<E> x[R], d[R];
     // a, 1 - a, w and 1 - w of every token (without an input gate w is 1 - a)
     uint64_t a[R], c[R], w[GATED ? R : 1], v[GATED ? R : 1], P = one, L = none, r = none;
@@ -709,10 +711,11 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
     back[warp][lane] = r;
     tc::fence_smem_to_async();
     if (__syncthreads_or(!ok)) {
-      gated_drain<S>(p, sm.full, phase);
+      gated_drain(p, sm, stages, it);
       if (!CL) break;
       feed.lost = lost = true;
     }
+    if (copied) stages.taken(it);
     if (feeder) {
       if (it > 0) feed.store(sm.job[(it - 1) % (2 * S)]);
       feed.load(it + S);
