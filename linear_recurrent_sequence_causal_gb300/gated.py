@@ -158,7 +158,7 @@ def prism_layer_norm(x, *, weight=None, bias=None, eps=1e-5, seq_lens=None, out=
     and ``bias`` [D] fp32 (None: ones, zeros).  Returns out [B,T,D], contiguous, in x's type,
     0 at padding tokens."""
     keep, dims, _, D, B = _norm_dims(x.shape, x.stride(), x.dtype, float(eps), None)
-    dev, raw, side = _stream(x, stream)
+    dev, raw, side = _stream(x, stream, "x")
     if side is not None:
         _used(side, x, weight, bias, seq_lens, out)
     w, b = _whole("weight", weight, D, torch.float32, dev), _whole("bias", bias, D, torch.float32, dev)
@@ -176,7 +176,7 @@ def prism_layer_norm_backward(x, d_out, *, weight=None, bias=None, eps=1e-5, seq
     xs = x.shape
     _like("d_out", d_out, xs, x.dtype)
     keep, dims, nbytes, D, B = _norm_dims(xs, x.stride(), x.dtype, float(eps), d_out.stride())
-    dev, raw, side = _stream(x, stream)
+    dev, raw, side = _stream(x, stream, "x")
     g = dict(grads) if grads else {}
     if side is not None:
         _used(side, x, d_out, weight, bias, seq_lens, workspace, *g.values())
@@ -221,7 +221,7 @@ def prism_gated_scan_forward(x, forget, *, input_gate=None, initial_state=None, 
     it may be initial_state itself).  ``states`` (see gated_scan_states) is filled for the backward pass."""
     xs, dt, ist = _gates(x, forget, input_gate)
     keep, dims, nbytes, rows, ss, B = _gated_dims(xs, dt, x.stride(), forget.stride(), ist, None, int(flags))
-    dev, raw, side = _stream(x, stream)
+    dev, raw, side = _stream(x, stream, "x")
     if side is not None:
         _used(side, x, forget, input_gate, initial_state, out, final_state, states, seq_lens, workspace)
     f, i = _strided("forget", forget, dev), None if input_gate is None else _strided("input_gate", input_gate, dev)
@@ -247,7 +247,7 @@ def prism_gated_scan_backward(x, forget, states, d_out, *, input_gate=None, d_fi
     xs, dt, ist = _gates(x, forget, input_gate)
     _like("d_out", d_out, xs, dt)
     keep, dims, nbytes, rows, ss, B = _gated_dims(xs, dt, x.stride(), forget.stride(), ist, d_out.stride(), int(flags))
-    dev, raw, side = _stream(x, stream)
+    dev, raw, side = _stream(x, stream, "x")
     g = dict(grads) if grads else {}
     if side is not None:
         _used(side, x, forget, input_gate, states, d_out, d_final_state, seq_lens, workspace, *g.values())
@@ -276,7 +276,7 @@ def prism_gated_scan_decode_step(x, forget, state, *, input_gate=None, slots=Non
     sequence is not there, its output is 0).  Returns out [B,D] in x's type."""
     xs, dt, ist = _gates(x, forget, input_gate)
     keep, dims, B = _decode_dims(xs, dt, x.stride(), forget.stride(), ist)
-    dev, raw, side = _stream(x, stream)
+    dev, raw, side = _stream(x, stream, "x")
     N = state.shape[0]
     if side is not None:
         _used(side, x, forget, input_gate, state, slots, out)

@@ -101,13 +101,13 @@ def _whole(name, t, shape, dtype, dev):
     if t.dtype != dtype or t.shape != shape:
         raise PrismError(1, f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
     if t.get_device() != dev or not t.is_contiguous():
-        raise PrismError(1, f"{name} must be a contiguous CUDA tensor on q's device")
+        raise PrismError(1, f"{name} must be a contiguous CUDA tensor on the call's device")
     return t.data_ptr()
 
 
 def _strided(name, t, dev):
     if t.get_device() != dev:
-        raise PrismError(1, f"{name} must be a CUDA tensor on q's device")
+        raise PrismError(1, f"{name} must be a CUDA tensor on the call's device")
     return t.data_ptr()
 
 
@@ -116,21 +116,21 @@ def _room(t, dev):
     if t is None:
         return None, 0
     if t.get_device() != dev or not t.is_contiguous():
-        raise PrismError(1, "workspace must be a contiguous CUDA tensor on q's device")
+        raise PrismError(1, "workspace must be a contiguous CUDA tensor on the call's device")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _stream(t, stream):
+def _stream(t, stream, name="q"):
     """The call's device, the handle of its stream, and the stream itself where it is not the
     device's current one."""
     dev = t.get_device()
     if dev < 0:
-        raise PrismError(1, "q must be a CUDA tensor")
+        raise PrismError(1, f"{name} must be a CUDA tensor")
     here = torch._C._cuda_getCurrentRawStream(dev)
     if stream is None:
         return dev, here, None
     if stream.device.index != dev:
-        raise PrismError(1, f"stream is on device {stream.device.index}, q on device {dev}")
+        raise PrismError(1, f"stream is on device {stream.device.index}, {name} on device {dev}")
     return dev, stream.cuda_stream, None if stream.cuda_stream == here else stream
 
 
