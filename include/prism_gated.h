@@ -20,7 +20,7 @@
  * 16-byte aligned; those of seq_lens and slots 4-byte aligned, workspaces 256-byte.  A workspace
  * is scratch for one call: two calls that may run at the same time take one each.
  *
- *   D   channels of a token: a multiple of 8 (layer norm: up to 16384)
+ *   D   channels of a token: a multiple of 8 up to 2^30 (layer norm: up to 16384)
  *   T   up to 2^30 tokens, B * T below 2^31
  *   seq_lens [B] int32 or NULL: tokens t >= seq_lens[b] are padding, as in prism.h: their
  *   outputs and gradients are 0 and their values, NaN included, reach nothing.  Lengths

@@ -69,6 +69,7 @@ int check_gated(const prism_gated_dims* d, unsigned flags) {
   if (d->flags & ~flags) return PRISM_ERR_INVALID_ARG;
   const int rc = check_tokens(d->B, d->T, d->D, d->dtype);
   if (rc != PRISM_OK) return rc;
+  if (d->D > 1 << 30) return PRISM_ERR_UNSUPPORTED;                                   // channel numbers are 32-bit, strips rounded up
   if (tiles_of(d, prism::kGatedChunk, 32) > kMost) return PRISM_ERR_UNSUPPORTED;     // more than any plan has
   return PRISM_OK;
 }
