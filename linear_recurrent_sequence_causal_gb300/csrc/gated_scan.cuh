@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_kernel
     } else {
       auto arrive = [&](uint64_t h) {              // the state before the tile is known
         const uint64_t end = fma2(P, h, L);
+        __syncwarp();                              // lanes of other runs have read the same state, which s_out may replace
         if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
         else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
         sm.carry[lane] = h;
@@ -764,6 +765,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
     } else {
       auto arrive = [&](uint64_t g) {              // what comes from behind the tile is known
         const uint64_t end = fma2(P, g, L);
+        __syncwarp();                              // lanes of other runs have read the same state, which s_out may replace
         if (!job.last) publish(p.incl + at + (long long)job.rank * step, end);
         else if (p.s_out && on) Two<float>::store(p.s_out + row, end);
         sm.carry[lane] = g;
