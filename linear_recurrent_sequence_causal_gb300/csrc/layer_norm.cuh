@@ -397,6 +397,7 @@ __device__ __forceinline__ void norm_copy(const LayerNormArgs& p, long long firs
   const unsigned all = __ballot_sync(0xffffffffu, on);
   if (lane == 0) {
     *live = all;
+    asm volatile("" ::: "memory");                 // the arrival releases it: with no row to copy it ends the phase
     tc::bar_expect_tx(bar, __popc(all) * (dy ? 2 : 1) * p.D * (int)sizeof(E));
   }
   __syncwarp();
