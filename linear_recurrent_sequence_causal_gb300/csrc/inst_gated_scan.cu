@@ -52,7 +52,6 @@ cudaError_t launch_backward(const GatedArgs& a, GatedPlan plan, cudaStream_t s) 
       gated_scan_backward_kernel<E, GATED, CW, TT, R, S, C, WAY>, a, plan, done, s);
 }
 
-#ifndef GATED_BENCH
 // The variants that gated_plan chooses from.  Stages and CTAs an SM are what its shared memory and registers hold.
 template <class E, bool GATED>
 cudaError_t launch_forward_t(const GatedArgs& a, GatedPlan plan, cudaStream_t s) {
@@ -150,7 +149,5 @@ cudaError_t launch_gated_decode(int dtype, const GatedDecodeArgs& a, cudaStream_
   if (dtype == 0) return a.i ? launch_gated_decode_t<float, true>(a, s) : launch_gated_decode_t<float, false>(a, s);
   return a.i ? launch_gated_decode_t<__nv_bfloat16, true>(a, s) : launch_gated_decode_t<__nv_bfloat16, false>(a, s);
 }
-
-#endif
 
 }  // namespace prism

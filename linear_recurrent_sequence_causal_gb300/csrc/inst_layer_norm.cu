@@ -65,7 +65,6 @@ cudaError_t norm_columns(const LayerNormArgs& a, cudaStream_t s, size_t* count =
   return BACK ? norm_weights(a, (int)grid, s) : cudaGetLastError();
 }
 
-#ifndef NORM_BENCH
 // Which way a width goes: as many lanes a row as its eighths fill, as much of a row a lane as its registers hold
 // (us at 67 million elements, bf16 unless said otherwise):
 //  forward   64 channels: 4 lanes 45, 8 lanes 49; 96: 4 lanes by bulk copies 47, 16 lanes 70; 128: 8 lanes 47, 16 lanes 55;
@@ -170,6 +169,5 @@ size_t layer_norm_partial_rows(int dtype, int D) {
   else backward_e<__nv_bfloat16>(a, nullptr, &count);
   return count;
 }
-#endif
 
 }  // namespace prism
