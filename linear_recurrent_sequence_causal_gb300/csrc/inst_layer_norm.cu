@@ -17,6 +17,30 @@ cudaError_t norm_forward(const LayerNormArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// dw[ch], db[ch] = the partial rows' sum, in order.  A CTA takes 32 columns of the 2 D, each of its 32 warps every
+// 32nd row; a warp then joins what the 32 summed of a column.
+static __global__ void __launch_bounds__(1024) layer_norm_dw_kernel(const float* partial, int rows, int D, float* dw, float* db) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  float t = 0.f;
+  if (col < 2 * D) {
+#pragma unroll 16
+    for (int r = warp; r < rows; r += 32) t += partial[(long long)r * 2 * D + col];
+  }
+  sums[lane][warp] = t;
+  __syncthreads();
+  t = sums[warp][lane];                            // warp: column, lane: what a warp summed
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const int c = blockIdx.x * 32 + warp;
+  if (lane == 0 && c < 2 * D) {
+    if (c < D && dw) dw[c] = t;
+    if (c >= D && db) db[c - D] = t;
+  }
+}
+
 // dw and db from the partial rows: launched while the first kernel drains; it waits for it before it reads.
 static cudaError_t norm_weights(const LayerNormArgs& a, int rows, cudaStream_t s) {
   const cudaError_t e = cudaGetLastError();
@@ -30,21 +54,21 @@ static cudaError_t norm_weights(const LayerNormArgs& a, int rows, cudaStream_t s
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, layer_norm_dw_kernel<32>, (const float*)a.partial, rows, a.D, a.dw, a.db);
+  return cudaLaunchKernelEx(&cfg, layer_norm_dw_kernel, (const float*)a.partial, rows, a.D, a.dw, a.db);
 }
 
 // A grid of up to C CTAs an SM, resident at once.
 static long long norm_grid(long long tiles, int C) { return tiles < kSMs * C ? tiles : kSMs * C; }
 
 // With `count` a gradient's launcher only says how many CTAs, each a row of sums, it ever takes.
-template <class E, int G, int V, int R, int C, bool AHEAD>
+template <class E, int G, int V, int R, int C>
 cudaError_t norm_backward(const LayerNormArgs& a, cudaStream_t s, size_t* count = nullptr) {
   constexpr int rows = kNormThreads<G> / G * R;
   if (count) *count = (size_t)kSMs * C;
   if (count) return cudaSuccess;
   if (a.D > 8 * G * V) return cudaErrorInvalidValue;
   const long long grid = norm_grid(((long long)a.B * a.T + rows - 1) / rows, C);
-  layer_norm_backward_kernel<E, G, V, R, C, AHEAD><<<(unsigned)grid, kNormThreads<G>, 0, s>>>(a);
+  layer_norm_backward_kernel<E, G, V, R, C><<<(unsigned)grid, kNormThreads<G>, 0, s>>>(a);
   return norm_weights(a, (int)grid, s);
 }
 
@@ -133,17 +157,17 @@ cudaError_t backward_e(const LayerNormArgs& a, cudaStream_t s, size_t* count = n
     if (D <= 8192) return norm_columns<E, 512, 512, 2, 2, 2, 1, true>(a, s, count);
     return norm_columns<E, 512, 512, 4, 1, 2, 1, true>(a, s, count);
   } else {
-    if (D <= 32) return norm_backward<E, 4, 1, 2, 2, true>(a, s, count);
-    if (D <= 64) return norm_backward<E, 8, 1, 2, 2, true>(a, s, count);
-    if (D <= 128) return norm_backward<E, 16, 1, 2, 2, true>(a, s, count);
+    if (D <= 32) return norm_backward<E, 4, 1, 2, 2>(a, s, count);
+    if (D <= 64) return norm_backward<E, 8, 1, 2, 2>(a, s, count);
+    if (D <= 128) return norm_backward<E, 16, 1, 2, 2>(a, s, count);
     if (D <= 160) return norm_columns<E, 256, 8, 3, 2, 2, 1, true>(a, s, count);
-    if (D <= 256) return norm_backward<E, 32, 1, 2, 2, true>(a, s, count);
+    if (D <= 256) return norm_backward<E, 32, 1, 2, 2>(a, s, count);
     if (D <= 304) return norm_columns<E, 256, 16, 3, 2, 2, 1, true>(a, s, count);
     if (D <= 384) return norm_columns<E, 256, 16, 3, 1, 3, 1, true>(a, s, count);
-    if (D <= 512) return norm_backward<E, 64, 1, 2, 2, true>(a, s, count);
+    if (D <= 512) return norm_backward<E, 64, 1, 2, 2>(a, s, count);
     if (D <= 640) return norm_columns<E, 256, 32, 3, 2, 2, 1, true>(a, s, count);
     if (D <= 832) return norm_columns<E, 64, 64, 2, 2, 3, 4, true>(a, s, count);
-    if (D <= 1024) return norm_backward<E, 128, 1, 2, 2, true>(a, s, count);
+    if (D <= 1024) return norm_backward<E, 128, 1, 2, 2>(a, s, count);
     if (D <= 1280) return norm_columns<E, 96, 96, 2, 2, 3, 3, true>(a, s, count);
     if (D <= 2048) return norm_columns<E, 128, 128, 2, 2, 3, 2, true>(a, s, count);
     if (D <= 2560) return norm_columns<E, 160, 160, 2, 2, 2, 2, true>(a, s, count);

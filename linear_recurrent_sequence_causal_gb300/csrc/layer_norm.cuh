@@ -237,9 +237,9 @@ __global__ void __launch_bounds__(kNormThreads<G>, C) layer_norm_kernel(LayerNor
   }
 }
 
-// Gradient.  A fixed grid walks the rows, R at once; a thread keeps its channels' sums for dw and db, and the
-// CTA writes one partial row of each.
-template <class E, int G, int V, int R, int C, bool AHEAD>
+// Gradient.  A fixed grid walks the rows, R at once and the next ones on their way; a thread keeps its channels' sums for dw
+// and db, and the CTA writes one partial row of each.
+template <class E, int G, int V, int R, int C>
 __global__ void __launch_bounds__(kNormThreads<G>, C) layer_norm_backward_kernel(LayerNormArgs p) {
   constexpr int NT = kNormThreads<G>, NG = NT / G;
   __shared__ __align__(16) float room[2][2][NT / 32][2 * R];
@@ -284,14 +284,10 @@ __global__ void __launch_bounds__(kNormThreads<G>, C) layer_norm_backward_kernel
   int turn = 0;
   long long first = (long long)blockIdx.x * NG * R;
   Rows next;
-  if (AHEAD) load(next, first + mine);
+  load(next, first + mine);
   for (; first < rows; first += stride, turn ^= 1) {
-    if (AHEAD) {
-      now = next;
-      if (first + stride < rows) load(next, first + stride + mine);
-    } else {
-      load(now, first + mine);
-    }
+    now = next;
+    if (first + stride < rows) load(next, first + stride + mine);
     float s[2 * R], q[2 * R];
     uint64_t v[R][V][4], d[R][V][4];
 #pragma unroll
@@ -360,26 +356,17 @@ __global__ void __launch_bounds__(kNormThreads<G>, C) layer_norm_backward_kernel
   asm volatile("griddepcontrol.launch_dependents;\n");       // the sums' kernel may come up; it waits for this one's end
   // the CTA's groups of threads joined, in order
   float* to = p.partial + (long long)blockIdx.x * 2 * p.D;
-  if constexpr (NG == 1) {
+  static_assert(NG > 1 && V == 1, "rows that share a CTA have one piece a thread");
+  __shared__ float sums[NT][9];                    // a column of padding: threads a row of banks apart
+  for (int side = 0; side < 2; ++side) {
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (8 * (u + G * k) < p.D) {
-        Eight<float>::store(to + 8 * (u + G * k), dw[k]);
-        Eight<float>::store(to + p.D + 8 * (u + G * k), db[k]);
-      }
-  } else {
-    static_assert(NG == 1 || V == 1, "rows that share a CTA have one piece a thread");
-    __shared__ float sums[NT][9];                  // a column of padding: threads a row of banks apart
-    for (int side = 0; side < 2; ++side) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) unpack2(side ? db[0][j] : dw[0][j], sums[threadIdx.x][2 * j], sums[threadIdx.x][2 * j + 1]);
-      __syncthreads();
-      for (int ch = threadIdx.x; ch < p.D; ch += NT) {
-        float t = 0.f;
-        for (int i = 0; i < NG; ++i) t += sums[i * G + ch / 8][ch % 8];
-        to[side * p.D + ch] = t;
-      }
+    for (int j = 0; j < 4; ++j) unpack2(side ? db[0][j] : dw[0][j], sums[threadIdx.x][2 * j], sums[threadIdx.x][2 * j + 1]);
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < p.D; ch += NT) {
+      float t = 0.f;
+      for (int i = 0; i < NG; ++i) t += sums[i * G + ch / 8][ch % 8];
+      to[side * p.D + ch] = t;
     }
   }
 }
@@ -599,32 +586,6 @@ __global__ void __launch_bounds__(NT, C) layer_norm_columns_kernel(LayerNormArgs
       Eight<float>::store(to + ch, dw[k]);
       Eight<float>::store(to + p.D + ch, db[k]);
     }
-  }
-}
-
-// dw[ch], db[ch] = the partial rows' sum, in order.  A CTA takes 32 columns of the 2 D, a warp every
-// W-th row.
-template <int W>
-__global__ void __launch_bounds__(32 * W) layer_norm_dw_kernel(const float* partial, int rows, int D, float* dw, float* db) {
-  static_assert(W == 32, "a warp joins what the W warps summed of a column");
-  __shared__ float sums[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  float t = 0.f;
-  if (col < 2 * D) {
-#pragma unroll 16
-    for (int r = warp; r < rows; r += W) t += partial[(long long)r * 2 * D + col];
-  }
-  sums[lane][warp] = t;
-  __syncthreads();
-  t = sums[warp][lane];                            // warp: column, lane: what a warp summed
-#pragma unroll
-  for (int o = 16; o >= 1; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
-  const int c = blockIdx.x * 32 + warp;
-  if (lane == 0 && c < 2 * D) {
-    if (c < D && dw) dw[c] = t;
-    if (c >= D && db) db[c - D] = t;
   }
 }
 
