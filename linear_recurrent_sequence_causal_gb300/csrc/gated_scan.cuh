@@ -843,8 +843,7 @@ __global__ void __launch_bounds__(kGatedThreads<CW, TT, R>, C) gated_scan_backwa
 
 // Short sequences, up to kGatedShort tokens: a thread takes 2 P channels of one sequence from token to token,
 // and nothing waits for anything.  (A tile of 64 tokens would be mostly padding: 512 sequences of 4
-// tokens, 1512 channels, fp32, took 47 us in tiles.)  P = 2 where there are threads enough: 1000 x 8 x 4096 bf16 66 us,
-// 82 with P = 1; 8 x 4 x 2048 2.5 and 2.4.
+// tokens, 1512 channels, fp32, took 47 us in tiles.)  launch_short_t says where P is 2.
 struct GatedShortArgs {
   const void *x, *f, *i, *dy;                      // i null: w = 1 - a
   long long xs[2], fs[2], is[2], ds[2];            // strides: sequence, token (elements)

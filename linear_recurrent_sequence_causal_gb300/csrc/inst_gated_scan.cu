@@ -123,13 +123,24 @@ cudaError_t launch_gated_scan(int dtype, bool backward, const GatedArgs& a, Gate
                  : launch_scan_t<__nv_bfloat16, false>(backward, a, plan, s);
 }
 
+// Four channels a thread where there are threads enough and registers (forwards; us with four and with two channels):
+//  bf16, one gate    from 2^18 channels on (1024 x 4 x 256: 4.1 and 5.3, 256 x 32 x 1024: 13.4 and 17.0; 128 x 20 x 1024: 7.9 and 7.6)
+//  bf16, both gates  from 2^19 on (512 x 4 x 1512: 11.2 and 13.0, 1000 x 8 x 4096: 57.7 and 71.2; 256 x 32 x 1024: 20.4 and 19.5)
+//  fp32, one gate    from 2^19 on (512 x 1 x 4096: 17.4 and 20.0, 1000 x 8 x 4096: 68.7 and 71.8; 256 x 32 x 1024: 23.6 and 21.8)
+//  fp32, both gates  never: 238 registers (512 x 4 x 1512: 17.5 and 16.8, 256 x 32 x 1024: 30.0 and 29.6, 1000 x 8 x 4096: 105 and 105)
 template <class E, bool GATED>
 cudaError_t launch_short_t(bool backward, const GatedShortArgs& a, cudaStream_t s) {
-  const int P = !backward && (long long)a.B * a.D >= 1 << 17 ? 2 : 1;
+  constexpr bool four = sizeof(E) == 2 || !GATED;
+  const bool wide = four && !backward && (long long)a.B * a.D >= 1 << (sizeof(E) == 2 && !GATED ? 18 : 19);
+  const int P = wide ? 2 : 1;
   const unsigned grid = (unsigned)(((long long)a.B * (a.D / (2 * P)) + kGatedShortThreads - 1) / kGatedShortThreads);
-  if (backward) gated_short_backward_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
-  else if (P == 2) gated_short_kernel<E, GATED, 2><<<grid, kGatedShortThreads, 0, s>>>(a);
-  else gated_short_kernel<E, GATED, 1><<<grid, kGatedShortThreads, 0, s>>>(a);
+  if (backward) {
+    gated_short_backward_kernel<E, GATED><<<grid, kGatedShortThreads, 0, s>>>(a);
+  } else if (wide) {
+    if constexpr (four) gated_short_kernel<E, GATED, 2><<<grid, kGatedShortThreads, 0, s>>>(a);
+  } else {
+    gated_short_kernel<E, GATED, 1><<<grid, kGatedShortThreads, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 
