@@ -84,8 +84,8 @@ typedef struct {
  * Gates and states are fp32; out is rounded once.  A gate below 2^-126 counts as 0, and so may a
  * product of gates below it (an infinite state may become NaN there).  Tiles of a
  * sequence wait for the state of the tiles before them; the result does not depend on their
- * timing (two calls agree bit for bit).  The workspace has prism_gated_scan_workspace_bytes (0 for short
- * sequences, where no tile looks back: it may then be NULL). */
+ * timing (two calls agree bit for bit).  The workspace has prism_gated_scan_workspace_bytes (0 where
+ * no tile looks back: it may then be NULL). */
 PRISM_API size_t prism_gated_scan_workspace_bytes(const prism_gated_dims* dims);
 PRISM_API int prism_gated_scan_forward(const prism_gated_dims* dims, const void* x, const void* forget,
                                        const void* input_gate, const float* initial_state, void* out,
@@ -112,15 +112,18 @@ PRISM_API int prism_gated_scan_decode_step(const prism_gated_dims* dims, const v
                                            const void* input_gate, float* state, int n_states,
                                            const int32_t* slots, void* out, void* stream);
 
-/* Failure detection: every wait, a tile's for the state before it and a kernel's for its own copies, is
- * bounded (about a second); one that gives up sets the library's word for the current device, which
- * stays set until it is cleared, and the call's outputs are then undefined.  Synchronises the device and returns the word in *word (0: no
+/* Failure detection: a tile's look back for the state before it, and a kernel's waits for its own copies, are
+ * bounded (about a second); one that gives up sets the library's word for the current device, which stays
+ * set until it is cleared, and the call's outputs are then undefined.  (Where the tiles of a sequence are the
+ * CTAs of a cluster, they meet at its barrier, which has no limit of its own: the CTAs of a cluster run at the same time, and
+ * each gets there behind bounded waits alone.)  Synchronises the device and returns the word in *word (0: no
  * wait gave up), clearing it when `clear` is nonzero.  PRISM_ERR_INVALID_ARG for a NULL word,
  * PRISM_ERR_CUDA when the synchronisation or the copy fails.
  *
- * PRISM_FLAG_CHECK_WAIT_TIMEOUT in dims->flags is a diagnostic of this path (refused by
- * prism_gated_scan_decode_step): every tile that has to wait first waits, for a millisecond, for what
- * never comes, and gives up.  The word is set; the outputs are then computed as without the flag. */
+ * PRISM_FLAG_CHECK_WAIT_TIMEOUT in dims->flags is a diagnostic of the look back (refused by
+ * prism_gated_scan_decode_step): every tile that looks back first waits, for a millisecond, for what
+ * never comes, and gives up.  The word is set; the outputs are then computed as without the flag.  Where no
+ * tile looks back (a call that needs no workspace, sequences of one tile) the flag does nothing. */
 PRISM_API int prism_gated_status(int* word, int clear);
 
 #ifdef __cplusplus
