@@ -22,8 +22,8 @@ cudaError_t launch_tiles(F* fn, GatedArgs a, GatedPlan plan, std::atomic<unsigne
   a.strips = (a.D + CW - 1) / CW;
   const long long chains = (long long)a.B * a.strips, most = kSMs * C / a.tiles > 0 ? kSMs * C / a.tiles : 1;
   const long long tiles = chains * a.tiles, grid = CL ? (chains < most ? chains : most) * a.tiles : tiles < kSMs * C ? tiles : kSMs * C;
-  // Where 16 tiles of a chain run at once, look_near finds only runs (gradient, 1 x 55647 x 328: 91 us, 103 with
-  // it; 1 x 10807 x 2368, 8 tiles: 74 and 69).
+  // Where 16 tiles of a chain run at once, look_near finds only runs (gradient, 1 x 55647 x 328: 83 us, 89 with
+  // it; fewer at once, 1 x 10807 x 2368: 80 us with it, 88 without).
   a.deep = grid >= 16 * chains;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
